@@ -40,6 +40,11 @@ RSSM_DEV_OK, RSSM_DEV_ACCEPTED_RANGE, RSSM_DEV_COUNT_RANGE, RSSM_DEV_TIMEOUT = 0
 
 READ_FMT = {"none": RSSM_READ_NONE, "fp8": RSSM_READ_FP8, "nvfp4": RSSM_READ_NVFP4}
 DTYPE = {"f32": RSSM_F32, "bf16": RSSM_BF16}
+RSSM_DEV_PAGES_EMPTY, RSSM_DEV_PAGES_ROW, RSSM_DEV_PAGES_COUNT, RSSM_DEV_PAGES_SLOTS, RSSM_DEV_ATTN_LEN, \
+    RSSM_DEV_ATTN_PAGE, RSSM_DEV_ATTN_SLOT = range(16, 23)
+RSSM_KV_FP8 = 4
+RSSM_GATE_SILU, RSSM_GATE_SIGMOID = 1, 2
+GATE = {"silu": RSSM_GATE_SILU, "sigmoid": RSSM_GATE_SIGMOID}
 
 
 class RssmError(RuntimeError):
@@ -67,6 +72,41 @@ _LAYOUT_REGIONS = ("ckpt", "counts", "err", "buf_x", "buf_b", "buf_dt", "buf_k",
 class Layout(ctypes.Structure):
     _fields_ = ([(f, ctypes.c_size_t) for r in _LAYOUT_REGIONS for f in (r, r + "_bytes")]
                 + [("total_bytes", ctypes.c_size_t), ("capacity", ctypes.c_int32)])
+
+
+def _i32(*names):
+    return [(n, ctypes.c_int32) for n in names]
+
+
+def _i64(*names):
+    return [(n, ctypes.c_int64) for n in names]
+
+
+def _f32(*names):
+    return [(n, ctypes.c_float) for n in names]
+
+
+class PagesConfig(ctypes.Structure):
+    _fields_ = _i32("batch", "page_size", "num_pages", "max_pages")
+
+
+class PagesLayout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("lens", "table", "free", "free_count", "err", "total_bytes")]
+
+
+class AttnConfig(ctypes.Structure):
+    _fields_ = (_i32("batch", "q_heads", "kv_heads", "head_dim", "page_size", "num_pages", "max_pages", "max_draft",
+                     "in_dtype", "kv_dtype", "window") + _f32("scale") + _i64("page_stride"))
+
+
+class AddNormConfig(ctypes.Structure):
+    _fields_ = (_i64("rows") + _i32("dim", "res_dtype", "dtype") + _f32("eps", "scale", "w_offset")
+                + _i64("u_stride", "x_stride", "gate_stride", "u_out_stride", "n_out_stride"))
+
+
+class GatedNormConfig(ctypes.Structure):
+    _fields_ = (_i64("rows") + _i32("dim", "group", "w_dim", "dtype", "norm_first", "act") + _f32("eps", "w_offset")
+                + _i64("y_stride", "z_stride", "out_stride"))
 
 
 # --------------------------------------------------------------------------
@@ -154,6 +194,21 @@ def load():
             "rssm_sync_counts": ([p, p], i32),
             "rssm_count_summary": ([p, ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)], i32),
             "rssm_destroy": ([p], i32),
+            "rssm_pages_layout_for": ([ctypes.POINTER(PagesConfig), ctypes.POINTER(PagesLayout)], i32),
+            "rssm_pages_create": ([ctypes.POINTER(PagesConfig), p, sz, p, p, ctypes.POINTER(p)], i32),
+            "rssm_pages_extend": ([p, i32, p, p, p, i32, p], i32),
+            "rssm_pages_rollback": ([p, i32, p, p], i32),
+            "rssm_pages_truncate": ([p, p, p], i32),
+            "rssm_pages_get_error": ([p, ctypes.POINTER(i32), p], i32),
+            "rssm_pages_destroy": ([p], i32),
+            "rssm_attn_workspace_size": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(sz)], i32),
+            "rssm_attn_create": ([ctypes.POINTER(AttnConfig), p, p, p, p, p, sz, p, ctypes.POINTER(p)], i32),
+            "rssm_attn_append": ([p, i32, p, i64, p, i64, p, p], i32),
+            "rssm_attn_decode": ([p, i32, p, i64, p, p, p, p, p], i32),
+            "rssm_attn_get_error": ([p, ctypes.POINTER(i32), p], i32),
+            "rssm_attn_destroy": ([p], i32),
+            "rssm_add_norm": ([ctypes.POINTER(AddNormConfig), p, p, p, p, p, p, p, p], i32),
+            "rssm_gated_norm": ([ctypes.POINTER(GatedNormConfig), p, p, p, p, p], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -293,6 +348,87 @@ def rssm_destroy(handle: int) -> None:
     _check("rssm_destroy", load().rssm_destroy(handle))
 
 
+def rssm_pages_layout_for(cfg: PagesConfig) -> PagesLayout:
+    lay = PagesLayout()
+    _check("rssm_pages_layout_for", load().rssm_pages_layout_for(ctypes.byref(cfg), ctypes.byref(lay)))
+    return lay
+
+
+def rssm_pages_create(cfg: PagesConfig, workspace, workspace_bytes: int, free0=None, stream=None) -> int:
+    h = ctypes.c_void_p(0)
+    _check("rssm_pages_create", load().rssm_pages_create(ctypes.byref(cfg), _addr(workspace), workspace_bytes,
+                                                         _addr(free0), _stream(stream), ctypes.byref(h)))
+    return h.value
+
+
+def rssm_pages_extend(handle: int, T: int, new, slots, positions, max_tokens: int, stream=None) -> None:
+    _check("rssm_pages_extend", load().rssm_pages_extend(handle, T, _addr(new), _addr(slots), _addr(positions),
+                                                         max_tokens, _stream(stream)))
+
+
+def rssm_pages_rollback(handle: int, T: int, accepted, stream=None) -> None:
+    _check("rssm_pages_rollback", load().rssm_pages_rollback(handle, T, _addr(accepted), _stream(stream)))
+
+
+def rssm_pages_truncate(handle: int, keep, stream=None) -> None:
+    _check("rssm_pages_truncate", load().rssm_pages_truncate(handle, _addr(keep), _stream(stream)))
+
+
+def rssm_pages_get_error(handle: int, stream=None) -> tuple:
+    err = (ctypes.c_int32 * 4)()
+    _check("rssm_pages_get_error", load().rssm_pages_get_error(handle, err, _stream(stream)))
+    return tuple(err)
+
+
+def rssm_pages_destroy(handle: int) -> None:
+    _check("rssm_pages_destroy", load().rssm_pages_destroy(handle))
+
+
+def rssm_attn_workspace_size(cfg: AttnConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check("rssm_attn_workspace_size", load().rssm_attn_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def rssm_attn_create(cfg: AttnConfig, k_cache, v_cache, k_scale, v_scale, workspace, workspace_bytes: int,
+                     stream=None) -> int:
+    h = ctypes.c_void_p(0)
+    _check("rssm_attn_create", load().rssm_attn_create(ctypes.byref(cfg), _addr(k_cache), _addr(v_cache),
+                                                       _addr(k_scale), _addr(v_scale), _addr(workspace),
+                                                       workspace_bytes, _stream(stream), ctypes.byref(h)))
+    return h.value
+
+
+def rssm_attn_append(handle: int, tokens: int, k, k_stride: int, v, v_stride: int, slots, stream=None) -> None:
+    _check("rssm_attn_append", load().rssm_attn_append(handle, tokens, _addr(k), k_stride, _addr(v), v_stride,
+                                                       _addr(slots), _stream(stream)))
+
+
+def rssm_attn_decode(handle: int, T: int, q, q_stride: int, lens, table, out, lse=None, stream=None) -> None:
+    _check("rssm_attn_decode", load().rssm_attn_decode(handle, T, _addr(q), q_stride, _addr(lens), _addr(table),
+                                                       _addr(out), _addr(lse), _stream(stream)))
+
+
+def rssm_attn_get_error(handle: int, stream=None) -> tuple:
+    err = (ctypes.c_int32 * 4)()
+    _check("rssm_attn_get_error", load().rssm_attn_get_error(handle, err, _stream(stream)))
+    return tuple(err)
+
+
+def rssm_attn_destroy(handle: int) -> None:
+    _check("rssm_attn_destroy", load().rssm_attn_destroy(handle))
+
+
+def rssm_add_norm(cfg: AddNormConfig, u, x, w_post, gate, w, u_out, n_out, stream=None) -> None:
+    _check("rssm_add_norm", load().rssm_add_norm(ctypes.byref(cfg), _addr(u), _addr(x), _addr(w_post), _addr(gate),
+                                                 _addr(w), _addr(u_out), _addr(n_out), _stream(stream)))
+
+
+def rssm_gated_norm(cfg: GatedNormConfig, y, z, w, out, stream=None) -> None:
+    _check("rssm_gated_norm", load().rssm_gated_norm(ctypes.byref(cfg), _addr(y), _addr(z), _addr(w), _addr(out),
+                                                     _stream(stream)))
+
+
 # --------------------------------------------------------------------------
 # convenience: a layer owning its workspace tensor
 # --------------------------------------------------------------------------
@@ -383,3 +519,9 @@ class Layer:
     def counts(self):
         import torch
         return self.region("counts", torch.int32, (self.cfg.batch, self.cfg.heads))
+
+
+# --------------------------------------------------------------------------
+# convenience: the attention side on torch tensors (hybrid.py)
+# --------------------------------------------------------------------------
+from .hybrid import Attention, PageTable, add_norm, gated_norm  # noqa: E402

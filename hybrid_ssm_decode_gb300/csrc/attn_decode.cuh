@@ -1,0 +1,880 @@
+// Attention of T new tokens a request over a paged cache.
+//
+// The mathematics. The queries that read one cache head, T drafts times
+// q_heads/kv_heads, are the rows of one small matrix Q; the scores of a group of
+// 16 cached tokens are Q K^T, and the outputs a running sum. A softmax needs
+// one pass over the tokens: with m the running maximum of the scores (in units
+// of log2) and l, O the running sums,
+//   m' = max(m, max s);  l' = l 2^(m-m') + sum 2^(s-m');  O' = O 2^(m-m') + 2^(s-m') V
+// and parts (m, l, O) of one row made apart join by the same rule.
+//
+// The split. A cached token costs its bytes once and 4 D flops a row, so for up
+// to 64 rows the cache's bytes bound it, and the question is only that every SM
+// streams all the time, whatever the requests' lengths. The work of the launch is
+// laid out as one line of units (request, cache head, 64 tokens) and cut into
+// equal shares, one per block. A block's share may begin and end inside a
+// request; those at most two parts go to the workspace, and the last of a
+// request's blocks to arrive joins them in the order of the tokens (no float
+// atomics: reruns give the same bits).
+//
+// The block. One producer warp looks pages up and copies groups of 16 tokens (K
+// and V, one 5-D TMA box each, swizzled so that fragment loads meet no bank
+// twice) into a ring of slots; a box never leaves a page, because a page is a
+// multiple of 16 tokens. The consumer warps take groups in turn, each with its
+// own running (m, l, O) in registers, so that they meet only at the end of a
+// part. Groups whose tokens not all rows see (the request's end, the drafts, the
+// window's start) take a masked path: scores by selection, values of unseen
+// tokens replaced by zero bits, and where a value that some rows see and others do
+// not is not finite, the rows' products are made draft by draft.
+//
+// Matrix instructions. m16n8k16 on BF16 caches, with 2^(s-m) split into two
+// BF16 terms, so that the outputs carry only their own rounding; on FP8 caches the codes
+// widen exactly to FP16 (Q scaled per row by a power of two into FP16's range;
+// 2^(s-m) rounded to FP16's 11 bits), and on FP32 caches m16n8k8 on TF32 with both
+// operands split in two (three products; what is left out is below 2^-21).
+#pragma once
+
+#include "attn.h"
+
+namespace rssm {
+namespace attn {
+
+enum { kF32 = 0, kBF16 = 1, kFP8 = 2 };
+
+template <int KV, int D_, int WM_>
+struct Shape {
+    static constexpr int D = D_;
+    static constexpr int WM = WM_;                       // row groups of 16
+    // Consumer warps per row group. Registers are shared out per quarter of an
+    // SM: nine warps put three on one of them and leave 168 a thread, which
+    // heads of 256 do not fit (128 of them are the outputs); up to eight leave 255.
+    static constexpr int NT = D == 256 ? (WM == 1 ? 4 : WM == 2 ? 3 : 1) : WM == 4 ? 2 : 4;
+    static constexpr int kRows = 16 * WM;
+    static constexpr int kConsumers = WM * NT;
+    static constexpr int kThreads = (kConsumers + 1) * 32;
+    static constexpr int kEsz = KV == kF32 ? 4 : KV == kBF16 ? 2 : 1;
+    static constexpr int kQsz = KV == kF32 ? 4 : 2;
+    static constexpr int RB = D * kEsz;                  // bytes of a cached token
+    static constexpr int CB = RB < 128 ? RB : 128;       // swizzled row
+    static constexpr int CH = RB / CB;
+    static constexpr int kHalf = kAttnGroup * RB;        // K (or V) of a slot
+    static constexpr int kSlot = 2 * kHalf;
+    static constexpr int QS = D * kQsz + 16;             // bytes from one query row to the next
+    static constexpr int OS = D + 8;                     // floats from one merged row to the next
+    // Two blocks per SM where the registers allow it: one block's joins then
+    // overlap the other's stream.
+    static constexpr int kMinBlocks = (WM == 1 && D <= 128) ? 2 : 1;
+    static constexpr int kFixed = 2 * kRows * QS + kRows * OS * 4 + NT * kRows * 8 + kRows * 8 + 512;
+    static constexpr int kBudget = (kMinBlocks == 2 ? 113 : 226) * 1024 - 1024;
+    static constexpr int kSlotsFit = (kBudget - kFixed) / kSlot;
+    static constexpr int NS = kSlotsFit > 24 ? 24 : kSlotsFit;
+    static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
+    static_assert(NS >= NT, "ring too small");
+};
+
+// ---- instructions -----------------------------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two E4M3 codes -> two FP16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+    return h;
+}
+__device__ __forceinline__ uint32_t tf32(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+// x = hi + lo to 22 bits. A non-finite x stays in hi alone.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    hi = tf32(x);
+    const float d = x - __uint_as_float(hi);
+    lo = tf32(d == d ? d : 0.f);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int row, int head, int page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4,%5,%6}], [%7];"
+        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(0), "r"(head), "r"(page), "r"(smem_u32(bar)) : "memory");
+}
+
+// 2^n for n in [-126, 127].
+__device__ __forceinline__ float pow2(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
+
+// Wait for a phase, for at most kWaitLimitNs; false once any warp of the block
+// has given up (the block then only runs its loops out).
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*dead) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *dead = 1;
+            report_error(err, RSSM_DEV_TIMEOUT, -1, 0);
+            return false;
+        }
+    }
+    return true;
+}
+
+// ---- the share of a block ----------------------------------------------------
+// Tokens of a request that any draft sees, as groups [g0, g1), and its units.
+struct Span {
+    int len, g0, g1, units;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
+    Span s;
+    const int most = a.max_pages * a.page_size;
+    int len = __ldg(a.lens + b);
+    s.len = min(max(len, 0), most);
+    const int64_t start = a.window > 0 ? static_cast<int64_t>(s.len) - a.T - a.window + 1 : 0;
+    s.g0 = start > 0 ? static_cast<int>(start / kAttnGroup) : 0;
+    s.g1 = (s.len + kAttnGroup - 1) / kAttnGroup;
+    s.units = max(1, (s.g1 - s.g0 + kAttnUnit - 1) / kAttnUnit);   // an empty request still writes its zeros
+    return s;
+}
+
+// Walks the parts of a block's share. Every warp keeps its own copy.
+struct Cursor {
+    int64_t total, w, w1, base;   // units: in all, next, end, before request b
+    int grid, b;
+    Span sp;
+    // the current part
+    int pair, u0, u1;
+
+    __device__ __forceinline__ void start(const AttnArgs& a, int lane) {
+        const int heads = a.kv_heads * a.chunks;
+        const int per = (a.B + 31) / 32;
+        int64_t mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int r = lane * per + i;
+            if (r < a.B) mine += span_of(a, r).units;
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t n = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += n;
+        }
+        total = __shfl_sync(0xffffffffu, incl, 31) * heads;
+        grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+        const int c = blockIdx.x;
+        if (c >= grid) {
+            w = w1 = 0;
+            return;
+        }
+        w = total * c / grid;
+        w1 = total * (c + 1) / grid;
+        // the lane whose requests hold unit w, then the request
+        const int64_t excl = (incl - mine) * heads;
+        const unsigned has = __ballot_sync(0xffffffffu, mine > 0 && excl <= w);
+        const int src = 31 - __clz(has);
+        int rb = lane * per;
+        int64_t at = excl;
+        if (lane == src) {
+            for (;;) {
+                const int64_t n = static_cast<int64_t>(span_of(a, rb).units) * heads;
+                if (at + n > w) break;
+                at += n;
+                ++rb;
+            }
+        }
+        b = __shfl_sync(0xffffffffu, rb, src);
+        base = __shfl_sync(0xffffffffu, at, src);
+        sp = span_of(a, b);
+    }
+    // The next part of the share; false at its end.
+    __device__ __forceinline__ bool next(const AttnArgs& a) {
+        if (w >= w1) return false;
+        const int heads = a.kv_heads * a.chunks;
+        if (w - base >= static_cast<int64_t>(sp.units) * heads) {
+            base += static_cast<int64_t>(sp.units) * heads;
+            sp = span_of(a, ++b);
+        }
+        const int64_t r = w - base;
+        pair = static_cast<int>(r / sp.units);
+        u0 = static_cast<int>(r - static_cast<int64_t>(pair) * sp.units);
+        u1 = static_cast<int>(min(static_cast<int64_t>(sp.units), u0 + (w1 - w)));
+        w += u1 - u0;
+        return true;
+    }
+    __device__ __forceinline__ int first_group() const { return sp.g0 + u0 * kAttnUnit; }
+    __device__ __forceinline__ int end_group() const { return min(sp.g1, sp.g0 + u1 * kAttnUnit); }
+    // The block whose share holds unit x of the launch.
+    __device__ __forceinline__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * grid - 1) / total); }
+};
+
+// ---- one warp's products -----------------------------------------------------
+// The byte of a slot's K or V at (token r, 16-byte chunk c) under the TMA swizzle.
+template <class S>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+    if (S::CB == 128) return (c >> 3) * (kAttnGroup * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    return r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4);
+}
+
+template <int KV, class S>
+struct Warp {
+    static constexpr int D = S::D;
+    static constexpr int kQRegs = KV == kF32 ? 1 : D / 16;
+    static constexpr int kTiles = D / 8;
+    float o[kTiles][4];
+    float m[2], l[2];            // rows lane/4 and lane/4 + 8; l is this lane's columns only
+    uint32_t qf[kQRegs][4];
+    const float* qs;             // FP32: the query rows in shared memory
+    float mul[2];                // score multiplier of the two rows
+    int lane, g, c;
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+
+    // Query rows (16 of them, QS bytes apart) as the A operand.
+    __device__ __forceinline__ void load_q(const char* rows, float scale_log2, float kscale) {
+        mul[0] = mul[1] = scale_log2;
+        if constexpr (KV == kF32) {
+            qs = reinterpret_cast<const float*>(rows);
+        } else if constexpr (KV == kBF16) {
+            const uint32_t at = smem_u32(rows) + (lane & 15) * S::QS + (lane >> 4) * 16;
+#pragma unroll
+            for (int k = 0; k < kQRegs; ++k) ldsm4(qf[k], at + k * 32);
+        } else {
+            // columns permuted within 16 so that a lane's four K codes are its
+            // own; each row scaled by a power of two so that its largest value
+            // lies in [2^14, 2^15)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const char* row = rows + (g + 8 * h) * S::QS;
+                float mx = 0.f;
+#pragma unroll
+                for (int k = 0; k < kQRegs; ++k) {
+                    const float4 v = load4(reinterpret_cast<const __nv_bfloat16*>(row + k * 32 + c * 8));
+                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // e with mx in [2^e, 2^(e+1)); zero, subnormal and non-finite rows stay as they are
+                int e = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFF) - 127;
+                if (e > 127 || e < -126) e = 14;
+                const int up = 14 - e, half = up / 2;        // 2^up may pass FP32: two factors
+                const float f1 = pow2(half), f2 = pow2(up - half);
+                mul[h] = scale_log2 * kscale * pow2(-half) * pow2(half - up);
+#pragma unroll
+                for (int k = 0; k < kQRegs; ++k) {
+                    const float4 v = load4(reinterpret_cast<const __nv_bfloat16*>(row + k * 32 + c * 8));
+                    qf[k][h] = pack_f16(v.x * f1 * f2, v.y * f1 * f2);
+                    qf[k][2 + h] = pack_f16(v.z * f1 * f2, v.w * f1 * f2);
+                }
+            }
+        }
+    }
+
+    // Scores of 16 tokens: s[i][..] holds tokens 8 i + 2 c, +1 of rows g and g + 8.
+    __device__ __forceinline__ void scores(uint32_t k, float (&s)[2][4]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+        uint32_t b[4];
+        if constexpr (KV == kBF16) {
+            const int r = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+#pragma unroll
+            for (int i = 0; i < kQRegs; ++i) {
+                ldsm4(b, k + swz<S>(r, 2 * i + ch));
+                mma_bf16(s[0], qf[i], b[0], b[1]);
+                mma_bf16(s[1], qf[i], b[2], b[3]);
+            }
+        } else if constexpr (KV == kFP8) {
+            const int r = lane & 15, ch = lane >> 4;         // tokens 0-7, 8-15 of one chunk, then of the next
+#pragma unroll
+            for (int i = 0; i < kQRegs; i += 2) {
+                ldsm4(b, k + swz<S>(r, i + ch));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    mma_f16(s[0], qf[i + j], e4m3x2_to_h2(b[2 * j]), e4m3x2_to_h2(b[2 * j] >> 16));
+                    mma_f16(s[1], qf[i + j], e4m3x2_to_h2(b[2 * j + 1]), e4m3x2_to_h2(b[2 * j + 1] >> 16));
+                }
+            }
+        } else {
+            const int r = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                uint32_t ah[4], al[4], bh[4], bl[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    split_tf32(qs[(g + 8 * (j & 1)) * (S::QS / 4) + i * 8 + c + 4 * (j >> 1)], ah[j], al[j]);
+                ldsm4(b, k + swz<S>(r, 2 * i + ch));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) split_tf32(__uint_as_float(b[j]), bh[j], bl[j]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    mma_tf32(s[j], al, bh[2 * j], bh[2 * j + 1]);
+                    mma_tf32(s[j], ah, bl[2 * j], bl[2 * j + 1]);
+                    mma_tf32(s[j], ah, bh[2 * j], bh[2 * j + 1]);
+                }
+            }
+        }
+    }
+
+    // The weights as the A operand: P[x][..] of the tokens' two halves (TF32: of
+    // 8 tokens each) or of all 16, with the part that the first rounding left.
+    struct Weights {
+        uint32_t hi[KV == kF32 ? 2 : 1][4];
+        uint32_t lo[KV == kF32 ? 2 : 1][4];
+    };
+    __device__ __forceinline__ Weights weights(const float (&p)[2][4]) const {
+        Weights w;
+        if constexpr (KV == kF32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float v[4] = {p[i][0], p[i][2], p[i][1], p[i][3]};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) split_tf32(v[j], w.hi[i][j], w.lo[i][j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = p[j >> 1][2 * (j & 1)], y = p[j >> 1][2 * (j & 1) + 1];
+                if constexpr (KV == kBF16) {
+                    w.hi[0][j] = pack_bf16(x, y);
+                    w.lo[0][j] = pack_bf16(x - __uint_as_float(w.hi[0][j] << 16),
+                                           y - __uint_as_float(w.hi[0][j] & 0xFFFF0000u));
+                } else {
+                    w.hi[0][j] = pack_f16(x, y);
+                    w.lo[0][j] = 0;
+                }
+            }
+        }
+        return w;
+    }
+
+    // B fragments of V for output tiles 2 i and 2 i + 1: v[0..1] and v[2..3], as
+    // stored (BF16, widened FP8) or FP32 bits; FP32 for the 8 tokens of half h.
+    __device__ __forceinline__ void values(uint32_t vb, int i, int h, uint32_t (&v)[4]) const {
+        if constexpr (KV == kBF16) {
+            ldsm4t(v, vb + swz<S>(lane & 15, 2 * i + (lane >> 4)));
+        }
+        if constexpr (KV == kF32) {
+            const int d0 = i * 16 + g, r0 = h * 8 + 2 * c;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int d = d0 + 8 * (j >> 1), r = r0 + (j & 1);
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[j]) : "r"(vb + swz<S>(r, d >> 2) + (d & 3) * 4));
+            }
+        }
+    }
+    // FP8: one load covers 32 columns (two pairs of tiles); tile 2 i holds the
+    // even columns of chunk i, tile 2 i + 1 the odd ones.
+    __device__ __forceinline__ void values_fp8(uint32_t vb, int i, uint32_t (&v)[2][4]) const {
+        uint32_t r[4];
+        ldsm4t(r, vb + swz<S>(lane & 15, i + (lane >> 4)));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {                     // tokens 0-7, 8-15
+                const uint32_t x = e4m3x2_to_h2(r[2 * j + k]), y = e4m3x2_to_h2(r[2 * j + k] >> 16);
+                v[j][k] = __byte_perm(x, y, 0x5410);
+                v[j][2 + k] = __byte_perm(x, y, 0x7632);
+            }
+    }
+
+    __device__ __forceinline__ void product(float (&acc)[4], const Weights& w, int h, uint32_t b0, uint32_t b1) const {
+        if constexpr (KV == kBF16) {
+            mma_bf16(acc, w.hi[0], b0, b1);
+            mma_bf16(acc, w.lo[0], b0, b1);
+        } else if constexpr (KV == kFP8) {
+            mma_f16(acc, w.hi[0], b0, b1);
+        } else {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(__uint_as_float(b0), h0, l0);
+            split_tf32(__uint_as_float(b1), h1, l1);
+            mma_tf32(acc, w.lo[h], h0, h1);
+            mma_tf32(acc, w.hi[h], l0, l1);
+            mma_tf32(acc, w.hi[h], h0, h1);
+        }
+    }
+
+    // Every (tile, half) fragment of V through f(tile, half, b0, b1); half is 0
+    // but for FP32, where 0 and 1 are tokens 0-7 and 8-15.
+    template <class F>
+    __device__ __forceinline__ void each_value(uint32_t vb, F f) const {
+        if constexpr (KV == kFP8) {
+#pragma unroll
+            for (int i = 0; i < D / 16; i += 2) {
+                uint32_t v[2][4];
+                values_fp8(vb, i, v);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    f(2 * (i + j), 0, v[j][0], v[j][1]);
+                    f(2 * (i + j) + 1, 0, v[j][2], v[j][3]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTiles / 2; ++i)
+#pragma unroll
+                for (int h = 0; h < (KV == kF32 ? 2 : 1); ++h) {
+                    uint32_t v[4];
+                    values(vb, i, h, v);
+                    f(2 * i, h, v[0], v[1]);
+                    f(2 * i + 1, h, v[2], v[3]);
+                }
+        }
+    }
+
+    // A fragment with the tokens outside [lo, hi] (of the group: 0..15) set to zero bits.
+    __device__ __forceinline__ uint32_t cut(uint32_t v, int half, int which, int lo, int hi) const {
+        if constexpr (KV == kF32) {
+            const int t = half * 8 + 2 * c + which;
+            return (t >= lo && t <= hi) ? v : 0u;
+        } else {
+            const int t = which * 8 + 2 * c;
+            return v & ((t >= lo && t <= hi ? 0x0000FFFFu : 0u) | (t + 1 >= lo && t + 1 <= hi ? 0xFFFF0000u : 0u));
+        }
+    }
+    __device__ __forceinline__ bool not_finite(uint32_t v) const {
+        if constexpr (KV == kF32) return (v & 0x7F800000u) == 0x7F800000u;
+        const uint32_t e = KV == kBF16 ? 0x7F807F80u : 0x7C007C00u, one = KV == kBF16 ? 0x00800080u : 0x04000400u;
+        return (((v & e) + one) & 0x80008000u) != 0;
+    }
+
+    // Running maximum, sum and outputs over one group. Rows g and g + 8 see the
+    // tokens lo[x]..hi[x] of it (0..15); with kMasked false, all rows see all.
+    // any_lo..any_hi: the tokens that some row of the block sees. first[t]..: see below.
+    template <bool kMasked>
+    __device__ __forceinline__ void step(uint32_t kb, uint32_t vb, const int (&lo)[2], const int (&hi)[2], int any_lo,
+                                         int any_hi, int T, int tok0, int len, int window, const int (&draft)[2]) {
+        float s[2][4];
+        scores(kb, s);
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int x = j >> 1;
+                s[i][j] *= mul[x];
+                if (kMasked) {
+                    const int t = 8 * i + 2 * c + (j & 1);
+                    if (t < lo[x] || t > hi[x]) s[i][j] = -INFINITY;
+                }
+                mx[x] = fmaxf(mx[x], s[i][j]);
+            }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+            mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+            mx[x] = fmaxf(mx[x], m[x]);
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+            float f[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                f[x] = ex2(m[x] - (mx[x] == -INFINITY ? 0.f : mx[x]));
+                m[x] = mx[x];
+                l[x] *= f[x];
+            }
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                o[i][0] *= f[0];
+                o[i][1] *= f[0];
+                o[i][2] *= f[1];
+                o[i][3] *= f[1];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float ref = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float& p = s[i][2 * x + j];
+                    p = ex2(p - ref);
+                    l[x] += p;
+                }
+        }
+        const Weights w = weights(s);
+        if (!kMasked) {
+            each_value(vb, [&](int t, int h, uint32_t b0, uint32_t b1) { product(o[t], w, h, b0, b1); });
+            return;
+        }
+        bool bad = false;
+        if (T > 1) {
+            each_value(vb, [&](int, int h, uint32_t b0, uint32_t b1) {
+                bad = bad || not_finite(cut(b0, h, 0, any_lo, any_hi)) || not_finite(cut(b1, h, 1, any_lo, any_hi));
+            });
+            bad = __any_sync(0xffffffffu, bad);
+        }
+        if (!bad) {
+            each_value(vb, [&](int t, int h, uint32_t b0, uint32_t b1) {
+                product(o[t], w, h, cut(b0, h, 0, any_lo, any_hi), cut(b1, h, 1, any_lo, any_hi));
+            });
+            return;
+        }
+        // 0 * infinity must not reach a row that does not see the token: draft
+        // by draft, with only that draft's tokens in place, into its rows alone
+        for (int t = 0; t < T; ++t) {
+            const int p = len - T + t;
+            const int a0 = window > 0 ? max(0, p - window + 1) - tok0 : 0, a1 = p - tok0;
+            each_value(vb, [&](int tile, int h, uint32_t b0, uint32_t b1) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                product(acc, w, h, cut(b0, h, 0, a0, a1), cut(b1, h, 1, a0, a1));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (draft[j >> 1] == t) o[tile][j] += acc[j];
+            });
+        }
+    }
+
+    // Column of o[tile][j] (0, 1: of row g; 2, 3: of row g + 8).
+    __device__ __forceinline__ int column(int tile, int j) const {
+        if constexpr (KV == kFP8) return (tile >> 1) * 16 + 4 * c + 2 * j + (tile & 1);
+        return tile * 8 + 2 * c + j;
+    }
+};
+
+// ---- the kernel --------------------------------------------------------------
+template <int KV, class S>
+__global__ void __launch_bounds__(S::kThreads, S::kMinBlocks)
+attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    constexpr int D = S::D, NS = S::NS;
+    extern __shared__ char smem_raw[];
+    char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    char* slots = smem;
+    char* qbuf = slots + NS * S::kSlot;                                  // [2][kRows][QS]
+    float* merged = reinterpret_cast<float*>(qbuf + 2 * S::kRows * S::QS);   // [kRows][OS]
+    float2* s_ml = reinterpret_cast<float2*>(merged + S::kRows * S::OS); // [NT][kRows]
+    float2* s_row = s_ml + S::NT * S::kRows;                             // [kRows]
+    uint64_t* full = reinterpret_cast<uint64_t*>(s_row + S::kRows);      // [NS]
+    uint64_t* empty = full + NS;
+    uint64_t* qfull = empty + NS;                                        // [2]
+    uint64_t* qempty = qfull + 2;
+    volatile int* dead = reinterpret_cast<volatile int*>(qempty + 2);
+    volatile int* s_last = dead + 1;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, S::WM);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull + i, 1);
+            mbar_init(qempty + i, S::kConsumers);
+        }
+        *dead = 0;
+        fence_mbar_init();
+    }
+    Cursor cur;
+    cur.start(a, lane);
+    __syncthreads();
+
+    const int rows_all = a.T * a.group;
+    int64_t gi = 0;            // groups of the share so far, in order
+    int parts = 0;
+
+    if (warp == S::kConsumers) {
+        // ---- producer ----
+        const uint32_t q_bytes = D * S::kQsz;
+        while (cur.next(a)) {
+            const int head = cur.pair / a.chunks, row0 = (cur.pair % a.chunks) * S::kRows;
+            const int rows = min(S::kRows, rows_all - row0);
+            const int pq = parts & 1;
+            bool ok = true;
+            if (parts >= 2) ok = wait_phase(qempty + pq, ((parts >> 1) - 1) & 1, dead, a.err);
+            if (ok && !*dead) {
+                if (lane == 0) mbar_arrive_expect_tx(qfull + pq, rows * q_bytes);
+                __syncwarp();
+                for (int r = lane; r < rows; r += 32) {
+                    const int t = (row0 + r) / a.group, j = (row0 + r) % a.group;
+                    const char* src = static_cast<const char*>(a.q) +
+                                      ((static_cast<int64_t>(cur.b) * a.T + t) * a.q_stride +
+                                       static_cast<int64_t>(head * a.group + j) * D) * S::kQsz;
+                    bulk_g2s(qbuf + (pq * S::kRows + r) * S::QS, src, q_bytes, qfull + pq);
+                }
+            }
+            ++parts;
+            const int g0 = cur.first_group(), g1 = cur.end_group();
+            for (int base = g0; base < g1; base += 32) {
+                int page = 0, row = 0;
+                if (base + lane < g1) {
+                    const int tok = (base + lane) * kAttnGroup;
+                    const int at = tok / a.page_size;
+                    row = tok - at * a.page_size;
+                    page = __ldg(a.table + static_cast<int64_t>(cur.b) * a.max_pages + at);
+                    if (page < 0 || page >= a.num_pages) {
+                        report_error(a.err, RSSM_DEV_ATTN_PAGE, cur.b, page);
+                        page = a.num_pages;              // outside the map: read as zeros
+                    }
+                }
+                const int n = min(32, g1 - base);
+                for (int i = 0; i < n; ++i, ++gi) {
+                    if (lane == i) {
+                        const int s = static_cast<int>(gi % NS);
+                        const int64_t turn = gi / NS;
+                        if ((turn == 0 || wait_phase(empty + s, (turn - 1) & 1, dead, a.err)) && !*dead) {
+                            const uint32_t dst = smem_u32(slots + s * S::kSlot);
+                            mbar_arrive_expect_tx(full + s, S::kSlot);
+                            tma_load_5d(dst, &kmap, row, head, page, full + s);
+                            tma_load_5d(dst + S::kHalf, &vmap, row, head, page, full + s);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (*dead && lane == 0) {
+            // let the copies in flight land before the block's memory goes
+            for (int64_t i = max(static_cast<int64_t>(0), gi - NS); i < gi; ++i)
+                mbar_wait_bounded(full + i % NS, (i / NS) & 1, kWaitLimitNs / 16);
+            for (int i = max(0, parts - 2); i < parts; ++i)
+                mbar_wait_bounded(qfull + (i & 1), (i >> 1) & 1, kWaitLimitNs / 16);
+        }
+        return;
+    }
+
+    // ---- consumers ----
+    constexpr int kThreads = S::kConsumers * 32;
+    const int wm = warp / S::NT, wt = warp % S::NT;
+    Warp<KV, S> wp;
+    wp.lane = lane;
+    wp.g = lane >> 2;
+    wp.c = lane & 3;
+    while (cur.next(a)) {
+        const int head = cur.pair / a.chunks, row0 = (cur.pair % a.chunks) * S::kRows;
+        const int rows = min(S::kRows, rows_all - row0);
+        const int b = cur.b, len = cur.sp.len;
+        if (cur.u0 == 0 && cur.pair == 0 && tid == 0) {
+            const int given = __ldg(a.lens + b);
+            if (given != len) report_error(a.err, RSSM_DEV_ATTN_LEN, b, given);
+        }
+        // what the warp's two rows see: [see_lo, see_hi]
+        int draft[2], see_lo[2], see_hi[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = min(row0 + wm * 16 + wp.g + 8 * x, rows_all - 1);
+            draft[x] = r / a.group;
+            see_hi[x] = len - a.T + draft[x];
+            see_lo[x] = a.window > 0 ? max(0, see_hi[x] - a.window + 1) : 0;
+        }
+        const int all_hi = len - a.T;                             // the last token that all drafts see
+        const int all_lo = a.window > 0 ? max(0, len - a.window) : 0;   // and the first
+        const int some_lo = a.window > 0 ? max(0, len - a.T - a.window + 1) : 0;
+        const int pq = parts & 1;
+        wp.reset();
+        bool ok = wait_phase(qfull + pq, (parts >> 1) & 1, dead, a.err);
+        if (ok) wp.load_q(qbuf + (pq * S::kRows + wm * 16) * S::QS, a.scale_log2, KV == kFP8 ? __ldg(a.k_scale + head) : 1.f);
+        if (KV != kF32) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qempty + pq);
+        }
+        const int g0 = cur.first_group(), g1 = cur.end_group();
+        // this warp's groups: those whose running index is wt modulo NT
+        int64_t i = gi + ((wt - gi) % S::NT + S::NT) % S::NT;
+        for (; i < gi + (g1 - g0); i += S::NT) {
+            const int s = static_cast<int>(i % NS);
+            ok = wait_phase(full + s, (i / NS) & 1, dead, a.err);
+            const int tok = (g0 + static_cast<int>(i - gi)) * kAttnGroup;
+            const uint32_t kb = smem_u32(slots + s * S::kSlot), vb = kb + S::kHalf;
+            if (ok) {
+                const int lo[2] = {see_lo[0] - tok, see_lo[1] - tok}, hi[2] = {see_hi[0] - tok, see_hi[1] - tok};
+                if (tok >= all_lo && tok + kAttnGroup - 1 <= all_hi)
+                    wp.template step<false>(kb, vb, lo, hi, 0, 0, a.T, tok, len, a.window, draft);
+                else
+                    wp.template step<true>(kb, vb, lo, hi, some_lo - tok, len - 1 - tok, a.T, tok, len, a.window, draft);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + s);
+        }
+        gi += g1 - g0;
+        if (KV == kF32) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qempty + pq);
+        }
+        ++parts;
+
+        // ---- join the warps of each row ----
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            wp.l[x] += __shfl_xor_sync(0xffffffffu, wp.l[x], 1);
+            wp.l[x] += __shfl_xor_sync(0xffffffffu, wp.l[x], 2);
+            if (wp.c == 0) s_ml[wt * S::kRows + wm * 16 + wp.g + 8 * x] = make_float2(wp.m[x], wp.l[x]);
+        }
+        named_sync(1, kThreads);
+        float f[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = wm * 16 + wp.g + 8 * x;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < S::NT; ++w) M = fmaxf(M, s_ml[w * S::kRows + r].x);
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < S::NT; ++w) L += s_ml[w * S::kRows + r].y * ex2(s_ml[w * S::kRows + r].x - ref);
+            f[x] = ex2(wp.m[x] - ref);
+            if (wt == 0 && wp.c == 0) s_row[r] = make_float2(M, L);
+        }
+        for (int w = 0; w < S::NT; ++w) {
+            if (w == wt) {
+#pragma unroll
+                for (int i2 = 0; i2 < Warp<KV, S>::kTiles; ++i2)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float* d = merged + (wm * 16 + wp.g + 8 * (j >> 1)) * S::OS + wp.column(i2, j & 1);
+                        const float v = wp.o[i2][j] * f[j >> 1];
+                        *d = w == 0 ? v : *d + v;
+                    }
+            }
+            named_sync(1, kThreads);
+        }
+        const bool whole = cur.u0 == 0 && cur.u1 == cur.sp.units;
+        const float vscale = KV == kFP8 ? __ldg(a.v_scale + head) : 1.f;
+        const auto put = [&](int r, int col, float4 v, float M, float L) {
+            const int t = (row0 + r) / a.group, j = (row0 + r) % a.group;
+            const int64_t at = (static_cast<int64_t>(b) * a.T + t) * a.q_heads + head * a.group + j;
+            const float inv = L == 0.f ? 0.f : vscale / L;
+            v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+            if (KV == kF32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + col) = v;
+            } else {
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * D + col) =
+                    make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+            }
+            if (a.lse != nullptr && col == 0)
+                a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        };
+        if (whole) {
+            for (int x = tid; x < rows * (D / 4); x += kThreads) {
+                const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+                put(r, col, *reinterpret_cast<const float4*>(merged + r * S::OS + col), s_row[r].x, s_row[r].y);
+            }
+            continue;
+        }
+        // a part: to the workspace; the last block of the request's to arrive joins
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (cur.u0 == 0 ? 1 : 0);
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+            __stcg(reinterpret_cast<float4*>(a.part_o + (slot * S::kRows + r) * D + col),
+                   *reinterpret_cast<const float4*>(merged + r * S::OS + col));
+            if (col == 0) __stcg(a.part_ml + slot * S::kRows + r, s_row[r]);
+        }
+        __threadfence();
+        named_sync(1, kThreads);
+        const int64_t first = cur.base + static_cast<int64_t>(cur.pair) * cur.sp.units;
+        const int c0 = cur.owner(first), c1 = cur.owner(first + cur.sp.units - 1);
+        if (tid == 0) {
+            uint32_t* n = a.arrived + static_cast<int64_t>(b) * a.kv_heads * a.chunks + cur.pair;
+            const bool last = atomicAdd(n, 1u) == static_cast<uint32_t>(c1 - c0);
+            if (last) *n = 0;
+            __threadfence();
+            *s_last = last;
+        }
+        named_sync(1, kThreads);
+        if (!*s_last) continue;
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+            float M = -INFINITY, L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int kAhead = 8;
+            for (int p = c0; p <= c1; p += kAhead) {
+                float2 ml[kAhead];
+                float4 v[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int64_t at = (2 * static_cast<int64_t>(min(p + k, c1)) + (p + k == c0 ? 1 : 0)) * S::kRows + r;
+                    ml[k] = __ldcg(a.part_ml + at);
+                    v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (p + k > c1) break;
+                    const float M2 = fmaxf(M, ml[k].x), ref = M2 == -INFINITY ? 0.f : M2;
+                    const float fa = ex2(M - ref), fb = ex2(ml[k].x - ref);
+                    M = M2;
+                    L = L * fa + ml[k].y * fb;
+                    acc.x = acc.x * fa + v[k].x * fb;
+                    acc.y = acc.y * fa + v[k].y * fb;
+                    acc.z = acc.z * fa + v[k].z * fb;
+                    acc.w = acc.w * fa + v[k].w * fb;
+                }
+            }
+            put(r, col, acc, M, L);
+        }
+    }
+}
+
+// Launch of one shape: as many blocks as the GPU holds at once, at most kAttnMaxGrid.
+template <int KV, class S>
+cudaError_t launch_shape(const AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+    static LaunchCache lc;
+    int sms = 0, optin = 0;
+    cudaError_t e = device_limits(&sms, &optin);
+    if (e != cudaSuccess) return e;
+    auto kernel = attn_decode_kernel<KV, S>;
+    e = cached_dyn_smem(lc, kernel, S::kSmem);
+    if (e != cudaSuccess) return e;
+    const int want = sms * S::kMinBlocks;
+    kernel<<<want < kAttnMaxGrid ? want : kAttnMaxGrid, S::kThreads, S::kSmem, s>>>(a, k, v);
+    return cudaGetLastError();
+}
+
+template <int KV, int D>
+cudaError_t launch_rows(const AttnArgs& a, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+    switch (rows) {
+        case 16: return launch_shape<KV, Shape<KV, D, 1>>(a, k, v, s);
+        case 32: return launch_shape<KV, Shape<KV, D, 2>>(a, k, v, s);
+        default:
+            if constexpr (KV == kF32 && D == 256) return cudaErrorInvalidValue;
+            else return launch_shape<KV, Shape<KV, D, 4>>(a, k, v, s);
+    }
+}
+
+template <int KV>
+cudaError_t launch_dim(const AttnArgs& a, int D, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+    switch (D) {
+        case 64: return launch_rows<KV, 64>(a, rows, k, v, s);
+        case 128: return launch_rows<KV, 128>(a, rows, k, v, s);
+        default: return launch_rows<KV, 256>(a, rows, k, v, s);
+    }
+}
+
+}  // namespace attn
+}  // namespace rssm

@@ -1,0 +1,391 @@
+// The norms around a block of a hybrid model: add_norm (block output into the
+// residual stream, and the norm of the sum) and gated_norm (the norm after an
+// SSM mixer, fused with its gate).
+//
+// Both read each input once and write each output once: a row (add_norm) or a
+// group of a row's columns (gated_norm) is held in registers, in FP32, from
+// its load through one or two sums of squares to its store. They are bound by
+// HBM for many rows and by latency for few.
+#include "common.cuh"
+
+namespace rssm {
+namespace {
+
+constexpr int kMaxNormDim = 32768;   // columns that the threads of one block hold in registers
+
+struct AddNormArgs {
+    const void *u, *x, *gate;
+    void *u_out, *n_out;
+    const float *w_post, *w;
+    int64_t rows, u_stride, x_stride, gate_stride, uo_stride, no_stride;
+    int dim;
+    float eps, scale, w_off;
+};
+
+struct GatedNormArgs {
+    const void *y, *z;
+    const float* w;
+    void* out;
+    int64_t rows, y_stride, z_stride, out_stride;
+    int group, groups, w_dim;
+    int norm_first, act;
+    float eps, w_off;
+};
+
+// VEC consecutive elements as floats (VEC = 8: 16-byte aligned, or 1).
+template <int VEC>
+__device__ __forceinline__ void load_vec(float (&v)[VEC], const float* p) {
+    if (VEC == 8) {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x; v[1 % VEC] = a.y; v[2 % VEC] = a.z; v[3 % VEC] = a.w;
+        v[4 % VEC] = b.x; v[5 % VEC] = b.y; v[6 % VEC] = b.z; v[7 % VEC] = b.w;
+    } else {
+        v[0] = *p;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void load_vec(float (&v)[VEC], const __nv_bfloat16* p) {
+    if (VEC == 8) {
+        const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+        const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[(2 * i) % VEC] = __uint_as_float(r[i] << 16);
+            v[(2 * i + 1) % VEC] = __uint_as_float(r[i] & 0xFFFF0000u);
+        }
+    } else {
+        v[0] = __bfloat162float(*p);
+    }
+}
+// Weights stay in cache: every row reads them.
+template <int VEC>
+__device__ __forceinline__ void load_w(float (&v)[VEC], const float* p) {
+    if (VEC == 8) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x; v[1 % VEC] = a.y; v[2 % VEC] = a.z; v[3 % VEC] = a.w;
+        v[4 % VEC] = b.x; v[5 % VEC] = b.y; v[6 % VEC] = b.z; v[7 % VEC] = b.w;
+    } else {
+        v[0] = __ldg(p);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
+    if (VEC == 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1 % VEC], v[2 % VEC], v[3 % VEC]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4 % VEC], v[5 % VEC], v[6 % VEC], v[7 % VEC]);
+    } else {
+        *p = v[0];
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[VEC]) {
+    if (VEC == 8) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[(2 * i) % VEC], v[(2 * i + 1) % VEC]);
+            r[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+    } else {
+        *p = __float2bfloat16_rn(v[0]);
+    }
+}
+
+// Sum over the tpr threads that share a row: a power of two of adjacent lanes
+// up to 32, else the whole block (a multiple of 32). `slot` alternates between
+// two halves of s_red, so consecutive sums need one barrier each.
+__device__ __forceinline__ float row_sum(float v, int tpr, float* s_red) {
+    if (tpr <= 32) {
+        for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    v = warp_sum(v);
+    const int warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = (static_cast<int>(threadIdx.x & 31) < warps) ? s_red[threadIdx.x & 31] : 0.f;
+    return warp_sum(t);
+}
+
+template <class TU, class TX, int VEC, int VPT>
+__global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a, int tpr) {
+    __shared__ float s_red[2][32];
+    const int rows_per_block = blockDim.x / tpr;
+    const int lane = threadIdx.x % tpr;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + threadIdx.x / tpr;
+    const bool live = row < a.rows;
+    const int nvec = a.dim / VEC;
+    const TU* u = static_cast<const TU*>(a.u) + (live ? row : 0) * a.u_stride;
+    const TX* x = static_cast<const TX*>(a.x) + (live ? row : 0) * a.x_stride;
+    const TX* gt = static_cast<const TX*>(a.gate) + (live ? row : 0) * a.gate_stride;
+
+    float uv[VPT][VEC], xv[VPT][VEC];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * tpr;
+        if (live && c < nvec) {
+            load_vec<VEC>(uv[i], u + static_cast<int64_t>(c) * VEC);
+            if (a.x != nullptr) load_vec<VEC>(xv[i], x + static_cast<int64_t>(c) * VEC);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) uv[i][e] = xv[i][e] = 0.f;
+        }
+    }
+    if (a.x != nullptr) {
+        float r = 1.f;
+        if (a.w_post != nullptr) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) ss = fmaf(xv[i][e], xv[i][e], ss);
+            r = rsqrtf(row_sum(ss, tpr, s_red[0]) / static_cast<float>(a.dim) + a.eps);
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * tpr;
+            if (!live || c >= nvec) continue;
+            if (a.w_post != nullptr) {
+                float w[VEC];
+                load_w<VEC>(w, a.w_post + c * VEC);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) xv[i][e] *= r * (a.w_off + w[e]);
+            }
+            if (a.gate != nullptr) {
+                float g[VEC];
+                load_vec<VEC>(g, gt + static_cast<int64_t>(c) * VEC);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) xv[i][e] *= g[e];
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) uv[i][e] = fmaf(a.scale, xv[i][e], uv[i][e]);
+        }
+    }
+    if (a.u_out != nullptr) {
+        TU* uo = static_cast<TU*>(a.u_out) + (live ? row : 0) * a.uo_stride;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * tpr;
+            if (live && c < nvec) store_vec<VEC>(uo + static_cast<int64_t>(c) * VEC, uv[i]);
+        }
+    }
+    if (a.n_out == nullptr) return;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ss = fmaf(uv[i][e], uv[i][e], ss);
+    const float r = rsqrtf(row_sum(ss, tpr, s_red[1]) / static_cast<float>(a.dim) + a.eps);
+    TX* no = static_cast<TX*>(a.n_out) + (live ? row : 0) * a.no_stride;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * tpr;
+        if (!live || c >= nvec) continue;
+        float w[VEC];
+        load_w<VEC>(w, a.w + c * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = uv[i][e] * r * (a.w_off + w[e]);
+        store_vec<VEC>(no + static_cast<int64_t>(c) * VEC, w);
+    }
+}
+
+template <class T, int VEC, int VPT>
+__global__ void __launch_bounds__(1024) gated_norm_kernel(const GatedNormArgs a, int tpr) {
+    __shared__ float s_red[32];
+    const int per_block = blockDim.x / tpr;
+    const int lane = threadIdx.x % tpr;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / tpr;
+    const bool live = item < a.rows * a.groups;
+    const int64_t row = live ? item / a.groups : 0;
+    const int col0 = live ? static_cast<int>(item - row * a.groups) * a.group : 0;
+    const int nvec = a.group / VEC;
+    const T* y = static_cast<const T*>(a.y) + row * a.y_stride + col0;
+    const T* z = static_cast<const T*>(a.z) + row * a.z_stride + col0;
+    float v[VPT][VEC], g[VPT][VEC];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * tpr;
+        if (live && c < nvec) {
+            load_vec<VEC>(v[i], y + static_cast<int64_t>(c) * VEC);
+            load_vec<VEC>(g[i], z + static_cast<int64_t>(c) * VEC);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v[i][e] = g[i][e] = 0.f;
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float d = 1.f + expf(-g[i][e]);
+            g[i][e] = ((a.act == RSSM_GATE_SILU) ? g[i][e] : 1.f) / d;
+            if (!a.norm_first) v[i][e] *= g[i][e];
+            ss = fmaf(v[i][e], v[i][e], ss);
+        }
+    const float r = rsqrtf(row_sum(ss, tpr, s_red) / static_cast<float>(a.group) + a.eps);
+    const float* w = a.w + (a.w_dim == a.group ? 0 : col0);
+    T* out = static_cast<T*>(a.out) + row * a.out_stride + col0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * tpr;
+        if (!live || c >= nvec) continue;
+        float wv[VEC];
+        load_w<VEC>(wv, w + c * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            wv[e] = v[i][e] * r * (a.w_off + wv[e]);
+            if (a.norm_first) wv[e] *= g[i][e];
+        }
+        store_vec<VEC>(out + static_cast<int64_t>(c) * VEC, wv);
+    }
+}
+
+// Threads per row for nvec vectors of a row, vpt at most per thread: a power of
+// two of lanes, or a block of whole warps.
+int threads_per_row(int nvec, int vpt) {
+    const int need = (nvec + vpt - 1) / vpt;
+    if (need > 32) return (need + 31) / 32 * 32;
+    int t = 1;
+    while (t < need) t *= 2;
+    return t;
+}
+
+struct NormShape {
+    int tpr, vpt, threads;
+    int64_t blocks;
+};
+
+// vec 8: 1, 2 or 4 vectors a thread; vec 1: 2, 8 or 32 elements. The fewest
+// that cover the row with at most 1024 threads.
+NormShape norm_shape(int cols, int vec, int64_t items) {
+    const int nvec = cols / vec;
+    const int choice[2][3] = {{1, 2, 4}, {2, 8, 32}};
+    const int* c = choice[vec == 8 ? 0 : 1];
+    NormShape s{};
+    for (int i = 0; i < 3; ++i) {
+        s.vpt = c[i];
+        s.tpr = threads_per_row(nvec, s.vpt);
+        if (s.tpr <= 1024) break;
+    }
+    s.threads = s.tpr <= 32 ? 256 : s.tpr;
+    const int per = s.threads / s.tpr;
+    s.blocks = (items + per - 1) / per;
+    return s;
+}
+
+bool vec_ok(const void* p, int64_t stride, int esz) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride * esz) % 16 == 0;
+}
+
+template <class TU, class TX>
+cudaError_t launch_add(const AddNormArgs& a, int vec, const NormShape& s, cudaStream_t st) {
+    const dim3 g(static_cast<unsigned>(s.blocks));
+    if (vec == 8) {
+        if (s.vpt == 1) add_norm_kernel<TU, TX, 8, 1><<<g, s.threads, 0, st>>>(a, s.tpr);
+        else if (s.vpt == 2) add_norm_kernel<TU, TX, 8, 2><<<g, s.threads, 0, st>>>(a, s.tpr);
+        else add_norm_kernel<TU, TX, 8, 4><<<g, s.threads, 0, st>>>(a, s.tpr);
+    } else {
+        if (s.vpt == 2) add_norm_kernel<TU, TX, 1, 2><<<g, s.threads, 0, st>>>(a, s.tpr);
+        else if (s.vpt == 8) add_norm_kernel<TU, TX, 1, 8><<<g, s.threads, 0, st>>>(a, s.tpr);
+        else add_norm_kernel<TU, TX, 1, 32><<<g, s.threads, 0, st>>>(a, s.tpr);
+    }
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_gated(const GatedNormArgs& a, int vec, const NormShape& s, cudaStream_t st) {
+    const dim3 g(static_cast<unsigned>(s.blocks));
+    if (vec == 8) {
+        if (s.vpt == 1) gated_norm_kernel<T, 8, 1><<<g, s.threads, 0, st>>>(a, s.tpr);
+        else if (s.vpt == 2) gated_norm_kernel<T, 8, 2><<<g, s.threads, 0, st>>>(a, s.tpr);
+        else gated_norm_kernel<T, 8, 4><<<g, s.threads, 0, st>>>(a, s.tpr);
+    } else {
+        if (s.vpt == 2) gated_norm_kernel<T, 1, 2><<<g, s.threads, 0, st>>>(a, s.tpr);
+        else if (s.vpt == 8) gated_norm_kernel<T, 1, 8><<<g, s.threads, 0, st>>>(a, s.tpr);
+        else gated_norm_kernel<T, 1, 32><<<g, s.threads, 0, st>>>(a, s.tpr);
+    }
+    return cudaGetLastError();
+}
+
+bool float_dtype(int d) { return d == RSSM_F32 || d == RSSM_BF16; }
+int elem_size(int d) { return d == RSSM_F32 ? 4 : 2; }
+
+// A row stride: 0 stands for `dim`; otherwise rows must not overlap.
+bool row_stride(int64_t s, int dim, int64_t* out) {
+    *out = s == 0 ? dim : s;
+    return s == 0 || s >= dim;
+}
+
+}  // namespace
+}  // namespace rssm
+
+using namespace rssm;
+
+extern "C" {
+
+rssm_status rssm_add_norm(const rssm_add_norm_config* c, const void* d_u, const void* d_x, const float* d_w_post,
+                          const void* d_gate, const float* d_w, void* d_u_out, void* d_n_out, void* stream) {
+    if (c == nullptr || c->rows < 0 || c->rows > 0x7FFFFFFF || c->dim < 1) return RSSM_ERR_INVALID_ARG;
+    if (!float_dtype(c->res_dtype) || !float_dtype(c->dtype) || !(c->eps >= 0.f)) return RSSM_ERR_INVALID_ARG;
+    if (c->dim > kMaxNormDim) return RSSM_ERR_UNSUPPORTED;
+    AddNormArgs a{};
+    if (!row_stride(c->u_stride, c->dim, &a.u_stride) || !row_stride(c->x_stride, c->dim, &a.x_stride) ||
+        !row_stride(c->u_out_stride, c->dim, &a.uo_stride) || !row_stride(c->n_out_stride, c->dim, &a.no_stride))
+        return RSSM_ERR_INVALID_ARG;
+    if (c->gate_stride != 0 && c->gate_stride < c->dim) return RSSM_ERR_INVALID_ARG;
+    if (c->rows == 0) return RSSM_OK;
+    if (d_u == nullptr || (d_u_out == nullptr && d_n_out == nullptr) || (d_n_out != nullptr && d_w == nullptr))
+        return RSSM_ERR_INVALID_ARG;
+    if (d_x == nullptr && (d_w_post != nullptr || d_gate != nullptr)) return RSSM_ERR_INVALID_ARG;
+    a.u = d_u; a.x = d_x; a.gate = d_gate; a.u_out = d_u_out; a.n_out = d_n_out;
+    a.w_post = d_w_post; a.w = d_w;
+    a.rows = c->rows; a.dim = c->dim; a.gate_stride = c->gate_stride;
+    a.eps = c->eps; a.scale = c->scale; a.w_off = c->w_offset;
+    const int eu = elem_size(c->res_dtype), ex = elem_size(c->dtype);
+    const bool wide = c->dim % 8 == 0 && vec_ok(d_u, a.u_stride, eu) && vec_ok(d_x, a.x_stride, ex) &&
+                      vec_ok(d_gate, a.gate_stride, ex) && vec_ok(d_u_out, a.uo_stride, eu) &&
+                      vec_ok(d_n_out, a.no_stride, ex) && vec_ok(d_w, 0, 4) && vec_ok(d_w_post, 0, 4);
+    const int vec = wide ? 8 : 1;
+    const NormShape s = norm_shape(c->dim, vec, c->rows);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (c->res_dtype == RSSM_F32)
+        e = c->dtype == RSSM_F32 ? launch_add<float, float>(a, vec, s, st) : launch_add<float, __nv_bfloat16>(a, vec, s, st);
+    else
+        e = c->dtype == RSSM_F32 ? launch_add<__nv_bfloat16, float>(a, vec, s, st)
+                                 : launch_add<__nv_bfloat16, __nv_bfloat16>(a, vec, s, st);
+    return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
+}
+
+rssm_status rssm_gated_norm(const rssm_gated_norm_config* c, const void* d_y, const void* d_z, const float* d_w,
+                            void* d_out, void* stream) {
+    if (c == nullptr || c->rows < 0 || c->dim < 1 || c->group < 1 || c->dim % c->group != 0) return RSSM_ERR_INVALID_ARG;
+    if (c->w_dim != c->dim && c->w_dim != c->group) return RSSM_ERR_INVALID_ARG;
+    if (!float_dtype(c->dtype) || !(c->eps >= 0.f)) return RSSM_ERR_INVALID_ARG;
+    if (c->act != RSSM_GATE_SILU && c->act != RSSM_GATE_SIGMOID) return RSSM_ERR_INVALID_ARG;
+    if (c->norm_first != 0 && c->norm_first != 1) return RSSM_ERR_INVALID_ARG;
+    GatedNormArgs a{};
+    if (!row_stride(c->y_stride, c->dim, &a.y_stride) || !row_stride(c->z_stride, c->dim, &a.z_stride) ||
+        !row_stride(c->out_stride, c->dim, &a.out_stride))
+        return RSSM_ERR_INVALID_ARG;
+    if (c->rows > 0x7FFFFFFF / (c->dim / c->group)) return RSSM_ERR_INVALID_ARG;
+    if (c->group > kMaxNormDim) return RSSM_ERR_UNSUPPORTED;
+    if (c->rows == 0) return RSSM_OK;
+    if (d_y == nullptr || d_z == nullptr || d_w == nullptr || d_out == nullptr) return RSSM_ERR_INVALID_ARG;
+    a.y = d_y; a.z = d_z; a.w = d_w; a.out = d_out;
+    a.rows = c->rows; a.group = c->group; a.groups = c->dim / c->group; a.w_dim = c->w_dim;
+    a.norm_first = c->norm_first; a.act = c->act; a.eps = c->eps; a.w_off = c->w_offset;
+    const int es = elem_size(c->dtype);
+    const bool wide = c->group % 8 == 0 && vec_ok(d_y, a.y_stride, es) && vec_ok(d_z, a.z_stride, es) &&
+                      vec_ok(d_out, a.out_stride, es) && vec_ok(d_w, 0, 4);
+    const int vec = wide ? 8 : 1;
+    const NormShape s = norm_shape(c->group, vec, a.rows * a.groups);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = c->dtype == RSSM_F32 ? launch_gated<float>(a, vec, s, st)
+                                               : launch_gated<__nv_bfloat16>(a, vec, s, st);
+    return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
+}
+
+}  // extern "C"

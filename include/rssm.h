@@ -486,6 +486,235 @@ rssm_status rssm_count_summary(const rssm_handle* h, int32_t* known, int32_t* mi
  */
 rssm_status rssm_destroy(rssm_handle* h);
 
+/* ==========================================================================
+ * The attention side of a hybrid decode step. A hybrid model's step runs, beside
+ * its SSM layers, attention layers over a paged key-value cache, and a norm
+ * around every mixer. The functions below are those parts: the page table of a
+ * batch, the cache's writer and the attention that reads it, and the two
+ * fused norms. The conventions at the top hold (caller-owned memory, calls
+ * asynchronous on `stream`, host-detectable errors as a status, device-detected
+ * errors in an error word).
+ * ========================================================================== */
+
+/* Further device error codes. */
+enum {
+    RSSM_DEV_PAGES_EMPTY = 16, /* the pool has no page left for a request          */
+    RSSM_DEV_PAGES_ROW = 17,   /* a request needs more than max_pages pages         */
+    RSSM_DEV_PAGES_COUNT = 18, /* a token count or length out of range              */
+    RSSM_DEV_PAGES_SLOTS = 19, /* the slot list is too short for a request's tokens */
+    RSSM_DEV_ATTN_LEN = 20,    /* a request's length out of 0 .. max_pages*page_size */
+    RSSM_DEV_ATTN_PAGE = 21,   /* a page number out of 0 .. num_pages - 1           */
+    RSSM_DEV_ATTN_SLOT = 22    /* a slot beyond num_pages*page_size - 1             */
+};
+
+/* ---- page table ----------------------------------------------------------
+ * A cache of num_pages pages of page_size tokens serves a batch of requests.
+ * Request b holds ceil(len_b / page_size) pages, listed in order in its row of
+ * the table; token i of the request lies in slot
+ *   table[b][i / page_size] * page_size + i % page_size.
+ * The free pages are a stack. Every step of a serving loop that changes lengths
+ * runs on the GPU from device counts, so the loop never waits for the host:
+ *   extend    need_b = ceil((len_b + new_b)/page_size) - ceil(len_b/page_size);
+ *             with the exclusive scan e_b of need over the requests in order and
+ *             N its total, page j of request b's new ones is
+ *             free[free_count - N + e_b + j]; then free_count -= N.
+ *   rollback, truncate   the pages past ceil(len'_b/page_size) go back:
+ *             free[free_count + e_b + j] = table[b][held'_b + j], table entry = -1.
+ * The order is that of the requests, whatever the launch, so a rollback undoes
+ * the extend before it to the last entry, and reruns give the same pages. */
+typedef struct {
+    int32_t batch;      /* requests, >= 1                              */
+    int32_t page_size;  /* tokens per page, >= 1                       */
+    int32_t num_pages;  /* pages of the cache; num_pages*page_size < 2^31 */
+    int32_t max_pages;  /* pages one request may hold (table row); batch*max_pages < 2^31 */
+} rssm_pages_config;
+
+/* Byte offsets of the regions in the page table's workspace:
+ *   lens int32 [batch]; table int32 [batch][max_pages], -1 where no page is
+ *   held; free int32 [num_pages], the stack, of which the first free_count
+ *   entries are free pages; free_count int32 [1]; err int32 [4]. */
+typedef struct {
+    size_t lens, table, free, free_count, err;
+    size_t total_bytes;
+} rssm_pages_layout;
+
+typedef struct rssm_pages rssm_pages;
+
+/* Host only. Errors: INVALID_ARG (null, a size out of range). */
+rssm_status rssm_pages_layout_for(const rssm_pages_config* cfg, rssm_pages_layout* out);
+
+/* A page table on the caller's workspace (256-byte aligned, total_bytes, outlives
+ * the handle), with all lengths 0 and all pages free.
+ *   d_free0  device int32 [num_pages], the free stack at the start (each page
+ *            once; the last is taken first); NULL: 0 .. num_pages - 1. Copied.
+ * Errors: INVALID_ARG, CAPACITY (workspace too small, no host memory), CUDA. */
+rssm_status rssm_pages_create(const rssm_pages_config* cfg, void* d_workspace, size_t workspace_bytes,
+                              const int32_t* d_free0, void* stream, rssm_pages** out);
+
+/* Room for more tokens, and where they go.
+ *   T, d_new     d_new == NULL: T >= 1 tokens for every request; else T = 0 and
+ *                d_new is device int32 [batch] (0 leaves a request as it is).
+ *   d_slots      device int32 [max_tokens]: slot of every new token, request
+ *                after request (request b's first token at the sum of new over the
+ *                requests before it; T tokens each: [batch][T]).
+ *   d_positions  NULL or device int32 [max_tokens]: each new token's position in
+ *                its request.
+ * A request that cannot be served (no page left, row full, count < 0, slots
+ * short) is left unchanged, its tokens' slots and positions are -1, and the
+ * error word is set; the others are served. Entries past the last token are
+ * not written. d_slots and d_positions: 4-byte aligned.
+ * Errors: INVALID_ARG (null, T, max_tokens < batch*T where d_new is NULL), CUDA. */
+rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, int32_t* d_slots,
+                              int32_t* d_positions, int32_t max_tokens, void* stream);
+
+/* Drop the drafts that a verification turned down: of the last T tokens of
+ * request b, d_accepted[b] (device int32 [batch], 0..T) stay. The counterpart of
+ * rssm_verify_rollback for the attention layers' cache: only lengths and pages
+ * move. A count out of 0..T, or T above the request's length, leaves the request
+ * unchanged and sets RSSM_DEV_PAGES_COUNT. Errors: INVALID_ARG, CUDA. */
+rssm_status rssm_pages_rollback(rssm_pages* h, int32_t T, const int32_t* d_accepted, void* stream);
+
+/* Cut request b to min(len_b, d_keep[b]) tokens (device int32 [batch]); 0 ends a
+ * request. A negative d_keep[b] leaves it unchanged and sets
+ * RSSM_DEV_PAGES_COUNT. Errors: INVALID_ARG, CUDA. */
+rssm_status rssm_pages_truncate(rssm_pages* h, const int32_t* d_keep, void* stream);
+
+/* Copy the error word (code, number of requests, request, value) to err4 and clear
+ * it. Synchronises `stream`. Errors: INVALID_ARG, CUDA. */
+rssm_status rssm_pages_get_error(rssm_pages* h, int32_t* err4, void* stream);
+
+/* Free the host handle; the workspace stays the caller's. */
+rssm_status rssm_pages_destroy(rssm_pages* h);
+
+/* ---- attention over a paged cache ------------------------------------------
+ * K and V caches [num_pages][kv_heads][page_size][head_dim], one layer each. For
+ * the T new tokens of a request of length len (the new ones included, their keys
+ * and values in the cache), token t = 0..T-1 has position p = len - T + t and sees
+ * positions max(0, p - window + 1) .. p (window 0: from 0):
+ *   s_i = scale q.k_i ; out = sum_i exp(s_i - lse) v_i ; lse = log sum_i exp(s_i)
+ * over the positions it sees. Query head h reads cache head h/(q_heads/kv_heads).
+ * A token that sees nothing (p < 0), or only scores of -inf, has out = 0 and
+ * lse = -inf. Nothing that a token does not see reaches its output, NaN and
+ * infinities included. */
+enum { RSSM_KV_FP8 = 4 };   /* kv_dtype: E4M3 codes, one FP32 scale per cache head for K and for V */
+
+typedef struct {
+    int32_t batch;
+    int32_t q_heads;    /* a multiple of kv_heads                                     */
+    int32_t kv_heads;
+    int32_t head_dim;   /* 64, 128 or 256                                             */
+    int32_t page_size;  /* a multiple of 16                                           */
+    int32_t num_pages;  /* num_pages*page_size < 2^31                                 */
+    int32_t max_pages;  /* entries in a row of the page table                         */
+    int32_t max_draft;  /* most new tokens per request and call, 1..8                 */
+    int32_t in_dtype;   /* RSSM_F32 or RSSM_BF16: q, k, v, out                        */
+    int32_t kv_dtype;   /* RSSM_F32 (F32 inputs), RSSM_BF16 or RSSM_KV_FP8 (BF16 inputs) */
+    int32_t window;     /* 0: none                                                    */
+    float scale;        /* 0: 1/sqrt(head_dim)                                        */
+    int64_t page_stride; /* elements from one page to the next, in both caches; 0:
+                            dense (kv_heads*page_size*head_dim). A multiple of 16
+                            bytes, so that K and V may lie in one array, page by page */
+} rssm_attn_config;
+
+typedef struct rssm_attn rssm_attn;
+
+/* Workspace bytes of rssm_attn_create (the parts of a request's attention that
+ * were split over blocks, their arrival counters, the error word). Host only.
+ * Errors: INVALID_ARG, UNSUPPORTED. */
+rssm_status rssm_attn_workspace_size(const rssm_attn_config* cfg, size_t* bytes);
+
+/* One attention layer on the caller's caches and workspace.
+ *   d_k_cache, d_v_cache  16-byte aligned; must outlive the handle.
+ *   d_k_scale, d_v_scale  RSSM_KV_FP8: FP32 [kv_heads], finite and > 0; the cache
+ *                         stands for code*scale. NULL otherwise. Must outlive the handle.
+ *   d_workspace           256-byte aligned. The layers of one stream may share one
+ *                         workspace (same or larger size): a call leaves it as it
+ *                         found it. Zeroed here, on `stream`.
+ * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY, CUDA. */
+rssm_status rssm_attn_create(const rssm_attn_config* cfg, void* d_k_cache, void* d_v_cache,
+                             const float* d_k_scale, const float* d_v_scale, void* d_workspace,
+                             size_t workspace_bytes, void* stream, rssm_attn** out);
+
+/* Write new tokens' keys and values to their slots.
+ *   d_k, d_v   in_dtype [tokens][kv_heads][head_dim], consecutive tokens
+ *              k_stride / v_stride elements apart (0: dense).
+ *   d_slots    int32 [tokens] as rssm_pages_extend gives them; a negative one is
+ *              skipped, one past the cache is skipped and reported.
+ * RSSM_KV_FP8 stores E4M3(x / scale), to nearest even, at most +-448.
+ * Errors: INVALID_ARG (null, tokens < 0, a stride below the row), CUDA. */
+rssm_status rssm_attn_append(rssm_attn* h, int32_t tokens, const void* d_k, int64_t k_stride, const void* d_v,
+                             int64_t v_stride, const int32_t* d_slots, void* stream);
+
+/* The attention of T new tokens a request.
+ *   d_q      in_dtype [batch][T][q_heads][head_dim], consecutive tokens q_stride
+ *            elements apart (0: dense); 16-byte aligned, q_stride a multiple of 16 bytes.
+ *   d_lens   int32 [batch], new tokens included.
+ *   d_table  int32 [batch][max_pages]; entries past a request's pages are not read.
+ *   d_out    in_dtype [batch][T][q_heads][head_dim], dense, 16-byte aligned.
+ *   d_lse    NULL or FP32 [batch][T][q_heads].
+ * A length out of range is cut to the range, and a page number out of range read
+ * as zeros; both are reported.
+ * Errors: INVALID_ARG, CAPACITY (T > max_draft), CUDA. */
+rssm_status rssm_attn_decode(rssm_attn* h, int32_t T, const void* d_q, int64_t q_stride, const int32_t* d_lens,
+                             const int32_t* d_table, void* d_out, float* d_lse, void* stream);
+
+/* As rssm_pages_get_error, for the layer's workspace (code, count, request or
+ * token, value; for RSSM_DEV_TIMEOUT the tile is -1). */
+rssm_status rssm_attn_get_error(rssm_attn* h, int32_t* err4, void* stream);
+
+/* Free the host handle; caches and workspace stay the caller's. */
+rssm_status rssm_attn_destroy(rssm_attn* h);
+
+/* ---- norms around a block --------------------------------------------------
+ * All sums in FP32; each output is rounded once. Weights are FP32 and enter as
+ * w_offset + w (0, or 1 for weights kept around zero). Row strides are in
+ * elements; 0 means dense, except gate_stride, where it means one gate vector
+ * for all rows. An output may be the input that it replaces (u_out = u,
+ * n_out = x, out = y), with the same stride. */
+typedef struct {
+    int64_t rows;
+    int32_t dim;
+    int32_t res_dtype;     /* u, u_out: RSSM_F32 or RSSM_BF16 */
+    int32_t dtype;         /* x, gate, n_out                  */
+    float eps;
+    float scale;           /* residual scale                  */
+    float w_offset;
+    int64_t u_stride, x_stride, gate_stride, u_out_stride, n_out_stride;
+} rssm_add_norm_config;
+
+/* Between two blocks: the block's output x into the residual stream u, and the
+ * norm of the sum that the next block reads.
+ *   a = x * rsqrt(mean(x^2) + eps) * (w_offset + w_post)     (w_post NULL: a = x)
+ *   u_out = u + scale * gate * a                             (gate NULL: 1; x NULL: u_out = u)
+ *   n_out = u_out * rsqrt(mean(u_out^2) + eps) * (w_offset + w)
+ * n_out is computed from the sum before its rounding to res_dtype. d_u_out may
+ * be NULL (the sum is not stored), and so may d_n_out (then d_w may be too).
+ * Errors: INVALID_ARG. rows = 0 is RSSM_OK. */
+rssm_status rssm_add_norm(const rssm_add_norm_config* cfg, const void* d_u, const void* d_x, const float* d_w_post,
+                          const void* d_gate, const float* d_w, void* d_u_out, void* d_n_out, void* stream);
+
+enum { RSSM_GATE_SILU = 1, RSSM_GATE_SIGMOID = 2 };
+
+typedef struct {
+    int64_t rows;
+    int32_t dim;
+    int32_t group;         /* columns normalised together; dim % group == 0      */
+    int32_t w_dim;         /* weights: dim, or group (the same for every group)  */
+    int32_t dtype;         /* y, z, out: RSSM_F32 or RSSM_BF16                   */
+    int32_t norm_first;    /* 1: norm(y) w act(z) ; 0: norm(y act(z)) w          */
+    int32_t act;           /* RSSM_GATE_*                                        */
+    float eps;
+    float w_offset;
+    int64_t y_stride, z_stride, out_stride;
+} rssm_gated_norm_config;
+
+/* After an SSM mixer: its output y [rows][dim], gated by z and normalised per
+ * group. norm_first = 0 is the Mamba-2 block's order (groups of d_inner/G
+ * columns), 1 the Gated DeltaNet block's (one group per head, w_dim = group).
+ * Errors: INVALID_ARG. rows = 0 is RSSM_OK. */
+rssm_status rssm_gated_norm(const rssm_gated_norm_config* cfg, const void* d_y, const void* d_z, const float* d_w,
+                            void* d_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
