@@ -67,9 +67,12 @@ struct Shape {
     static constexpr int kFixed = 2 * kRows * QS + kRows * OS * 4 + NT * kRows * 8 + kRows * 8 + 512;
     static constexpr int kBudget = (kMinBlocks == 2 ? 113 : 226) * 1024 - 1024;
     static constexpr int kSlotsFit = (kBudget - kFixed) / kSlot;
-    static constexpr int NS = kSlotsFit > 24 ? 24 : kSlotsFit;
+    // A multiple of NT, so that a slot always belongs to the same warp of each
+    // row group: a warp then never waits for a turn of a slot before it has seen
+    // the turn before, which the parity of the slot's barrier could not tell apart.
+    static constexpr int NS = (kSlotsFit > 24 ? 24 : kSlotsFit) / NT * NT;
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
-    static_assert(NS >= NT, "ring too small");
+    static_assert(NS >= NT && NS % NT == 0, "ring too small");
 };
 
 // ---- instructions -----------------------------------------------------------

@@ -154,6 +154,25 @@ def test_split_and_join(cuda_lib, lens, kv_heads, ps, kv):
     assert layer.get_error()[0] == 0
 
 
+@pytest.mark.parametrize("kv,dim,T", [("bf16", 64, 1), ("bf16", 128, 8), ("bf16", 256, 4), ("fp8", 64, 1), ("fp8", 256, 8),
+                                      ("f32", 128, 4), ("f32", 256, 8)])
+def test_long_shares(cuda_lib, kv, dim, T):
+    """Blocks whose share is many times their ring of slots: the small cache is
+    read by many requests through tables that repeat its pages."""
+    c = Case([1500], T=T, q_heads=8, kv_heads=2, dim=dim, kv=kv, seed=dim)
+    one, one_lse = c.run()
+    c.check((one, one_lse))
+    n = 300
+    c.table, c.lens_d, c.lens = c.table.repeat(n, 1), c.lens_d.repeat(n), c.lens * n
+    c.q = c.q.repeat(n, 1, 1, 1)
+    out, lse = c.run()
+    vmax = float(c.tokens[0][1].abs().max())
+    # the same sums in other parts: 2^-12 vmax (FP8 weights) and a rounding of the output
+    lim = 2.0 ** -11 * vmax + (one.float().abs() * 2.0 ** -7 if kv != "f32" else 0)
+    assert bool(((out.float() - one.float()).abs() <= lim).all())
+    assert float((lse - one_lse).abs().max()) < 2.0 ** -13
+
+
 def test_large_scores_and_scale(cuda_lib):
     """Scores whose exponentials pass FP32 either way, and a given scale."""
     c = Case([300, 40], q_heads=4, kv_heads=2, dim=64, seed=2)
