@@ -337,23 +337,40 @@ struct Warp {
                 }
             }
         } else {
+            // The tensor cores cut their sums off below FP32's last bit, always
+            // towards zero, so chains are kept short: the leading products of 32
+            // columns at a time, rounded into s by FP32 adds, and the two small
+            // products apart from them.
             const int r = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                uint32_t ah[4], al[4], bh[4], bl[4];
+            float small[2][4] = {};
+#pragma unroll 1
+            for (int i0 = 0; i0 < D / 8; i0 += 4) {
+                float lead[2][4] = {};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    split_tf32(qs[(g + 8 * (j & 1)) * (S::QS / 4) + i * 8 + c + 4 * (j >> 1)], ah[j], al[j]);
-                ldsm4(b, k + swz<S>(r, 2 * i + ch));
+                for (int i = i0; i < i0 + 4; ++i) {
+                    uint32_t ah[4], al[4], bh[4], bl[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) split_tf32(__uint_as_float(b[j]), bh[j], bl[j]);
+                    for (int j = 0; j < 4; ++j)
+                        split_tf32(qs[(g + 8 * (j & 1)) * (S::QS / 4) + i * 8 + c + 4 * (j >> 1)], ah[j], al[j]);
+                    ldsm4(b, k + swz<S>(r, 2 * i + ch));
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    mma_tf32(s[j], al, bh[2 * j], bh[2 * j + 1]);
-                    mma_tf32(s[j], ah, bl[2 * j], bl[2 * j + 1]);
-                    mma_tf32(s[j], ah, bh[2 * j], bh[2 * j + 1]);
+                    for (int j = 0; j < 4; ++j) split_tf32(__uint_as_float(b[j]), bh[j], bl[j]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        mma_tf32(small[j], al, bh[2 * j], bh[2 * j + 1]);
+                        mma_tf32(small[j], ah, bl[2 * j], bl[2 * j + 1]);
+                        mma_tf32(lead[j], ah, bh[2 * j], bh[2 * j + 1]);
+                    }
                 }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[j][x] += lead[j][x];
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[j][x] += small[j][x];
         }
     }
 
@@ -429,9 +446,12 @@ struct Warp {
             uint32_t h0, l0, h1, l1;
             split_tf32(__uint_as_float(b0), h0, l0);
             split_tf32(__uint_as_float(b1), h1, l1);
-            mma_tf32(acc, w.lo[h], h0, h1);
-            mma_tf32(acc, w.hi[h], l0, l1);
-            mma_tf32(acc, w.hi[h], h0, h1);
+            float p[4] = {};                                   // a short chain, as in scores()
+            mma_tf32(p, w.lo[h], h0, h1);
+            mma_tf32(p, w.hi[h], l0, l1);
+            mma_tf32(p, w.hi[h], h0, h1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += p[j];
         }
     }
 

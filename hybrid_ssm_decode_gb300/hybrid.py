@@ -6,15 +6,62 @@ Each call checks its tensors' type, device, shape and strides, and then makes
 one call of the C ABI (include/rssm.h) on the given stream, or torch's current
 one. Nothing here synchronises or copies; a ValueError names the argument that
 does not fit, and an RssmError a status of the library.
+
+A decode step makes these calls by the dozen, and a kernel of theirs takes a few
+microseconds, so what the checks conclude (strides, a filled configuration
+struct) is kept by what they looked at: the tensors' types, devices, shapes and
+strides, never their addresses. A call with a signature seen before is a look-up
+and the C call.
 """
 from __future__ import annotations
 
 import hybrid_ssm_decode_gb300 as _r
 
 
+_KEPT = 512          # signatures kept per kind of call
+
+
 def _torch():
     import torch
     return torch
+
+
+def _sig(t):
+    """What the checks look at of a tensor (or None)."""
+    return None if t is None else (t.dtype, t.get_device(), t.shape, t.stride())
+
+
+def _keep(store, key, value):
+    if len(store) >= _KEPT:
+        store.clear()
+    store[key] = value
+    return value
+
+
+def _raw_stream(device_index):
+    """torch's current stream on a device, as an address."""
+    torch = _torch()
+    return torch.cuda.current_stream(device_index).cuda_stream
+
+
+def _stream_of(stream, device_index):
+    if stream is None:
+        return _raw_stream(device_index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _bind():
+    """The library's functions and torch's raw-stream query, once both are loaded."""
+    global _lib, _raw_stream
+    if _lib is None:
+        _lib = _r.load()
+        raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            _raw_stream = raw
+    return _lib
+
+
+_lib = None
 
 
 _DTYPES: dict = {}
@@ -73,6 +120,8 @@ class PageTable:
                 n *= s
             return self.workspace[off:off + 4 * n].view(torch.int32).view(*shape)
 
+        self._seen = {}
+        self._fn = _bind()
         self.lens = view(lay.lens, batch)
         self.table = view(lay.table, batch, max_pages)
         self.free_count = view(lay.free_count, 1)
@@ -91,24 +140,42 @@ class PageTable:
     def extend(self, slots, T=0, new=None, positions=None, stream=None):
         """Room for T tokens more in every request, or new[b] (int32, device)
         in request b; writes the new tokens' slots (and positions)."""
-        _need((T == 0) != (new is None), "extend: give either T or new")
-        n = slots.numel()
-        _ints(slots, n, self.device, "slots")
-        if positions is not None:
-            _ints(positions, n, self.device, "positions")
-        if new is not None:
-            _ints(new, self.cfg.batch, self.device, "new")
-        _r.rssm_pages_extend(self.handle, T, new, slots, positions, n, stream)
+        key = (_sig(slots), _sig(new), _sig(positions), T == 0)
+        n = self._seen.get(key)
+        if n is None:
+            _need((T == 0) != (new is None), "extend: give either T or new")
+            n = slots.numel()
+            _ints(slots, n, self.device, "slots")
+            if positions is not None:
+                _ints(positions, n, self.device, "positions")
+            if new is not None:
+                _ints(new, self.cfg.batch, self.device, "new")
+            _keep(self._seen, key, n)
+        st = self._fn.rssm_pages_extend(self.handle, T, None if new is None else new.data_ptr(), slots.data_ptr(),
+                                        None if positions is None else positions.data_ptr(), n,
+                                        _stream_of(stream, self.device.index))
+        if st:
+            _r._check("rssm_pages_extend", st)
 
     def rollback(self, T, accepted, stream=None):
         """Of the last T tokens of request b, accepted[b] stay."""
-        _ints(accepted, self.cfg.batch, self.device, "accepted")
-        _r.rssm_pages_rollback(self.handle, T, accepted, stream)
+        self._counts(accepted, "accepted")
+        st = self._fn.rssm_pages_rollback(self.handle, T, accepted.data_ptr(), _stream_of(stream, self.device.index))
+        if st:
+            _r._check("rssm_pages_rollback", st)
 
     def truncate(self, keep, stream=None):
         """Cut request b to keep[b] tokens (0 ends it)."""
-        _ints(keep, self.cfg.batch, self.device, "keep")
-        _r.rssm_pages_truncate(self.handle, keep, stream)
+        self._counts(keep, "keep")
+        st = self._fn.rssm_pages_truncate(self.handle, keep.data_ptr(), _stream_of(stream, self.device.index))
+        if st:
+            _r._check("rssm_pages_truncate", st)
+
+    def _counts(self, t, name):
+        key = _sig(t)
+        if key not in self._seen:
+            _ints(t, self.cfg.batch, self.device, name)
+            _keep(self._seen, key, True)
 
     def get_error(self, stream=None):
         return _r.rssm_pages_get_error(self.handle, stream)
@@ -186,7 +253,9 @@ class Attention:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         _on(workspace, self.device, "workspace")
         self.workspace = workspace
-        self._keep = (k_cache, v_cache, k_scale, v_scale)
+        self._tensors = (k_cache, v_cache, k_scale, v_scale)
+        self._seen = {}
+        self._fn = _bind()
         self.handle = _r.rssm_attn_create(self.cfg, k_cache, v_cache, k_scale, v_scale, workspace,
                                           workspace.numel() * workspace.element_size(), stream)
 
@@ -204,20 +273,36 @@ class Attention:
     def append(self, k, v, slots, stream=None):
         """Write the new tokens' keys and values ([tokens][kv_heads][head_dim],
         slices of a wider projection too) to their slots."""
-        c = self.cfg
-        n = slots.numel()
-        _ints(slots, n, self.device, "slots")
-        ks = _tokens(k, n, c.kv_heads, c.head_dim, self.dtype, self.device, "k")
-        vs = _tokens(v, n, c.kv_heads, c.head_dim, self.dtype, self.device, "v")
-        _r.rssm_attn_append(self.handle, n, k, ks, v, vs, slots, stream)
+        key = (_sig(k), _sig(v), _sig(slots))
+        seen = self._seen.get(key)
+        if seen is None:
+            c, n = self.cfg, slots.numel()
+            _ints(slots, n, self.device, "slots")
+            seen = _keep(self._seen, key, (n, _tokens(k, n, c.kv_heads, c.head_dim, self.dtype, self.device, "k"),
+                                           _tokens(v, n, c.kv_heads, c.head_dim, self.dtype, self.device, "v")))
+        st = self._fn.rssm_attn_append(self.handle, seen[0], k.data_ptr(), seen[1], v.data_ptr(), seen[2],
+                                       slots.data_ptr(), _stream_of(stream, self.device.index))
+        if st:
+            _r._check("rssm_attn_append", st)
 
     def decode(self, out, q, lens, table, T=1, lse=None, stream=None):
         """The attention of T new tokens a request: q and out
         [batch][T][q_heads][head_dim] (q may be a slice of a wider projection)."""
+        key = (T, _sig(out), _sig(q), _sig(lens), _sig(table), _sig(lse))
+        step = self._seen.get(key)
+        if step is None:
+            step = _keep(self._seen, key, self._check_decode(out, q, lens, table, T, lse))
+        st = self._fn.rssm_attn_decode(self.handle, T, q.data_ptr(), step, lens.data_ptr(), table.data_ptr(),
+                                       out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                       _stream_of(stream, self.device.index))
+        if st:
+            _r._check("rssm_attn_decode", st)
+
+    def _check_decode(self, out, q, lens, table, T, lse):
         torch = _torch()
         c = self.cfg
         n = c.batch * T
-        qs = _tokens(q, n, c.q_heads, c.head_dim, self.dtype, self.device, "q")
+        step = _tokens(q, n, c.q_heads, c.head_dim, self.dtype, self.device, "q")
         _ints(lens, c.batch, self.device, "lens")
         _ints(table, c.batch * c.max_pages, self.device, "table")
         _on(out, self.device, "out")
@@ -227,7 +312,7 @@ class Attention:
             _on(lse, self.device, "lse")
             _need(lse.dtype == torch.float32 and lse.numel() == n * c.q_heads and lse.is_contiguous(),
                   f"lse: must be a dense float32 [{c.batch}][{T}][{c.q_heads}]")
-        _r.rssm_attn_decode(self.handle, T, q, qs, lens, table, out, lse, stream)
+        return step
 
     def get_error(self, stream=None):
         return _r.rssm_attn_get_error(self.handle, stream)
@@ -246,9 +331,16 @@ def _rows(t, rows, dim, device, name):
     return dim
 
 
+def _by_ref(cfg):
+    return _r.ctypes.byref(cfg)
+
+
 def _weights(w, n, device, name):
     _on(w, device, name)
     _need(w.dtype == _torch().float32 and w.numel() == n and w.is_contiguous(), f"{name}: must be {n} dense float32")
+
+
+_add_seen: dict = {}
 
 
 def add_norm(n_out, u, w, x=None, u_out=None, w_post=None, gate=None, scale=1.0, eps=1e-6, w_offset=0.0, stream=None):
@@ -258,6 +350,21 @@ def add_norm(n_out, u, w, x=None, u_out=None, w_post=None, gate=None, scale=1.0,
     such type; gate may be [dim], the same for all rows; w, w_post float32
     [dim]. u_out may be u, n_out may be x; u_out or n_out may be None.
     """
+    key = (_sig(u), _sig(n_out), _sig(w), _sig(x), _sig(u_out), _sig(w_post), _sig(gate), scale, eps, w_offset)
+    cfg = _add_seen.get(key)
+    if cfg is None:
+        cfg = _keep(_add_seen, key, _check_add(n_out, u, w, x, u_out, w_post, gate, scale, eps, w_offset))
+    st = _lib.rssm_add_norm(cfg, u.data_ptr(), None if x is None else x.data_ptr(),
+                            None if w_post is None else w_post.data_ptr(), None if gate is None else gate.data_ptr(),
+                            None if w is None else w.data_ptr(), None if u_out is None else u_out.data_ptr(),
+                            None if n_out is None else n_out.data_ptr(), _stream_of(stream, u.get_device()))
+    if st:
+        _r._check("rssm_add_norm", st)
+
+
+def _check_add(n_out, u, w, x, u_out, w_post, gate, scale, eps, w_offset):
+    """The configuration struct of add_norm, by reference."""
+    _bind()
     dim = u.shape[-1]
     rows = u.numel() // dim if dim else 0
     dev = u.device
@@ -285,7 +392,10 @@ def add_norm(n_out, u, w, x=None, u_out=None, w_post=None, gate=None, scale=1.0,
     for t, name in ((w, "w"), (w_post, "w_post")):
         if t is not None:
             _weights(t, dim, dev, name)
-    _r.rssm_add_norm(cfg, u, x, w_post, gate, w, u_out, n_out, stream)
+    return _by_ref(cfg)
+
+
+_gated_seen: dict = {}
 
 
 def gated_norm(out, y, z, w, group=None, norm_first=False, act="silu", eps=1e-6, w_offset=0.0, stream=None):
@@ -296,6 +406,19 @@ def gated_norm(out, y, z, w, group=None, norm_first=False, act="silu", eps=1e-6,
     block, one group per head). y, z, out [rows][dim] of one type; w float32
     [dim] or [group]. out may be y.
     """
+    key = (_sig(y), _sig(z), _sig(out), _sig(w), group, norm_first, act, eps, w_offset)
+    cfg = _gated_seen.get(key)
+    if cfg is None:
+        cfg = _keep(_gated_seen, key, _check_gated(out, y, z, w, group, norm_first, act, eps, w_offset))
+    st = _lib.rssm_gated_norm(cfg, y.data_ptr(), z.data_ptr(), w.data_ptr(), out.data_ptr(),
+                              _stream_of(stream, y.get_device()))
+    if st:
+        _r._check("rssm_gated_norm", st)
+
+
+def _check_gated(out, y, z, w, group, norm_first, act, eps, w_offset):
+    """The configuration struct of gated_norm, by reference."""
+    _bind()
     dim = y.shape[-1]
     rows = y.numel() // dim if dim else 0
     dev = y.device
@@ -308,4 +431,4 @@ def gated_norm(out, y, z, w, group=None, norm_first=False, act="silu", eps=1e-6,
     cfg = _r.GatedNormConfig(rows=rows, dim=dim, group=group, w_dim=w.numel(), dtype=d, norm_first=int(norm_first),
                              act=_r.GATE[act], eps=eps, w_offset=w_offset, y_stride=_rows(y, rows, dim, dev, "y"),
                              z_stride=_rows(z, rows, dim, dev, "z"), out_stride=_rows(out, rows, dim, dev, "out"))
-    _r.rssm_gated_norm(cfg, y, z, w, out, stream)
+    return _by_ref(cfg)
