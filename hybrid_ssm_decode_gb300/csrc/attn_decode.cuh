@@ -64,13 +64,21 @@ struct Shape {
     // Two blocks per SM where the registers allow it: one block's joins then
     // overlap the other's stream.
     static constexpr int kMinBlocks = (WM == 1 && D <= 128) ? 2 : 1;
-    static constexpr int kFixed = 2 * kRows * QS + kRows * OS * 4 + NT * kRows * 8 + kRows * 8 + 512;
     static constexpr int kBudget = (kMinBlocks == 2 ? 113 : 226) * 1024 - 1024;
+    // Buffers in which the warps of a row leave their outputs at the end of a
+    // part: one each where the ring keeps eight slots beside them, else one that
+    // they add to in turn.
+    static constexpr int fixed_bytes(int nb) {
+        return 2 * kRows * QS + nb * kRows * OS * 4 + NT * kRows * 8 + kRows * 8 + 512;
+    }
+    static constexpr int NB = (kBudget - fixed_bytes(NT)) / kSlot >= 8 ? NT : 1;
+    static constexpr int kFixed = fixed_bytes(NB);
     static constexpr int kSlotsFit = (kBudget - kFixed) / kSlot;
     // A multiple of NT, so that a slot always belongs to the same warp of each
     // row group: a warp then never waits for a turn of a slot before it has seen
     // the turn before, which the parity of the slot's barrier could not tell apart.
     static constexpr int NS = (kSlotsFit > 24 ? 24 : kSlotsFit) / NT * NT;
+    static constexpr int PB = NS >= 16 ? 8 : NS >= 8 ? 4 : NS >= 4 ? 2 : 1;   // groups the producer copies at a time
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
     static_assert(NS >= NT && NS % NT == 0, "ring too small");
 };
@@ -85,17 +93,17 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -319,23 +327,32 @@ struct Warp {
         uint32_t b[4];
         if constexpr (KV == kBF16) {
             const int r = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+            float s2[2][4] = {};                               // two chains a score: half the latency
 #pragma unroll
-            for (int i = 0; i < kQRegs; ++i) {
+            for (int i = 0; i < kQRegs; i += 2) {
+                uint32_t b2[4];
                 ldsm4(b, k + swz<S>(r, 2 * i + ch));
+                ldsm4(b2, k + swz<S>(r, 2 * i + 2 + ch));
                 mma_bf16(s[0], qf[i], b[0], b[1]);
                 mma_bf16(s[1], qf[i], b[2], b[3]);
+                mma_bf16(s2[0], qf[i + 1], b2[0], b2[1]);
+                mma_bf16(s2[1], qf[i + 1], b2[2], b2[3]);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[0][j] += s2[0][j], s[1][j] += s2[1][j];
         } else if constexpr (KV == kFP8) {
             const int r = lane & 15, ch = lane >> 4;         // tokens 0-7, 8-15 of one chunk, then of the next
+            float s2[2][4] = {};
 #pragma unroll
             for (int i = 0; i < kQRegs; i += 2) {
                 ldsm4(b, k + swz<S>(r, i + ch));
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    mma_f16(s[0], qf[i + j], e4m3x2_to_h2(b[2 * j]), e4m3x2_to_h2(b[2 * j] >> 16));
-                    mma_f16(s[1], qf[i + j], e4m3x2_to_h2(b[2 * j + 1]), e4m3x2_to_h2(b[2 * j + 1] >> 16));
-                }
+                mma_f16(s[0], qf[i], e4m3x2_to_h2(b[0]), e4m3x2_to_h2(b[0] >> 16));
+                mma_f16(s[1], qf[i], e4m3x2_to_h2(b[1]), e4m3x2_to_h2(b[1] >> 16));
+                mma_f16(s2[0], qf[i + 1], e4m3x2_to_h2(b[2]), e4m3x2_to_h2(b[2] >> 16));
+                mma_f16(s2[1], qf[i + 1], e4m3x2_to_h2(b[3]), e4m3x2_to_h2(b[3] >> 16));
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[0][j] += s2[0][j], s[1][j] += s2[1][j];
         } else {
             // The tensor cores cut their sums off below FP32's last bit, always
             // towards zero, so chains are kept short: the leading products of 32
@@ -556,7 +573,21 @@ struct Warp {
         }
         const Weights w = weights(s);
         if (!kMasked) {
-            each_value(vb, [&](int t, int h, uint32_t b0, uint32_t b1) { product(o[t], w, h, b0, b1); });
+            if constexpr (KV == kBF16) {
+                // four tiles' first terms, then their second ones: no product waits for its neighbour
+#pragma unroll
+                for (int i = 0; i < kTiles; i += 4) {
+                    uint32_t v[2][4];
+                    values(vb, i / 2, 0, v[0]);
+                    values(vb, i / 2 + 1, 0, v[1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_bf16(o[i + j], w.hi[0], v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_bf16(o[i + j], w.lo[0], v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
+                }
+            } else {
+                each_value(vb, [&](int t, int h, uint32_t b0, uint32_t b1) { product(o[t], w, h, b0, b1); });
+            }
             return;
         }
         bool bad = false;
@@ -603,8 +634,8 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
     char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     char* slots = smem;
     char* qbuf = slots + NS * S::kSlot;                                  // [2][kRows][QS]
-    float* merged = reinterpret_cast<float*>(qbuf + 2 * S::kRows * S::QS);   // [kRows][OS]
-    float2* s_ml = reinterpret_cast<float2*>(merged + S::kRows * S::OS); // [NT][kRows]
+    float* merged = reinterpret_cast<float*>(qbuf + 2 * S::kRows * S::QS);   // [NB][kRows][OS]
+    float2* s_ml = reinterpret_cast<float2*>(merged + S::NB * S::kRows * S::OS);   // [NT][kRows]
     float2* s_row = s_ml + S::NT * S::kRows;                             // [kRows]
     uint64_t* full = reinterpret_cast<uint64_t*>(s_row + S::kRows);      // [NS]
     uint64_t* empty = full + NS;
@@ -631,7 +662,7 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
     __syncthreads();
 
     const int rows_all = a.T * a.group;
-    int64_t gi = 0;            // groups of the share so far, in order
+    int pos = 0, turn = 0;     // ring: the next group's slot, and how often the ring went round
     int parts = 0;
 
     if (warp == S::kConsumers) {
@@ -656,38 +687,55 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
             }
             ++parts;
             const int g0 = cur.first_group(), g1 = cur.end_group();
+            // pages of 32 groups at a time, a step ahead; copies of PB groups at a time, a lane each
+            const auto look_up = [&](int base, int& page, int& row) {
+                page = a.num_pages;                      // outside the map: read as zeros
+                row = 0;
+                if (base + lane >= g1) return;
+                const int tok = (base + lane) * kAttnGroup;
+                const int at = tok / a.page_size;
+                row = tok - at * a.page_size;
+                page = __ldg(a.table + static_cast<int64_t>(cur.b) * a.max_pages + at);
+            };
+            int page, row, next_page, next_row;
+            look_up(g0, next_page, next_row);
             for (int base = g0; base < g1; base += 32) {
-                int page = 0, row = 0;
-                if (base + lane < g1) {
-                    const int tok = (base + lane) * kAttnGroup;
-                    const int at = tok / a.page_size;
-                    row = tok - at * a.page_size;
-                    page = __ldg(a.table + static_cast<int64_t>(cur.b) * a.max_pages + at);
-                    if (page < 0 || page >= a.num_pages) {
-                        report_error(a.err, RSSM_DEV_ATTN_PAGE, cur.b, page);
-                        page = a.num_pages;              // outside the map: read as zeros
-                    }
+                page = next_page;
+                row = next_row;
+                look_up(base + 32, next_page, next_row);
+                if (page < 0 || page > a.num_pages || (page == a.num_pages && base + lane < g1)) {
+                    report_error(a.err, RSSM_DEV_ATTN_PAGE, cur.b, page);
+                    page = a.num_pages;
                 }
                 const int n = min(32, g1 - base);
-                for (int i = 0; i < n; ++i, ++gi) {
-                    if (lane == i) {
-                        const int s = static_cast<int>(gi % NS);
-                        const int64_t turn = gi / NS;
-                        if ((turn == 0 || wait_phase(empty + s, (turn - 1) & 1, dead, a.err)) && !*dead) {
+                for (int i = 0; i < n; i += S::PB) {
+                    const int m = min(S::PB, n - i);
+                    const int pg = __shfl_sync(0xffffffffu, page, (i + lane) & 31), rw = __shfl_sync(0xffffffffu, row, (i + lane) & 31);
+                    if (lane < m) {
+                        const bool wrap = pos + lane >= NS;
+                        const int s = pos + lane - (wrap ? NS : 0), tn = turn + (wrap ? 1 : 0);
+                        if ((tn == 0 || wait_phase(empty + s, (tn - 1) & 1, dead, a.err)) && !*dead) {
                             const uint32_t dst = smem_u32(slots + s * S::kSlot);
                             mbar_arrive_expect_tx(full + s, S::kSlot);
-                            tma_load_5d(dst, &kmap, row, head, page, full + s);
-                            tma_load_5d(dst + S::kHalf, &vmap, row, head, page, full + s);
+                            tma_load_5d(dst, &kmap, rw, head, pg, full + s);
+                            tma_load_5d(dst + S::kHalf, &vmap, rw, head, pg, full + s);
                         }
                     }
                     __syncwarp();
+                    pos += m;
+                    if (pos >= NS) {
+                        pos -= NS;
+                        ++turn;
+                    }
                 }
             }
         }
         if (*dead && lane == 0) {
             // let the copies in flight land before the block's memory goes
-            for (int64_t i = max(static_cast<int64_t>(0), gi - NS); i < gi; ++i)
-                mbar_wait_bounded(full + i % NS, (i / NS) & 1, kWaitLimitNs / 16);
+            for (int s = 0; s < NS; ++s) {
+                const int tn = s < pos ? turn : turn - 1;   // the slot's last turn, if it had one
+                if (tn >= 0) mbar_wait_bounded(full + s, tn & 1, kWaitLimitNs / 16);
+            }
             for (int i = max(0, parts - 2); i < parts; ++i)
                 mbar_wait_bounded(qfull + (i & 1), (i >> 1) & 1, kWaitLimitNs / 16);
         }
@@ -730,12 +778,17 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
             if (lane == 0) mbar_arrive(qempty + pq);
         }
         const int g0 = cur.first_group(), g1 = cur.end_group();
-        // this warp's groups: those whose running index is wt modulo NT
-        int64_t i = gi + ((wt - gi) % S::NT + S::NT) % S::NT;
-        for (; i < gi + (g1 - g0); i += S::NT) {
-            const int s = static_cast<int>(i % NS);
-            ok = wait_phase(full + s, (i / NS) & 1, dead, a.err);
-            const int tok = (g0 + static_cast<int>(i - gi)) * kAttnGroup;
+        // this warp's groups: those whose slot is wt modulo NT
+        const int ng = g1 - g0;
+        int k = (wt + S::NT - pos % S::NT) % S::NT;
+        int s = pos + k, tn = turn;
+        for (; k < ng; k += S::NT, s += S::NT) {
+            if (s >= NS) {
+                s -= NS;
+                ++tn;
+            }
+            ok = wait_phase(full + s, tn & 1, dead, a.err);
+            const int tok = (g0 + k) * kAttnGroup;
             const uint32_t kb = smem_u32(slots + s * S::kSlot), vb = kb + S::kHalf;
             if (ok) {
                 const int lo[2] = {see_lo[0] - tok, see_lo[1] - tok}, hi[2] = {see_hi[0] - tok, see_hi[1] - tok};
@@ -747,7 +800,9 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + s);
         }
-        gi += g1 - g0;
+        pos += ng;
+        turn += pos / NS;
+        pos %= NS;
         if (KV == kF32) {
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty + pq);
@@ -775,19 +830,30 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
             f[x] = ex2(wp.m[x] - ref);
             if (wt == 0 && wp.c == 0) s_row[r] = make_float2(M, L);
         }
-        for (int w = 0; w < S::NT; ++w) {
-            if (w == wt) {
+        // warp w into buffer w % NB, those of later rounds adding to it
+#pragma unroll 1
+        for (int w = 0; w < S::NT; w += S::NB) {
+            if (wt >= w && wt < w + S::NB) {
 #pragma unroll
                 for (int i2 = 0; i2 < Warp<KV, S>::kTiles; ++i2)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float* d = merged + (wm * 16 + wp.g + 8 * (j >> 1)) * S::OS + wp.column(i2, j & 1);
+                        float* d = merged + ((wt - w) * S::kRows + wm * 16 + wp.g + 8 * (j >> 1)) * S::OS + wp.column(i2, j & 1);
                         const float v = wp.o[i2][j] * f[j >> 1];
                         *d = w == 0 ? v : *d + v;
                     }
             }
             named_sync(1, kThreads);
         }
+        const auto sum_of = [&](int r, int col) {
+            float4 v = *reinterpret_cast<const float4*>(merged + r * S::OS + col);
+#pragma unroll
+            for (int w = 1; w < S::NB; ++w) {
+                const float4 x = *reinterpret_cast<const float4*>(merged + (w * S::kRows + r) * S::OS + col);
+                v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+            }
+            return v;
+        };
         const bool whole = cur.u0 == 0 && cur.u1 == cur.sp.units;
         const float vscale = KV == kFP8 ? __ldg(a.v_scale + head) : 1.f;
         const auto put = [&](int r, int col, float4 v, float M, float L) {
@@ -807,7 +873,7 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
         if (whole) {
             for (int x = tid; x < rows * (D / 4); x += kThreads) {
                 const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-                put(r, col, *reinterpret_cast<const float4*>(merged + r * S::OS + col), s_row[r].x, s_row[r].y);
+                put(r, col, sum_of(r, col), s_row[r].x, s_row[r].y);
             }
             continue;
         }
@@ -815,8 +881,7 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (cur.u0 == 0 ? 1 : 0);
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
             const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-            __stcg(reinterpret_cast<float4*>(a.part_o + (slot * S::kRows + r) * D + col),
-                   *reinterpret_cast<const float4*>(merged + r * S::OS + col));
+            __stcg(reinterpret_cast<float4*>(a.part_o + (slot * S::kRows + r) * D + col), sum_of(r, col));
             if (col == 0) __stcg(a.part_ml + slot * S::kRows + r, s_row[r]);
         }
         __threadfence();
