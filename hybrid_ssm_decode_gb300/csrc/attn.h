@@ -22,8 +22,8 @@ struct AttnArgs {
     const float* v_scale;
     int32_t* err;
     uint32_t* arrived;          // [B][kv_heads][chunks], 0 between launches
-    float2* part_ml;            // [2 grid][rows]: maximum and sum of a part
-    float* part_o;              // [2 grid][rows][D]
+    float2* part_ml;            // [2 blocks][rows]: maximum and sum of a part
+    float* part_o;              // [2 blocks][rows][D]
     int B, q_heads, kv_heads, group, T, chunks;   // chunks: of the T*group query rows, per cache head
     int page_size, num_pages, max_pages, window;
     float scale_log2;           // softmax scale times log2(e)

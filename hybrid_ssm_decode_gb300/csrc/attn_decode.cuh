@@ -12,15 +12,20 @@
 // to 64 rows the cache's bytes bound it, and the question is only that every SM
 // streams all the time, whatever the requests' lengths. The work of the launch is
 // laid out as one line of units (request, cache head, 64 tokens) and cut into
-// equal shares, one per block. A block's share may begin and end inside a
-// request; those at most two parts go to the workspace, and the last of a
-// request's blocks to arrive joins them in the order of the tokens (no float
-// atomics: reruns give the same bits).
+// equal shares, one per block. A share may begin and end inside a request; those
+// at most two parts go to the workspace, and the last of a request's parts to
+// arrive joins them in the order of the tokens (no float atomics: reruns give the
+// same bits). SMs do not all see the same bandwidth: with equal shares the blocks
+// of a launch end within 5 to 14 % of their mean. Small shares taken in turn from
+// the last sixth of the line lost more to the joins than they evened out (BF16,
+// 64 requests of 1000 to 9999 tokens, 32 rows of 256: 194 -> 258 us; FP8, 8
+// requests of 128k: 318 -> 362 us).
 //
-// The block. One producer warp looks pages up and copies groups of 16 tokens (K
-// and V, one 5-D TMA box each, swizzled so that fragment loads meet no bank
-// twice) into a ring of slots; a box never leaves a page, because a page is a
-// multiple of 16 tokens. The consumer warps take groups in turn, each with its
+// The block. One producer warp walks the shares, looks pages up and copies groups
+// of 16 tokens (K and V, one 5-D TMA box each, swizzled so that fragment loads
+// meet no bank twice) into a ring of slots; a box never leaves a page, because a
+// page is a multiple of 16 tokens. With a part's query rows it leaves a
+// description of the part in shared memory, two parts ahead. The consumer warps take groups in turn, each with its
 // own running (m, l, O) in registers, so that they meet only at the end of a
 // part. Groups whose tokens not all rows see (the request's end, the drafts, the
 // window's start) take a masked path: scores by selection, values of unseen
@@ -78,10 +83,19 @@ struct Shape {
     // row group: a warp then never waits for a turn of a slot before it has seen
     // the turn before, which the parity of the slot's barrier could not tell apart.
     static constexpr int NS = (kSlotsFit > 24 ? 24 : kSlotsFit) / NT * NT;
+    // Consumers take two groups at a time: heads of 64, whose products are few
+    // beside the softmax. (At 128 the second group's scores cost registers that the
+    // loop needs: 392 -> 422 us over 256 BF16 requests of up to 4500 tokens.)
+    static constexpr bool kPair = KV != kF32 && D == 64;
     static constexpr int PB = NS >= 16 ? 8 : NS >= 8 ? 4 : NS >= 4 ? 2 : 1;   // groups the producer copies at a time
+    // A warp with a pair's first group in hand waits for the one NT further on,
+    // which must not be in a batch that waits for the first one's slot.
+    static_assert(!kPair || NS - NT >= PB, "a pair of groups must fit the ring");
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
     static_assert(NS >= NT && NS % NT == 0, "ring too small");
 };
+
+template <int N> struct Int { static constexpr int value = N; };
 
 // ---- instructions -----------------------------------------------------------
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -146,6 +160,26 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 // 2^n for n in [-126, 127].
 __device__ __forceinline__ float pow2(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
 
+// Count one arrival; orders the block's writes before it (they are behind a block
+// barrier) and the reads that follow the last arrival after it.
+__device__ __forceinline__ uint32_t arrive_gpu(uint32_t* n) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(n) : "memory");
+    return old;
+}
+
+// Whether `ok` holds for every thread at the named barrier.
+__device__ __forceinline__ bool all_of(bool ok, int id, int nthreads) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %2, %3, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(static_cast<int>(ok)), "r"(id), "r"(nthreads) : "memory");
+    return r != 0;
+}
+
 // Wait for a phase, for at most kWaitLimitNs; false once any warp of the block
 // has given up (the block then only runs its loops out).
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* err) {
@@ -179,18 +213,19 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
     return s;
 }
 
-// Walks the parts of a block's share. Every warp keeps its own copy.
+// Walks the parts of the block's share; one warp.
 struct Cursor {
-    int64_t total, w, w1, base;   // units: in all, next, end, before request b
+    int64_t total, w, w1, base;  // units: in all, next, end, before request b
     int grid, b;
     Span sp;
-    // the current part
-    int pair, u0, u1;
+    int pair, u0, u1;            // the current part
+    bool fresh;
 
-    __device__ __forceinline__ void start(const AttnArgs& a, int lane) {
-        const int heads = a.kv_heads * a.chunks;
-        const int per = (a.B + 31) / 32;
-        int64_t mine = 0;
+    // False for a block without a share.
+    __device__ __forceinline__ bool start(const AttnArgs& a, int lane) {
+        const int heads = a.kv_heads * a.chunks, per = (a.B + 31) / 32;
+        int64_t mine = 0;                     // units of this lane's requests, of one cache head
+#pragma unroll 4
         for (int i = 0; i < per; ++i) {
             const int r = lane * per + i;
             if (r < a.B) mine += span_of(a, r).units;
@@ -204,49 +239,71 @@ struct Cursor {
         total = __shfl_sync(0xffffffffu, incl, 31) * heads;
         grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
         const int c = blockIdx.x;
-        if (c >= grid) {
-            w = w1 = 0;
-            return;
-        }
+        if (c >= grid) return false;
         w = total * c / grid;
         w1 = total * (c + 1) / grid;
-        // the lane whose requests hold unit w, then the request
+        // the lane whose requests hold the first unit, then the request
         const int64_t excl = (incl - mine) * heads;
-        const unsigned has = __ballot_sync(0xffffffffu, mine > 0 && excl <= w);
-        const int src = 31 - __clz(has);
-        int rb = lane * per;
-        int64_t at = excl;
-        if (lane == src) {
-            for (;;) {
-                const int64_t n = static_cast<int64_t>(span_of(a, rb).units) * heads;
-                if (at + n > w) break;
-                at += n;
-                ++rb;
+        const int src = 31 - __clz(__ballot_sync(0xffffffffu, mine > 0 && excl <= w));
+        base = __shfl_sync(0xffffffffu, excl, src);
+        b = src * per;
+        for (int i0 = 0; i0 < per; i0 += 32) {
+            const int r = src * per + i0 + lane;
+            const int64_t n = (i0 + lane < per && r < a.B) ? static_cast<int64_t>(span_of(a, r).units) * heads : 0;
+            int64_t upto = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
             }
+            const unsigned past = __ballot_sync(0xffffffffu, base + upto > w);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                b = src * per + i0 + l;
+                base += __shfl_sync(0xffffffffu, upto - n, l);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, upto, 31);
         }
-        b = __shfl_sync(0xffffffffu, rb, src);
-        base = __shfl_sync(0xffffffffu, at, src);
         sp = span_of(a, b);
+        fresh = true;
+        return true;
     }
-    // The next part of the share; false at its end.
+    // The block whose share holds unit x: the last c with total c / grid <= x.
+    __device__ __forceinline__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * grid - 1) / total); }
+    // The next part of the share; false at its end. Parts after the first begin
+    // with a request's first unit.
     __device__ __forceinline__ bool next(const AttnArgs& a) {
         if (w >= w1) return false;
-        const int heads = a.kv_heads * a.chunks;
-        if (w - base >= static_cast<int64_t>(sp.units) * heads) {
-            base += static_cast<int64_t>(sp.units) * heads;
-            sp = span_of(a, ++b);
+        if (fresh) {
+            const int64_t r = w - base;
+            pair = static_cast<int>(r / sp.units);
+            u0 = static_cast<int>(r - static_cast<int64_t>(pair) * sp.units);
+            fresh = false;
+        } else {
+            u0 = 0;
+            if (++pair == a.kv_heads * a.chunks) {
+                pair = 0;
+                base += static_cast<int64_t>(sp.units) * a.kv_heads * a.chunks;
+                sp = span_of(a, ++b);
+            }
         }
-        const int64_t r = w - base;
-        pair = static_cast<int>(r / sp.units);
-        u0 = static_cast<int>(r - static_cast<int64_t>(pair) * sp.units);
         u1 = static_cast<int>(min(static_cast<int64_t>(sp.units), u0 + (w1 - w)));
         w += u1 - u0;
         return true;
     }
     __device__ __forceinline__ int first_group() const { return sp.g0 + u0 * kAttnUnit; }
     __device__ __forceinline__ int end_group() const { return min(sp.g1, sp.g0 + u1 * kAttnUnit); }
-    // The block whose share holds unit x of the launch.
-    __device__ __forceinline__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * grid - 1) / total); }
+};
+
+// A part as the producer describes it to the consumers.
+struct Part {
+    int b, len, head, row0;      // request, its length, cache head, first query row
+    int g0, ng;                  // groups of 16 tokens
+    int pair;                    // -1: no more parts
+    int first;                   // block of the request's first part
+    int others;                  // parts of the request and head beside this one
+    int at_start;                // the part begins with the request's first unit
 };
 
 // ---- one warp's products -----------------------------------------------------
@@ -447,9 +504,8 @@ struct Warp {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {                     // tokens 0-7, 8-15
-                const uint32_t x = e4m3x2_to_h2(r[2 * j + k]), y = e4m3x2_to_h2(r[2 * j + k] >> 16);
-                v[j][k] = __byte_perm(x, y, 0x5410);
-                v[j][2 + k] = __byte_perm(x, y, 0x7632);
+                v[j][k] = e4m3x2_to_h2(__byte_perm(r[2 * j + k], 0, 0x4420));
+                v[j][2 + k] = e4m3x2_to_h2(__byte_perm(r[2 * j + k], 0, 0x4431));
             }
     }
 
@@ -516,32 +572,19 @@ struct Warp {
         return (((v & e) + one) & 0x80008000u) != 0;
     }
 
-    // Running maximum, sum and outputs over one group. Rows g and g + 8 see the
-    // tokens lo[x]..hi[x] of it (0..15); with kMasked false, all rows see all.
-    // any_lo..any_hi: the tokens that some row of the block sees. first[t]..: see below.
-    template <bool kMasked>
-    __device__ __forceinline__ void step(uint32_t kb, uint32_t vb, const int (&lo)[2], const int (&hi)[2], int any_lo,
-                                         int any_hi, int T, int tok0, int len, int window, const int (&draft)[2]) {
-        float s[2][4];
-        scores(kb, s);
-        float mx[2] = {-INFINITY, -INFINITY};
+    // Running maximum and sum over the scores of 8 N tokens, which become their
+    // weights; the outputs so far are rescaled where the maximum grew.
+    template <int N>
+    __device__ __forceinline__ void softmax(float (&s)[N][4]) {
+        float mx[2] = {m[0], m[1]};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int x = j >> 1;
-                s[i][j] *= mul[x];
-                if (kMasked) {
-                    const int t = 8 * i + 2 * c + (j & 1);
-                    if (t < lo[x] || t > hi[x]) s[i][j] = -INFINITY;
-                }
-                mx[x] = fmaxf(mx[x], s[i][j]);
-            }
+            for (int j = 0; j < 4; ++j) mx[j >> 1] = fmaxf(mx[j >> 1], s[i][j]);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
             mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
-            mx[x] = fmaxf(mx[x], m[x]);
         }
         if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
             float f[2];
@@ -559,37 +602,68 @@ struct Warp {
                 o[i][3] *= f[1];
             }
         }
+        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const float ref = m[x] == -INFINITY ? 0.f : m[x];
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float& p = s[i][2 * x + j];
-                    p = ex2(p - ref);
-                    l[x] += p;
-                }
-        }
-        const Weights w = weights(s);
-        if (!kMasked) {
-            if constexpr (KV == kBF16) {
-                // four tiles' first terms, then their second ones: no product waits for its neighbour
-#pragma unroll
-                for (int i = 0; i < kTiles; i += 4) {
-                    uint32_t v[2][4];
-                    values(vb, i / 2, 0, v[0]);
-                    values(vb, i / 2 + 1, 0, v[1]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_bf16(o[i + j], w.hi[0], v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_bf16(o[i + j], w.lo[0], v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
-                }
-            } else {
-                each_value(vb, [&](int t, int h, uint32_t b0, uint32_t b1) { product(o[t], w, h, b0, b1); });
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = ex2(s[i][j] - ref[j >> 1]);
+                sum[j >> 1] += s[i][j];
             }
-            return;
+        l[0] += sum[0];
+        l[1] += sum[1];
+    }
+
+    // o += weights V of one group.
+    __device__ __forceinline__ void accumulate(uint32_t vb, const Weights& w) {
+        if constexpr (KV == kBF16) {
+            // four tiles' first terms, then their second ones: no product waits for its neighbour
+#pragma unroll
+            for (int i = 0; i < kTiles; i += 4) {
+                uint32_t v[2][4];
+                values(vb, i / 2, 0, v[0]);
+                values(vb, i / 2 + 1, 0, v[1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_bf16(o[i + j], w.hi[0], v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_bf16(o[i + j], w.lo[0], v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
+            }
+        } else {
+            each_value(vb, [&](int t, int h, uint32_t b0, uint32_t b1) { product(o[t], w, h, b0, b1); });
         }
+    }
+
+    // NG groups whose tokens all rows see.
+    template <int NG>
+    __device__ __forceinline__ void step(const uint32_t (&kb)[NG], const uint32_t (&vb)[NG]) {
+        float s[2 * NG][4];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) scores(kb[n], *reinterpret_cast<float(*)[2][4]>(&s[2 * n]));
+#pragma unroll
+        for (int i = 0; i < 2 * NG; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] *= mul[j >> 1];
+        softmax(s);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) accumulate(vb[n], weights(*reinterpret_cast<float(*)[2][4]>(&s[2 * n])));
+    }
+
+    // One group of which rows g and g + 8 see the tokens lo[x]..hi[x] (0..15) and
+    // some row of the block any_lo..any_hi; tok0 is its first token's position.
+    __device__ __forceinline__ void step_masked(uint32_t kb, uint32_t vb, const int (&lo)[2], const int (&hi)[2], int any_lo,
+                                                int any_hi, int T, int tok0, int len, int window, const int (&draft)[2]) {
+        float s[2][4];
+        scores(kb, s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int x = j >> 1, t = 8 * i + 2 * c + (j & 1);
+                s[i][j] = (t < lo[x] || t > hi[x]) ? -INFINITY : s[i][j] * mul[x];
+            }
+        softmax(s);
+        const Weights w = weights(s);
         bool bad = false;
         if (T > 1) {
             each_value(vb, [&](int, int h, uint32_t b0, uint32_t b1) {
@@ -618,17 +692,132 @@ struct Warp {
         }
     }
 
-    // Column of o[tile][j] (0, 1: of row g; 2, 3: of row g + 8).
-    __device__ __forceinline__ int column(int tile, int j) const {
-        if constexpr (KV == kFP8) return (tile >> 1) * 16 + 4 * c + 2 * j + (tile & 1);
-        return tile * 8 + 2 * c + j;
+    // The outputs times f[row] to rows g and g + 8 of a buffer (`to`: row g), or
+    // added to what is there.
+    template <bool kAdd>
+    __device__ __forceinline__ void leave(float* to, const float (&f)[2]) const {
+#pragma unroll
+        for (int i = 0; i < kTiles; i += 2)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float* d = to + 8 * x * S::OS;
+                const float a0 = o[i][2 * x] * f[x], a1 = o[i][2 * x + 1] * f[x];
+                const float b0 = o[i + 1][2 * x] * f[x], b1 = o[i + 1][2 * x + 1] * f[x];
+                if constexpr (KV == kFP8) {                   // tiles of even and of odd columns
+                    float4* p = reinterpret_cast<float4*>(d + 8 * i + 4 * c);
+                    float4 v = make_float4(a0, b0, a1, b1);
+                    if (kAdd) v.x += p->x, v.y += p->y, v.z += p->z, v.w += p->w;
+                    *p = v;
+                } else {
+                    float2 *p = reinterpret_cast<float2*>(d + 8 * i + 2 * c), *q = p + 4;
+                    float2 v = make_float2(a0, a1), u = make_float2(b0, b1);
+                    if (kAdd) v.x += p->x, v.y += p->y, u.x += q->x, u.y += q->y;
+                    *p = v;
+                    *q = u;
+                }
+            }
     }
 };
+
+// Outputs of row r of a part, columns col..col + 3, from the sums v under maximum
+// M and total L.
+template <int KV, class S>
+__device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, int col, float4 v, float M, float L) {
+    const int t = (part.row0 + r) / a.group, j = (part.row0 + r) % a.group;
+    const int64_t at = (static_cast<int64_t>(part.b) * a.T + t) * a.q_heads + part.head * a.group + j;
+    const float inv = L == 0.f ? 0.f : (KV == kFP8 ? __ldg(a.v_scale + part.head) : 1.f) / L;
+    v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+    if (KV == kF32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * S::D + col) = v;
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * S::D + col) =
+            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    }
+    if (a.lse != nullptr && col == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+}
+
+// Join the parts of a request and head: the consumer warps, once all have
+// arrived. Not inlined: it runs once or twice a block, and its registers are
+// not the stream's.
+template <int KV, class S>
+__device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, float* fw, float2* s_row) {
+    // Weights of the parts first (parts across the lanes, a warp a row at a
+    // time), then the outputs, with no product waiting for another.
+    const int rows = min(S::kRows, a.T * a.group - part.row0);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int D = S::D, kThreads = S::kConsumers * 32;
+    const int np = part.others + 1;
+    const auto part_at = [&](int p, int r) {
+        return (2 * static_cast<int64_t>(part.first + p) + (p == 0 ? 1 : 0)) * S::kRows + r;
+    };
+    // fw: [np][rows]
+    const bool fits = np * rows <= S::NB * S::kRows * S::OS;
+    for (int r = warp; r < rows; r += S::kConsumers) {
+        float M = -INFINITY, L = 0.f;
+        for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(a.part_ml + part_at(p, r)).x);
+        M = warp_max(M);
+        const float ref = M == -INFINITY ? 0.f : M;
+        for (int p = lane; p < np; p += 32) {
+            const float2 ml = __ldcg(a.part_ml + part_at(p, r));
+            const float fp = ex2(ml.x - ref);
+            L += ml.y * fp;
+            if (fits) fw[p * rows + r] = fp;
+        }
+        L = warp_sum(L);
+        if (lane == 0) s_row[r] = make_float2(M, L);
+    }
+    named_sync(1, kThreads);
+    // 16 loads ahead: of one output where there is one a thread, else of four
+    const auto sums = [&](auto items_c, auto ahead_c) {
+        constexpr int kItems = decltype(items_c)::value, kAhead = decltype(ahead_c)::value;
+        const int items = rows * (D / 4);
+        for (int x0 = tid; x0 < items; x0 += kItems * kThreads) {
+            float4 acc[kItems];
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p0 = 0; p0 < np; p0 += kAhead) {
+                float4 v[kItems][kAhead];
+                float fp[kItems][kAhead];
+#pragma unroll
+                for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) {
+                        const int x = x0 + i * kThreads, p = p0 + k;
+                        v[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        fp[i][k] = 0.f;
+                        if (x >= items || p >= np) continue;
+                        const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+                        v[i][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + part_at(p, r) * D + col));
+                        const float M = s_row[r].x;
+                        fp[i][k] = fits ? fw[p * rows + r] : ex2(__ldcg(a.part_ml + part_at(p, r)).x - (M == -INFINITY ? 0.f : M));
+                    }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        acc[i].x = fmaf(v[i][k].x, fp[i][k], acc[i].x);
+                        acc[i].y = fmaf(v[i][k].y, fp[i][k], acc[i].y);
+                        acc[i].z = fmaf(v[i][k].z, fp[i][k], acc[i].z);
+                        acc[i].w = fmaf(v[i][k].w, fp[i][k], acc[i].w);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int x = x0 + i * kThreads;
+                if (x >= items) break;
+                const int r = x / (D / 4);
+                put<KV, S>(a, part, r, (x % (D / 4)) * 4, acc[i], s_row[r].x, s_row[r].y);
+            }
+        }
+    };
+    if (rows * (D / 4) <= kThreads) sums(Int<1>{}, Int<16>{});
+    else sums(Int<4>{}, Int<4>{});
+}
 
 // ---- the kernel --------------------------------------------------------------
 template <int KV, class S>
 __global__ void __launch_bounds__(S::kThreads, S::kMinBlocks)
-attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     constexpr int D = S::D, NS = S::NS;
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -643,6 +832,7 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
     uint64_t* qempty = qfull + 2;
     volatile int* dead = reinterpret_cast<volatile int*>(qempty + 2);
     volatile int* s_last = dead + 1;
+    Part* s_part = reinterpret_cast<Part*>(const_cast<int*>(dead + 2));  // [2]
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -657,8 +847,6 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
         *dead = 0;
         fence_mbar_init();
     }
-    Cursor cur;
-    cur.start(a, lane);
     __syncthreads();
 
     const int rows_all = a.T * a.group;
@@ -668,43 +856,73 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
     if (warp == S::kConsumers) {
         // ---- producer ----
         const uint32_t q_bytes = D * S::kQsz;
-        while (cur.next(a)) {
-            const int head = cur.pair / a.chunks, row0 = (cur.pair % a.chunks) * S::kRows;
-            const int rows = min(S::kRows, rows_all - row0);
+        Cursor cur;
+        // The next part is found, and its first pages are looked up, before the
+        // current one's copies go out: a part's start then costs no round trip.
+        Part d, nd;
+        int g1 = 0, ng1 = 0, next_page = 0, next_row = 0;
+        const auto look_up = [&](int b, int base, int end, int& page, int& row) {
+            page = a.num_pages;                          // outside the map: read as zeros
+            row = 0;
+            if (base + lane >= end) return;
+            const int tok = (base + lane) * kAttnGroup;
+            const int at = tok / a.page_size;
+            row = tok - at * a.page_size;
+            page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + at);
+        };
+        const auto find = [&]() -> bool {
+            if (!cur.next(a)) return false;
+            nd.b = cur.b;
+            nd.len = cur.sp.len;
+            nd.head = cur.pair / a.chunks;
+            nd.row0 = (cur.pair - nd.head * a.chunks) * S::kRows;
+            nd.g0 = cur.first_group();
+            ng1 = cur.end_group();
+            nd.ng = ng1 - nd.g0;
+            nd.pair = cur.pair;
+            nd.first = nd.others = 0;
+            nd.at_start = cur.u0 == 0;
+            if (cur.u1 - cur.u0 < cur.sp.units) {
+                const int64_t first = cur.base + static_cast<int64_t>(cur.pair) * cur.sp.units;
+                nd.first = cur.owner(first);
+                nd.others = cur.owner(first + cur.sp.units - 1) - nd.first;
+            }
+            look_up(nd.b, nd.g0, ng1, next_page, next_row);
+            return true;
+        };
+        bool more = cur.start(a, lane) && find();
+        while (more) {
+            d = nd;
+            g1 = ng1;
+            int page = next_page, row = next_row;
+            const int rows = min(S::kRows, rows_all - d.row0);
             const int pq = parts & 1;
-            bool ok = true;
-            if (parts >= 2) ok = wait_phase(qempty + pq, ((parts >> 1) - 1) & 1, dead, a.err);
-            if (ok && !*dead) {
-                if (lane == 0) mbar_arrive_expect_tx(qfull + pq, rows * q_bytes);
+            if ((parts < 2 || wait_phase(qempty + pq, ((parts >> 1) - 1) & 1, dead, a.err)) && !*dead) {
+                if (lane == 0) {
+                    s_part[pq] = d;
+                    if (d.at_start && d.pair == 0) {
+                        const int given = __ldg(a.lens + d.b);
+                        if (given != d.len) report_error(a.err, RSSM_DEV_ATTN_LEN, d.b, given);
+                    }
+                    mbar_arrive_expect_tx(qfull + pq, rows * q_bytes);
+                }
                 __syncwarp();
                 for (int r = lane; r < rows; r += 32) {
-                    const int t = (row0 + r) / a.group, j = (row0 + r) % a.group;
+                    const int t = (d.row0 + r) / a.group, j = (d.row0 + r) - t * a.group;
                     const char* src = static_cast<const char*>(a.q) +
-                                      ((static_cast<int64_t>(cur.b) * a.T + t) * a.q_stride +
-                                       static_cast<int64_t>(head * a.group + j) * D) * S::kQsz;
+                                      ((static_cast<int64_t>(d.b) * a.T + t) * a.q_stride +
+                                       static_cast<int64_t>(d.head * a.group + j) * D) * S::kQsz;
                     bulk_g2s(qbuf + (pq * S::kRows + r) * S::QS, src, q_bytes, qfull + pq);
                 }
             }
             ++parts;
-            const int g0 = cur.first_group(), g1 = cur.end_group();
             // pages of 32 groups at a time, a step ahead; copies of PB groups at a time, a lane each
-            const auto look_up = [&](int base, int& page, int& row) {
-                page = a.num_pages;                      // outside the map: read as zeros
-                row = 0;
-                if (base + lane >= g1) return;
-                const int tok = (base + lane) * kAttnGroup;
-                const int at = tok / a.page_size;
-                row = tok - at * a.page_size;
-                page = __ldg(a.table + static_cast<int64_t>(cur.b) * a.max_pages + at);
-            };
-            int page, row, next_page, next_row;
-            look_up(g0, next_page, next_row);
-            for (int base = g0; base < g1; base += 32) {
-                page = next_page;
-                row = next_row;
-                look_up(base + 32, next_page, next_row);
-                if (page < 0 || page > a.num_pages || (page == a.num_pages && base + lane < g1)) {
-                    report_error(a.err, RSSM_DEV_ATTN_PAGE, cur.b, page);
+            more = find();
+            int page2 = 0, row2 = 0;
+            for (int base = d.g0; base < g1; base += 32, page = page2, row = row2) {
+                look_up(d.b, base + 32, g1, page2, row2);
+                if (base + lane < g1 && (page < 0 || page >= a.num_pages)) {
+                    report_error(a.err, RSSM_DEV_ATTN_PAGE, d.b, page);
                     page = a.num_pages;
                 }
                 const int n = min(32, g1 - base);
@@ -717,8 +935,8 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
                         if ((tn == 0 || wait_phase(empty + s, (tn - 1) & 1, dead, a.err)) && !*dead) {
                             const uint32_t dst = smem_u32(slots + s * S::kSlot);
                             mbar_arrive_expect_tx(full + s, S::kSlot);
-                            tma_load_5d(dst, &kmap, rw, head, pg, full + s);
-                            tma_load_5d(dst + S::kHalf, &vmap, rw, head, pg, full + s);
+                            tma_load_5d(dst, &kmap, rw, d.head, pg, full + s);
+                            tma_load_5d(dst + S::kHalf, &vmap, rw, d.head, pg, full + s);
                         }
                     }
                     __syncwarp();
@@ -729,6 +947,12 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
                     }
                 }
             }
+        }
+        // no more parts
+        const int pq = parts & 1;
+        if ((parts < 2 || wait_phase(qempty + pq, ((parts >> 1) - 1) & 1, dead, a.err)) && !*dead && lane == 0) {
+            s_part[pq].pair = -1;
+            mbar_arrive(qfull + pq);
         }
         if (*dead && lane == 0) {
             // let the copies in flight land before the block's memory goes
@@ -749,14 +973,27 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
     wp.lane = lane;
     wp.g = lane >> 2;
     wp.c = lane & 3;
-    while (cur.next(a)) {
-        const int head = cur.pair / a.chunks, row0 = (cur.pair % a.chunks) * S::kRows;
+    // The part that went to the workspace last: its arrival is counted while the
+    // next part runs (one thread waits for the writes and the count, not the
+    // block), and if it was the request's last, it is joined after that part.
+    Part left;
+    left.pair = -1;
+    const auto count_left = [&] {                            // thread 0, after a block barrier
+        uint32_t* n = a.arrived + static_cast<int64_t>(left.b) * a.kv_heads * a.chunks + left.pair;
+        const bool last = arrive_gpu(n) == static_cast<uint32_t>(left.others);
+        if (last) *n = 0;
+        *s_last = last;
+    };
+    for (;;) {
+        const int pq = parts & 1;
+        // all consumer warps go on, or none: one that gave up must not leave the
+        // others at a barrier
+        if (!all_of(wait_phase(qfull + pq, (parts >> 1) & 1, dead, a.err), 2, kThreads)) break;
+        const Part part = s_part[pq];
+        if (part.pair < 0) break;
+        if (left.pair >= 0 && tid == 0) count_left();
+        const int head = part.head, row0 = part.row0, len = part.len;
         const int rows = min(S::kRows, rows_all - row0);
-        const int b = cur.b, len = cur.sp.len;
-        if (cur.u0 == 0 && cur.pair == 0 && tid == 0) {
-            const int given = __ldg(a.lens + b);
-            if (given != len) report_error(a.err, RSSM_DEV_ATTN_LEN, b, given);
-        }
         // what the warp's two rows see: [see_lo, see_hi]
         int draft[2], see_lo[2], see_hi[2];
 #pragma unroll
@@ -769,36 +1006,56 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
         const int all_hi = len - a.T;                             // the last token that all drafts see
         const int all_lo = a.window > 0 ? max(0, len - a.window) : 0;   // and the first
         const int some_lo = a.window > 0 ? max(0, len - a.T - a.window + 1) : 0;
-        const int pq = parts & 1;
         wp.reset();
-        bool ok = wait_phase(qfull + pq, (parts >> 1) & 1, dead, a.err);
-        if (ok) wp.load_q(qbuf + (pq * S::kRows + wm * 16) * S::QS, a.scale_log2, KV == kFP8 ? __ldg(a.k_scale + head) : 1.f);
+        wp.load_q(qbuf + (pq * S::kRows + wm * 16) * S::QS, a.scale_log2, KV == kFP8 ? __ldg(a.k_scale + head) : 1.f);
         if (KV != kF32) {
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty + pq);
         }
-        const int g0 = cur.first_group(), g1 = cur.end_group();
-        // this warp's groups: those whose slot is wt modulo NT
-        const int ng = g1 - g0;
+        // this warp's groups: those whose slot is wt modulo NT; those that all rows
+        // see whole, [f0, f1), two at a time where the registers allow it
+        const int g0 = part.g0, ng = part.ng;
+        const int f0 = (all_lo + kAttnGroup - 1) / kAttnGroup - g0, f1 = (all_hi + 1) / kAttnGroup - g0;
+        constexpr int NG = S::kPair ? 2 : 1;
         int k = (wt + S::NT - pos % S::NT) % S::NT;
         int s = pos + k, tn = turn;
-        for (; k < ng; k += S::NT, s += S::NT) {
+        const auto forward = [&] {                            // to this warp's next group
+            k += S::NT;
+            s += S::NT;
             if (s >= NS) {
                 s -= NS;
                 ++tn;
             }
-            ok = wait_phase(full + s, tn & 1, dead, a.err);
-            const int tok = (g0 + k) * kAttnGroup;
+        };
+        if (s >= NS) {
+            s -= NS;
+            ++tn;
+        }
+        while (k < ng) {
             const uint32_t kb = smem_u32(slots + s * S::kSlot), vb = kb + S::kHalf;
-            if (ok) {
+            uint64_t* const done = empty + s;
+            bool ok = wait_phase(full + s, tn & 1, dead, a.err);
+            if (k >= f0 && k < f1) {
+                if (NG == 2 && k + S::NT < min(f1, ng)) {
+                    forward();
+                    const uint32_t kb2 = smem_u32(slots + s * S::kSlot), vb2 = kb2 + S::kHalf;
+                    ok = wait_phase(full + s, tn & 1, dead, a.err) && ok;
+                    const uint32_t ks[2] = {kb, kb2}, vs[2] = {vb, vb2};
+                    if (ok) wp.step(ks, vs);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty + s);
+                } else {
+                    const uint32_t ks[1] = {kb}, vs[1] = {vb};
+                    if (ok) wp.step(ks, vs);
+                }
+            } else if (ok) {
+                const int tok = (g0 + k) * kAttnGroup;
                 const int lo[2] = {see_lo[0] - tok, see_lo[1] - tok}, hi[2] = {see_hi[0] - tok, see_hi[1] - tok};
-                if (tok >= all_lo && tok + kAttnGroup - 1 <= all_hi)
-                    wp.template step<false>(kb, vb, lo, hi, 0, 0, a.T, tok, len, a.window, draft);
-                else
-                    wp.template step<true>(kb, vb, lo, hi, some_lo - tok, len - 1 - tok, a.T, tok, len, a.window, draft);
+                wp.step_masked(kb, vb, lo, hi, some_lo - tok, len - 1 - tok, a.T, tok, len, a.window, draft);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty + s);
+            if (lane == 0) mbar_arrive(done);
+            forward();
         }
         pos += ng;
         turn += pos / NS;
@@ -834,14 +1091,9 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
 #pragma unroll 1
         for (int w = 0; w < S::NT; w += S::NB) {
             if (wt >= w && wt < w + S::NB) {
-#pragma unroll
-                for (int i2 = 0; i2 < Warp<KV, S>::kTiles; ++i2)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float* d = merged + ((wt - w) * S::kRows + wm * 16 + wp.g + 8 * (j >> 1)) * S::OS + wp.column(i2, j & 1);
-                        const float v = wp.o[i2][j] * f[j >> 1];
-                        *d = w == 0 ? v : *d + v;
-                    }
+                float* to = merged + ((wt - w) * S::kRows + wm * 16 + wp.g) * S::OS;
+                if (w == 0) wp.template leave<false>(to, f);
+                else wp.template leave<true>(to, f);
             }
             named_sync(1, kThreads);
         }
@@ -854,78 +1106,30 @@ attn_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, c
             }
             return v;
         };
-        const bool whole = cur.u0 == 0 && cur.u1 == cur.sp.units;
-        const float vscale = KV == kFP8 ? __ldg(a.v_scale + head) : 1.f;
-        const auto put = [&](int r, int col, float4 v, float M, float L) {
-            const int t = (row0 + r) / a.group, j = (row0 + r) % a.group;
-            const int64_t at = (static_cast<int64_t>(b) * a.T + t) * a.q_heads + head * a.group + j;
-            const float inv = L == 0.f ? 0.f : vscale / L;
-            v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-            if (KV == kF32) {
-                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + col) = v;
-            } else {
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * D + col) =
-                    make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-            }
-            if (a.lse != nullptr && col == 0)
-                a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-        };
-        if (whole) {
+        if (part.others == 0) {
             for (int x = tid; x < rows * (D / 4); x += kThreads) {
                 const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-                put(r, col, sum_of(r, col), s_row[r].x, s_row[r].y);
+                put<KV, S>(a, part, r, col, sum_of(r, col), s_row[r].x, s_row[r].y);
             }
-            continue;
-        }
-        // a part: to the workspace; the last block of the request's to arrive joins
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (cur.u0 == 0 ? 1 : 0);
-        for (int x = tid; x < rows * (D / 4); x += kThreads) {
-            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-            __stcg(reinterpret_cast<float4*>(a.part_o + (slot * S::kRows + r) * D + col), sum_of(r, col));
-            if (col == 0) __stcg(a.part_ml + slot * S::kRows + r, s_row[r]);
-        }
-        __threadfence();
-        named_sync(1, kThreads);
-        const int64_t first = cur.base + static_cast<int64_t>(cur.pair) * cur.sp.units;
-        const int c0 = cur.owner(first), c1 = cur.owner(first + cur.sp.units - 1);
-        if (tid == 0) {
-            uint32_t* n = a.arrived + static_cast<int64_t>(b) * a.kv_heads * a.chunks + cur.pair;
-            const bool last = atomicAdd(n, 1u) == static_cast<uint32_t>(c1 - c0);
-            if (last) *n = 0;
-            __threadfence();
-            *s_last = last;
-        }
-        named_sync(1, kThreads);
-        if (!*s_last) continue;
-        for (int x = tid; x < rows * (D / 4); x += kThreads) {
-            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-            float M = -INFINITY, L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kAhead = 8;
-            for (int p = c0; p <= c1; p += kAhead) {
-                float2 ml[kAhead];
-                float4 v[kAhead];
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const int64_t at = (2 * static_cast<int64_t>(min(p + k, c1)) + (p + k == c0 ? 1 : 0)) * S::kRows + r;
-                    ml[k] = __ldcg(a.part_ml + at);
-                    v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
-                }
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    if (p + k > c1) break;
-                    const float M2 = fmaxf(M, ml[k].x), ref = M2 == -INFINITY ? 0.f : M2;
-                    const float fa = ex2(M - ref), fb = ex2(ml[k].x - ref);
-                    M = M2;
-                    L = L * fa + ml[k].y * fb;
-                    acc.x = acc.x * fa + v[k].x * fb;
-                    acc.y = acc.y * fa + v[k].y * fb;
-                    acc.z = acc.z * fa + v[k].z * fb;
-                    acc.w = acc.w * fa + v[k].w * fb;
-                }
+        } else {
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + part.at_start;
+            for (int x = tid; x < rows * (D / 4); x += kThreads) {
+                const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+                __stcg(reinterpret_cast<float4*>(a.part_o + (slot * S::kRows + r) * D + col), sum_of(r, col));
+                if (col == 0) __stcg(a.part_ml + slot * S::kRows + r, s_row[r]);
             }
-            put(r, col, acc, M, L);
         }
+        if (left.pair >= 0) {
+            named_sync(1, kThreads);                          // the buffers are read
+            if (*s_last) join_parts<KV, S>(a, left, merged, s_row);
+        }
+        left = part;
+        if (part.others == 0) left.pair = -1;
+    }
+    if (left.pair >= 0) {
+        if (tid == 0) count_left();
+        named_sync(1, kThreads);
+        if (*s_last) join_parts<KV, S>(a, left, merged, s_row);
     }
 }
 
