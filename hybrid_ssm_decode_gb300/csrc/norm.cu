@@ -32,16 +32,26 @@ struct GatedNormArgs {
     float eps, w_off;
 };
 
-// VEC consecutive elements as floats (VEC = 8: 16-byte aligned, or 1).
+// 32 bytes in one access, so that a warp's FP32 accesses have no gaps. L1 is
+// passed by for what is read once.
+__device__ __forceinline__ void ld32(float (&v)[8], const float* p) {
+    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void ld32_keep(float (&v)[8], const float* p) {
+    asm("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(p));
+}
+__device__ __forceinline__ void st32(float* p, const float (&v)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+}
+
+// VEC consecutive elements as floats (VEC = 8: aligned to their size, or 1).
 template <int VEC>
 __device__ __forceinline__ void load_vec(float (&v)[VEC], const float* p) {
-    if (VEC == 8) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x; v[1 % VEC] = a.y; v[2 % VEC] = a.z; v[3 % VEC] = a.w;
-        v[4 % VEC] = b.x; v[5 % VEC] = b.y; v[6 % VEC] = b.z; v[7 % VEC] = b.w;
-    } else {
-        v[0] = *p;
-    }
+    if constexpr (VEC == 8) ld32(v, p);
+    else v[0] = *p;
 }
 template <int VEC>
 __device__ __forceinline__ void load_vec(float (&v)[VEC], const __nv_bfloat16* p) {
@@ -60,22 +70,13 @@ __device__ __forceinline__ void load_vec(float (&v)[VEC], const __nv_bfloat16* p
 // Weights stay in cache: every row reads them.
 template <int VEC>
 __device__ __forceinline__ void load_w(float (&v)[VEC], const float* p) {
-    if (VEC == 8) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x; v[1 % VEC] = a.y; v[2 % VEC] = a.z; v[3 % VEC] = a.w;
-        v[4 % VEC] = b.x; v[5 % VEC] = b.y; v[6 % VEC] = b.z; v[7 % VEC] = b.w;
-    } else {
-        v[0] = __ldg(p);
-    }
+    if constexpr (VEC == 8) ld32_keep(v, p);
+    else v[0] = __ldg(p);
 }
 template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
-    if (VEC == 8) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1 % VEC], v[2 % VEC], v[3 % VEC]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4 % VEC], v[5 % VEC], v[6 % VEC], v[7 % VEC]);
-    } else {
-        *p = v[0];
-    }
+    if constexpr (VEC == 8) st32(p, v);
+    else *p = v[0];
 }
 template <int VEC>
 __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[VEC]) {
@@ -190,55 +191,139 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a, int
     }
 }
 
-template <class T, int VEC, int VPT>
-__global__ void __launch_bounds__(1024) gated_norm_kernel(const GatedNormArgs a, int tpr) {
-    __shared__ float s_red[32];
-    const int per_block = blockDim.x / tpr;
-    const int lane = threadIdx.x % tpr;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / tpr;
-    const bool live = item < a.rows * a.groups;
-    const int64_t row = live ? item / a.groups : 0;
-    const int col0 = live ? static_cast<int>(item - row * a.groups) * a.group : 0;
-    const int nvec = a.group / VEC;
-    const T* y = static_cast<const T*>(a.y) + row * a.y_stride + col0;
-    const T* z = static_cast<const T*>(a.z) + row * a.z_stride + col0;
-    float v[VPT][VEC], g[VPT][VEC];
+// act(z). FP32 keeps the exact exponential and division; for BF16 their
+// approximations, within 2^-20, are far inside the rounding and a quarter of the
+// instructions.
+template <class T, int ACT>
+__device__ __forceinline__ float gate_of(float z) {
+    if (sizeof(T) == 4) return (ACT == RSSM_GATE_SILU ? z : 1.f) / (1.f + expf(-z));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return ACT == RSSM_GATE_SILU ? z * r : r;
+}
+
+// Short groups are bound by instructions before memory: one group a thread cost 39
+// an element and 84 us over 16384 rows of 32 BF16 groups of 128. So a thread takes
+// several groups, with the weights of its columns in registers where all groups
+// share them (80 us), and loads the next group beside the sums of this one, which
+// doubles what is under way at 4 blocks of 256 an SM (70 us, 5.7 TB/s).
+// VEC elements as they are stored, so that a load can be long under way before
+// the values are widened.
+template <class T, int VEC>
+struct Raw {
+    uint32_t w[VEC * sizeof(T) / 4 > 0 ? VEC * sizeof(T) / 4 : 1];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+            else w[0] = *reinterpret_cast<const uint16_t*>(p);
+        } else if constexpr (sizeof(T) == 4) {
+            float v[8];
+            ld32(v, reinterpret_cast<const float*>(p));
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = lane + i * tpr;
-        if (live && c < nvec) {
-            load_vec<VEC>(v[i], y + static_cast<int64_t>(c) * VEC);
-            load_vec<VEC>(g[i], z + static_cast<int64_t>(c) * VEC);
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
         } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) v[i][e] = g[i][e] = 0.f;
+            asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p) : "memory");
         }
     }
-    float ss = 0.f;
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+        for (uint32_t& x : w) x = 0;
+    }
+    __device__ __forceinline__ void get(float (&v)[VEC]) const {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float d = 1.f + expf(-g[i][e]);
-            g[i][e] = ((a.act == RSSM_GATE_SILU) ? g[i][e] : 1.f) / d;
-            if (!a.norm_first) v[i][e] *= g[i][e];
-            ss = fmaf(v[i][e], v[i][e], ss);
+        for (int i = 0; i < VEC; ++i) {
+            if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+            else v[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
         }
-    const float r = rsqrtf(row_sum(ss, tpr, s_red) / static_cast<float>(a.group) + a.eps);
-    const float* w = a.w + (a.w_dim == a.group ? 0 : col0);
-    T* out = static_cast<T*>(a.out) + row * a.out_stride + col0;
+    }
+};
+
+template <class T, int VEC, int VPT, int FIRST, int ACT>
+__global__ void __launch_bounds__(1024) gated_norm_kernel(const GatedNormArgs a, int tpr, uint32_t items) {
+    __shared__ float s_red[2][32];
+    const uint32_t per_block = blockDim.x / tpr, step = gridDim.x * per_block;
+    const int lane = threadIdx.x % tpr;
+    const uint32_t groups = a.groups;
+    uint32_t item = blockIdx.x * per_block + threadIdx.x / tpr;
+    uint32_t row = item / groups, col = item - row * groups;
+    const uint32_t step_row = step / groups, step_col = step - step_row * groups;
+    const int nvec = a.group / VEC;
+    const bool shared_w = a.w_dim == a.group;
+    float wv[VPT][VEC];
+    if (shared_w) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = lane + i * tpr;
-        if (!live || c >= nvec) continue;
-        float wv[VEC];
-        load_w<VEC>(wv, w + c * VEC);
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * tpr;
+            if (c >= nvec) continue;
+            load_w<VEC>(wv[i], a.w + c * VEC);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            wv[e] = v[i][e] * r * (a.w_off + wv[e]);
-            if (a.norm_first) wv[e] *= g[i][e];
+            for (int e = 0; e < VEC; ++e) wv[i][e] += a.w_off;
         }
-        store_vec<VEC>(out + static_cast<int64_t>(c) * VEC, wv);
+    }
+    const float inv_n = 1.f / static_cast<float>(a.group);
+    int turn = 0;
+    Raw<T, VEC> ry[VPT], rz[VPT];
+    const auto fetch = [&](uint32_t it, uint32_t r, uint32_t cl) {
+        const int64_t at = static_cast<int64_t>(cl) * a.group;
+        const T* y = static_cast<const T*>(a.y) + r * a.y_stride + at;
+        const T* z = static_cast<const T*>(a.z) + r * a.z_stride + at;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * tpr;
+            if (it < items && c < nvec) {
+                ry[i].load(y + c * VEC);
+                rz[i].load(z + c * VEC);
+            } else {
+                ry[i].clear();
+                rz[i].clear();
+            }
+        }
+    };
+    fetch(item, row, col);
+    // whole blocks go round together: their rows meet at barriers
+    for (uint32_t first = blockIdx.x * per_block; first < items; first += step, turn ^= 1) {
+        const bool live = item < items;
+        const int64_t at = static_cast<int64_t>(col) * a.group;
+        T* out = static_cast<T*>(a.out) + row * a.out_stride + at;
+        float v[VPT][VEC], g[VPT][VEC];
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            ry[i].get(v[i]);
+            rz[i].get(g[i]);
+        }
+        item += step;
+        row += step_row;
+        col += step_col;
+        if (col >= groups) {
+            col -= groups;
+            ++row;
+        }
+        fetch(item, row, col);                 // the next group's loads, beside this one's sums
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                g[i][e] = gate_of<T, ACT>(g[i][e]);
+                if (!FIRST) v[i][e] *= g[i][e];
+                ss = fmaf(v[i][e], v[i][e], ss);
+            }
+        const float r = rsqrtf(fmaf(row_sum(ss, tpr, s_red[turn]), inv_n, a.eps));
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * tpr;
+            if (!live || c >= nvec) continue;
+            float w[VEC];
+            if (!shared_w) load_w<VEC>(w, a.w + at + c * VEC);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                v[i][e] *= r * (shared_w ? wv[i][e] : a.w_off + w[e]);
+                if (FIRST) v[i][e] *= g[i][e];
+            }
+            store_vec<VEC>(out + c * VEC, v[i]);
+        }
     }
 }
 
@@ -275,8 +360,9 @@ NormShape norm_shape(int cols, int vec, int64_t items) {
     return s;
 }
 
+// Whether rows of this type can be read 8 elements at a time.
 bool vec_ok(const void* p, int64_t stride, int esz) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride * esz) % 16 == 0;
+    return (reinterpret_cast<uintptr_t>(p) & (8u * esz - 1)) == 0 && (stride * esz) % (8 * esz) == 0;
 }
 
 template <class TU, class TX>
@@ -294,19 +380,34 @@ cudaError_t launch_add(const AddNormArgs& a, int vec, const NormShape& s, cudaSt
     return cudaGetLastError();
 }
 
-template <class T>
-cudaError_t launch_gated(const GatedNormArgs& a, int vec, const NormShape& s, cudaStream_t st) {
-    const dim3 g(static_cast<unsigned>(s.blocks));
+template <class T, int FIRST, int ACT>
+cudaError_t launch_gated_as(const GatedNormArgs& a, int vec, const NormShape& s, uint32_t items, cudaStream_t st) {
+    int sms = 0, smem = 0;
+    const cudaError_t e = device_limits(&sms, &smem);
+    if (e != cudaSuccess) return e;
+    // as many blocks as are resident at 64 registers a thread
+    const int64_t most = static_cast<int64_t>(sms) * (1024 / s.threads);
+    const dim3 g(static_cast<unsigned>(s.blocks < most ? s.blocks : most));
     if (vec == 8) {
-        if (s.vpt == 1) gated_norm_kernel<T, 8, 1><<<g, s.threads, 0, st>>>(a, s.tpr);
-        else if (s.vpt == 2) gated_norm_kernel<T, 8, 2><<<g, s.threads, 0, st>>>(a, s.tpr);
-        else gated_norm_kernel<T, 8, 4><<<g, s.threads, 0, st>>>(a, s.tpr);
+        if (s.vpt == 1) gated_norm_kernel<T, 8, 1, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
+        else if (s.vpt == 2) gated_norm_kernel<T, 8, 2, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
+        else gated_norm_kernel<T, 8, 4, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
     } else {
-        if (s.vpt == 2) gated_norm_kernel<T, 1, 2><<<g, s.threads, 0, st>>>(a, s.tpr);
-        else if (s.vpt == 8) gated_norm_kernel<T, 1, 8><<<g, s.threads, 0, st>>>(a, s.tpr);
-        else gated_norm_kernel<T, 1, 32><<<g, s.threads, 0, st>>>(a, s.tpr);
+        if (s.vpt == 2) gated_norm_kernel<T, 1, 2, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
+        else if (s.vpt == 8) gated_norm_kernel<T, 1, 8, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
+        else gated_norm_kernel<T, 1, 32, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
     }
     return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_gated(const GatedNormArgs& a, int vec, const NormShape& s, cudaStream_t st) {
+    const uint32_t n = static_cast<uint32_t>(a.rows * a.groups);
+    if (a.act == RSSM_GATE_SILU)
+        return a.norm_first ? launch_gated_as<T, 1, RSSM_GATE_SILU>(a, vec, s, n, st)
+                            : launch_gated_as<T, 0, RSSM_GATE_SILU>(a, vec, s, n, st);
+    return a.norm_first ? launch_gated_as<T, 1, RSSM_GATE_SIGMOID>(a, vec, s, n, st)
+                        : launch_gated_as<T, 0, RSSM_GATE_SIGMOID>(a, vec, s, n, st);
 }
 
 bool float_dtype(int d) { return d == RSSM_F32 || d == RSSM_BF16; }

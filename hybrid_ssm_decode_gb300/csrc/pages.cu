@@ -3,15 +3,17 @@
 // position of every new token.
 //
 // Both are one exclusive scan over the requests (pages per request) followed by
-// work on the scan's items (tokens, or pages going back). Every block makes
-// the whole scan for itself, which costs it one pass over 8 bytes a request
-// from L2, and then takes an equal share of the items. So one launch does it
-// without any block waiting for another; the last block to have read the
-// lengths (a ticket) writes the new ones and the free count. The order of the
-// pages is that of the requests whatever the launch.
+// work on the scan's items (tokens, or pages going back). The order of the pages
+// is that of the requests whatever the launch.
 //
-// Bound by latency for a decode step (a block, two barriers a scan), and by the
-// slot and position stores (8 bytes a token) for prompts.
+// A decode step (the same few tokens for every request) is a single block, a
+// thread a request: bound by latency, of which a scan is one barrier. Prompts and
+// ended requests take a block per 2048 items, up to two per SM: every block makes
+// the whole scan for itself, which costs it one pass over 8 bytes a request from L2,
+// and then takes an equal share of the items. So one launch does it without any
+// block waiting for another; the last block to have read the lengths (a ticket)
+// writes the new ones and the free count. There the slot and position stores
+// (8 bytes a token) are the floor.
 #include <cstring>
 #include <new>
 
@@ -20,8 +22,10 @@
 namespace rssm {
 namespace {
 
-constexpr int kPagesThreads = 1024;
-constexpr int kTokensPerBlock = 4096;   // at least; more blocks than this gives cost more scans than they save
+constexpr int kPagesThreads = 512;      // of the kernels that share items out
+constexpr int kItemsPerBlock = 2048;    // four a thread
+constexpr int kStepThreads = 1024;      // most of the single-block kernels
+constexpr int kStepTokens = 16;         // most tokens a request that those take
 
 struct PagesArgs {
     int32_t* lens;
@@ -31,6 +35,7 @@ struct PagesArgs {
     int32_t* err;
     uint32_t* ticket;
     int32_t batch, page_size, num_pages, max_pages;
+    int32_t shift;        // log2(page_size), or -1: a division costs 20 instructions
     // extend
     const int32_t* d_new;
     int32_t T;
@@ -42,31 +47,57 @@ struct PagesArgs {
     const int32_t* keep;
 };
 
-// Inclusive scan of one value a thread over the block, added to *carry (the
-// total so far, the same in every thread), which the block's total then grows by.
-template <class V>
-__device__ __forceinline__ V block_scan(V v, V* s_warp, V* carry) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive scans of one int32 and one int64 a thread over the block, added to
+// the totals so far, which the block's totals then join. One barrier: consecutive
+// scans use the two halves of the buffers in turn.
+struct ScanBuf {
+    int32_t x[2][32];
+    int64_t y[2][32];
+};
+struct Scan {
+    int32_t cx = 0;
+    int64_t cy = 0;
+    int turn = 0;
+    __device__ __forceinline__ void reset() { cx = 0, cy = 0; }
+    template <bool kBoth>
+    __device__ __forceinline__ void run(ScanBuf& s, int32_t& x, int64_t& y) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const V n = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += n;
-    }
-    __syncthreads();                      // s_warp may hold an earlier scan
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    V w = s_warp[lane];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t n = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += n;
+            if (kBoth) {
+                const int64_t m = __shfl_up_sync(0xffffffffu, y, o);
+                if (lane >= o) y += m;
+            }
+        }
+        if (lane == 31) {
+            s.x[turn][warp] = x;
+            if (kBoth) s.y[turn][warp] = y;
+        }
+        __syncthreads();
+        int32_t w = lane < warps ? s.x[turn][lane] : 0;
+        int64_t v = kBoth && lane < warps ? s.y[turn][lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const V n = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t n = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += n;
+            if (kBoth) {
+                const int64_t m = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += m;
+            }
+        }
+        const int32_t bx = __shfl_sync(0xffffffffu, w, max(warp - 1, 0)), tx = __shfl_sync(0xffffffffu, w, 31);
+        x += cx + (warp ? bx : 0);
+        cx += tx;
+        if (kBoth) {
+            const int64_t by = __shfl_sync(0xffffffffu, v, max(warp - 1, 0)), ty = __shfl_sync(0xffffffffu, v, 31);
+            y += cy + (warp ? by : 0);
+            cy += ty;
+        }
+        turn ^= 1;
     }
-    const V before = warp == 0 ? V(0) : __shfl_sync(0xffffffffu, w, warp - 1);
-    const V total = __shfl_sync(0xffffffffu, w, 31);
-    v += *carry + before;
-    *carry += total;
-    return v;
-}
+};
 
 // What one request asks for.
 struct Ask {
@@ -76,8 +107,12 @@ struct Ask {
     int32_t newlen;
 };
 
-__device__ __forceinline__ int32_t pages_of(int64_t tokens, int32_t ps) {
-    return static_cast<int32_t>((tokens + ps - 1) / ps);
+// Tokens to whole pages, for 0 <= n < 2^31 and a page more.
+__device__ __forceinline__ int32_t whole_pages(const PagesArgs& a, uint32_t n) {
+    return static_cast<int32_t>(a.shift >= 0 ? n >> a.shift : n / static_cast<uint32_t>(a.page_size));
+}
+__device__ __forceinline__ int32_t pages_of(const PagesArgs& a, uint32_t tokens) {
+    return whole_pages(a, tokens + static_cast<uint32_t>(a.page_size) - 1);
 }
 
 // The tokens of request b as they count for the slots' offsets: at least 0.
@@ -91,7 +126,7 @@ __device__ __forceinline__ Ask ask_extend(const PagesArgs& a, int b) {
     if (n < 0 || r.len < 0 || r.len > most) r.bad = RSSM_DEV_PAGES_COUNT;
     else if (static_cast<int64_t>(r.len) + n > most) r.bad = RSSM_DEV_PAGES_ROW;
     r.newlen = r.len;
-    if (r.bad == 0) r.need = pages_of(static_cast<int64_t>(r.len) + n, a.page_size) - pages_of(r.len, a.page_size);
+    if (r.bad == 0) r.need = pages_of(a, r.len + n) - pages_of(a, r.len);
     return r;
 }
 
@@ -109,25 +144,26 @@ __device__ __forceinline__ Ask ask_shrink(const PagesArgs& a, int b) {
         if (k < 0) r.bad = RSSM_DEV_PAGES_COUNT;
         else r.newlen = min(r.len, k);
     }
-    r.count = pages_of(r.len, a.page_size) - pages_of(r.newlen, a.page_size);
+    if (r.newlen != r.len) r.count = pages_of(a, r.len) - pages_of(a, r.newlen);
     return r;
 }
 
-// The requests of one batch of the scan that own items of this block, in order.
-struct Listed {
-    int64_t first[kPagesThreads];   // the request's first item
-    int32_t request[kPagesThreads];
-    int32_t len[kPagesThreads];     // extend: tokens before; shrink: pages left
-    int32_t page[kPagesThreads];    // extend: the scan of its pages; -1: refused
-    int32_t n;
+// One round of the scan as a table to find items in: entry i is request
+// `base + i`. Entries of no items share their first item with the next entry
+// that has some.
+struct Round {
+    int32_t first[kPagesThreads];   // the request's first item (2^31 - 1: past every list)
+    int32_t len[kPagesThreads];     // extend: tokens before
+    int32_t held[kPagesThreads];    // pages before (extend) or left (shrink)
+    int32_t page[kPagesThreads];    // extend: pages handed out before the request's; -1: refused
 };
 
-// The list entry that item `it` belongs to: the last whose first item is <= it.
-__device__ __forceinline__ int find_item(const Listed& L, int64_t it) {
-    int lo = 0, hi = L.n - 1;
+// The last entry whose first item is <= it.
+__device__ __forceinline__ int find_item(const Round& R, int n, int32_t it) {
+    int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int m = (lo + hi + 1) >> 1;
-        if (L.first[m] <= it) lo = m;
+        if (R.first[m] <= it) lo = m;
         else hi = m - 1;
     }
     return lo;
@@ -148,128 +184,148 @@ __device__ __forceinline__ bool last_block(uint32_t* ticket) {
     return last;
 }
 
+// One round of an extend's scan. On return `upto` and `tok_end` are the scan's
+// values past the request; a request that the slot list cannot hold is refused
+// before its pages are counted.
+__device__ __forceinline__ void extend_round(const PagesArgs& a, int b, ScanBuf& buf, Scan& scan, Ask& r, int32_t& upto,
+                                             int64_t& tok_end) {
+    r = ask_extend(a, b);
+    tok_end = r.count;
+    upto = r.need;
+    const Scan before = scan;
+    scan.run<true>(buf, upto, tok_end);
+    if (scan.cy <= a.max_tokens) return;                       // uniform: the lists hold every token so far
+    if (r.bad == 0 && tok_end > a.max_tokens) {
+        r.bad = RSSM_DEV_PAGES_SLOTS;
+        r.need = 0;
+    }
+    int64_t unused = 0;
+    upto = r.need;
+    scan.cx = before.cx;
+    scan.run<false>(buf, upto, unused);
+}
+
 __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const PagesArgs a) {
-    __shared__ int32_t s_need[32];
-    __shared__ int64_t s_tok[32];
+    __shared__ ScanBuf buf;
     __shared__ int32_t s_fit;
-    __shared__ Listed L;
+    __shared__ Round R;
     const int tid = threadIdx.x;
     const int32_t nfree = *a.free_count;
     const int rounds = (a.batch + kPagesThreads - 1) / kPagesThreads;
 
-    // total tokens, and the pages that go out: the largest scan value that the
-    // pool still covers (the scan grows, so the requests past it get none)
+    // Total tokens, and the pages that go out: all that are asked for, or else
+    // the largest scan value that the pool covers (the scan grows, so the requests
+    // past it get none).
     if (tid == 0) s_fit = 0;
-    __syncthreads();
-    int32_t c_need = 0;
-    int64_t c_tok = 0;
+    Scan scan;
     Ask r{};
     int32_t upto = 0;
     int64_t tok_end = 0;
     for (int i = 0; i < rounds; ++i) {
-        r = ask_extend(a, i * kPagesThreads + tid);
-        tok_end = block_scan<int64_t>(r.count, s_tok, &c_tok);
-        if (r.bad == 0 && tok_end > a.max_tokens) {
-            r.bad = RSSM_DEV_PAGES_SLOTS;
-            r.need = 0;
-        }
-        upto = block_scan<int32_t>(r.need, s_need, &c_need);
-        if (r.need > 0 && upto <= nfree) atomicMax(&s_fit, upto);
+        extend_round(a, i * kPagesThreads + tid, buf, scan, r, upto, tok_end);
+        if (scan.cx > nfree && r.need > 0 && upto <= nfree) atomicMax(&s_fit, upto);
+        else if (scan.cx <= nfree && tid == 0) atomicMax(&s_fit, scan.cx);
     }
     __syncthreads();
-    const int32_t out = s_fit;               // pages handed out
-    const int32_t base = nfree - out;
-    const int64_t total = min(c_tok, static_cast<int64_t>(a.max_tokens));
+    const int32_t out = s_fit, base = nfree - out;
+    const int64_t total = min(scan.cy, static_cast<int64_t>(a.max_tokens));
     const int64_t per = ((total + gridDim.x - 1) / gridDim.x + 3) / 4 * 4;
-    const int64_t t0 = min(total, per * blockIdx.x), t1 = min(total, t0 + per);
+    const int32_t t0 = static_cast<int32_t>(min(total, per * blockIdx.x)), t1 = static_cast<int32_t>(min(total, t0 + per));
 
     // The requests again, in order, now with what each one gets (with one round
     // the values are still in registers).
-    c_need = 0;
-    c_tok = 0;
+    scan.reset();
     for (int i = 0; i < rounds; ++i) {
-        const int b = i * kPagesThreads + tid;
         if (rounds > 1) {
-            r = ask_extend(a, b);
-            tok_end = block_scan<int64_t>(r.count, s_tok, &c_tok);
-            if (r.bad == 0 && tok_end > a.max_tokens) {
-                r.bad = RSSM_DEV_PAGES_SLOTS;
-                r.need = 0;
-            }
-            upto = block_scan<int32_t>(r.need, s_need, &c_need);
+            __syncthreads();                                   // the round before is used up
+            extend_round(a, i * kPagesThreads + tid, buf, scan, r, upto, tok_end);
         }
         if (r.bad == 0 && r.need > 0 && upto > out) r.bad = RSSM_DEV_PAGES_EMPTY;
-        const int64_t tok0 = tok_end - r.count;
-        const bool mine = r.count > 0 && tok0 < t1 && tok_end > t0;
-        // positions in the list, by a count over the block
-        int32_t zero = 0;
-        const int32_t at = block_scan<int32_t>(mine ? 1 : 0, s_need, &zero) - 1;
-        if (mine) {
-            L.first[at] = tok0;
-            L.request[at] = b;
-            L.len[at] = r.len;
-            L.page[at] = r.bad ? -1 : upto - r.need;
-        }
-        if (tid == 0) L.n = zero;
+        R.first[tid] = static_cast<int32_t>(min(tok_end - r.count, static_cast<int64_t>(0x7FFFFFFF)));
+        R.len[tid] = r.len;
+        R.held[tid] = pages_of(a, max(r.len, 0));
+        R.page[tid] = r.bad ? -1 : upto - r.need;
         __syncthreads();
-        if (zero > 0) {
-            const int64_t g0 = max(t0, L.first[0]);
-            // the list's last token: of the last request, or the block's last
-            const int64_t g1 = min(t1, rounds > 1 ? c_tok : total);
-            for (int64_t q = g0 / 4 * 4 + 4 * tid; q < g1; q += 4 * kPagesThreads) {
-                int e = find_item(L, max(q, g0));
-                int4 sl, po;
-                int32_t* slv = &sl.x;
-                int32_t* pov = &po.x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t it = q + j;
-                    slv[j] = pov[j] = -1;
-                    if (it < g0 || it >= g1) continue;
-                    while (e + 1 < L.n && L.first[e + 1] <= it) ++e;
-                    if (L.page[e] < 0) continue;
-                    const int32_t pos = L.len[e] + static_cast<int32_t>(it - L.first[e]);
-                    const int32_t p = pos / a.page_size, off = pos - p * a.page_size;
-                    const int32_t held = pages_of(L.len[e], a.page_size);
-                    int32_t* row = a.table + static_cast<int64_t>(L.request[e]) * a.max_pages;
-                    int32_t page;
-                    if (p < held) {
-                        page = row[p];
-                    } else {
-                        page = a.free_list[base + L.page[e] + (p - held)];
-                        if (off == 0) row[p] = page;   // a fresh page's first token is a new one
-                    }
-                    slv[j] = page < 0 ? -1 : page * a.page_size + off;
-                    pov[j] = pos;
-                }
-                if (a.wide && q >= g0 && q + 4 <= g1) {
-                    *reinterpret_cast<int4*>(a.slots + q) = sl;
-                    if (a.positions) *reinterpret_cast<int4*>(a.positions + q) = po;
-                } else {
-                    for (int j = 0; j < 4; ++j) {
-                        if (q + j < g0 || q + j >= g1) continue;
-                        a.slots[q + j] = slv[j];
-                        if (a.positions) a.positions[q + j] = pov[j];
-                    }
+        const int32_t g0 = max(t0, R.first[0]), g1 = static_cast<int32_t>(min(static_cast<int64_t>(t1), rounds > 1 ? scan.cy : total));
+        int e = -1;
+        int32_t next = 0;
+        for (int64_t q8 = g0 / 4 * 4 + 4 * tid; q8 < g1; q8 += 4 * kPagesThreads) {
+            const int32_t q = static_cast<int32_t>(q8);
+            // in a long prompt the next four tokens are the same request's, and mostly one page's
+            if (max(q, g0) >= next || e < 0) {
+                e = find_item(R, kPagesThreads, max(q, g0));
+                next = e + 1 < kPagesThreads ? R.first[e + 1] : 0x7FFFFFFF;
+            }
+            if (a.wide && q >= g0 && q <= g1 - 4 && q >= R.first[e] && q <= next - 4 && R.page[e] >= 0) {
+                const int32_t pos = R.len[e] + (q - R.first[e]), p = whole_pages(a, pos), off = pos - p * a.page_size;
+                if (off <= a.page_size - 4) {
+                    const int32_t held = R.held[e];
+                    int32_t* at = a.table + static_cast<int64_t>(i * kPagesThreads + e) * a.max_pages + p;
+                    const int32_t page = p < held ? *at : a.free_list[base + R.page[e] + (p - held)];
+                    if (p >= held && off == 0) *at = page;
+                    const int32_t slot = page * a.page_size + off;
+                    *reinterpret_cast<int4*>(a.slots + q) = make_int4(slot, slot + 1, slot + 2, slot + 3);
+                    if (a.positions) *reinterpret_cast<int4*>(a.positions + q) = make_int4(pos, pos + 1, pos + 2, pos + 3);
+                    continue;
                 }
             }
-            __syncthreads();
+            int32_t sl[4], po[4];
+            // a request's tokens one after another: a division and a look-up per page
+            int32_t pos = -1, off = 0, slot = -1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sl[j] = po[j] = -1;
+                if (q8 + j < g0 || q8 + j >= g1) continue;
+                const int32_t it = q + j;
+                bool look = pos < 0;
+                while (next <= it && e + 1 < kPagesThreads) {
+                    ++e;
+                    next = e + 1 < kPagesThreads ? R.first[e + 1] : 0x7FFFFFFF;
+                    look = true;
+                }
+                const int32_t before = R.page[e];
+                if (before < 0) {
+                    pos = -1;
+                    continue;
+                }
+                if (look) {
+                    pos = R.len[e] + (it - R.first[e]);
+                    off = pos - whole_pages(a, pos) * a.page_size;
+                } else {
+                    ++pos;
+                    ++slot;
+                    if (++off == a.page_size) off = 0;
+                }
+                if (look || off == 0) {
+                    const int32_t p = whole_pages(a, pos), held = R.held[e];
+                    int32_t* at = a.table + static_cast<int64_t>(i * kPagesThreads + e) * a.max_pages + p;
+                    const int32_t page = p < held ? *at : a.free_list[base + before + (p - held)];
+                    if (p >= held && off == 0) *at = page;       // a fresh page's first token is a new one
+                    slot = page * a.page_size + off;
+                }
+                sl[j] = slot;
+                po[j] = pos;
+            }
+            if (a.wide && q >= g0 && q + 4 <= g1) {
+                *reinterpret_cast<int4*>(a.slots + q) = make_int4(sl[0], sl[1], sl[2], sl[3]);
+                if (a.positions) *reinterpret_cast<int4*>(a.positions + q) = make_int4(po[0], po[1], po[2], po[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (q + j < g0 || q + j >= g1) continue;
+                    a.slots[q + j] = sl[j];
+                    if (a.positions) a.positions[q + j] = po[j];
+                }
+            }
         }
     }
     if (!last_block(a.ticket)) return;
     // The new lengths and the free count, by the last block.
-    c_need = 0;
-    c_tok = 0;
+    scan.reset();
     for (int i = 0; i < rounds; ++i) {
         const int b = i * kPagesThreads + tid;
         if (rounds > 1) {
-            r = ask_extend(a, b);
-            tok_end = block_scan<int64_t>(r.count, s_tok, &c_tok);
-            if (r.bad == 0 && tok_end > a.max_tokens) {
-                r.bad = RSSM_DEV_PAGES_SLOTS;
-                r.need = 0;
-            }
-            upto = block_scan<int32_t>(r.need, s_need, &c_need);
+            extend_round(a, b, buf, scan, r, upto, tok_end);
             if (r.bad == 0 && r.need > 0 && upto > out) r.bad = RSSM_DEV_PAGES_EMPTY;
         }
         if (b < a.batch) {
@@ -281,50 +337,41 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
 }
 
 __global__ void __launch_bounds__(kPagesThreads) pages_shrink_kernel(const PagesArgs a) {
-    __shared__ int32_t s_back[32];
-    __shared__ Listed L;
+    __shared__ ScanBuf buf;
+    __shared__ Round R;
     const int tid = threadIdx.x;
     const int32_t nfree = *a.free_count;
     const int rounds = (a.batch + kPagesThreads - 1) / kPagesThreads;
-    int32_t c_back = 0;
+    Scan scan;
     Ask r{};
     int32_t upto = 0;
+    int64_t unused = 0;
     for (int i = 0; i < rounds; ++i) {
         r = ask_shrink(a, i * kPagesThreads + tid);
-        upto = block_scan<int32_t>(r.count, s_back, &c_back);
+        upto = r.count;
+        scan.run<false>(buf, upto, unused);
     }
     // never past the stack's end, whatever the lengths say
-    const int32_t total = min(c_back, a.num_pages - nfree);
+    const int32_t total = min(scan.cx, a.num_pages - nfree);
     const int32_t per = (total + gridDim.x - 1) / gridDim.x;
     const int32_t t0 = min(total, per * static_cast<int32_t>(blockIdx.x)), t1 = min(total, t0 + per);
-    int32_t c2 = 0;
+    if (rounds > 1) scan.reset();
     for (int i = 0; i < rounds; ++i) {
-        const int b = i * kPagesThreads + tid;
         if (rounds > 1) {
-            r = ask_shrink(a, b);
-            upto = block_scan<int32_t>(r.count, s_back, &c2);
+            __syncthreads();                                   // the round before is used up
+            r = ask_shrink(a, i * kPagesThreads + tid);
+            upto = r.count;
+            scan.run<false>(buf, upto, unused);
         }
-        const bool mine = r.count > 0 && upto - r.count < t1 && upto > t0;
-        int32_t zero = 0;
-        const int32_t at = block_scan<int32_t>(mine ? 1 : 0, s_back, &zero) - 1;
-        if (mine) {
-            L.first[at] = upto - r.count;
-            L.request[at] = b;
-            L.len[at] = pages_of(r.newlen, a.page_size);
-        }
-        if (tid == 0) L.n = zero;
+        R.first[tid] = upto - r.count;
+        R.held[tid] = pages_of(a, max(r.newlen, 0));
         __syncthreads();
-        if (zero > 0) {
-            const int32_t g0 = max(t0, static_cast<int32_t>(L.first[0]));
-            const int32_t g1 = min(t1, rounds > 1 ? c2 : c_back);
-            for (int32_t it = g0 + tid; it < g1; it += kPagesThreads) {
-                const int e = find_item(L, it);
-                int32_t* p = a.table + static_cast<int64_t>(L.request[e]) * a.max_pages + L.len[e] +
-                             (it - static_cast<int32_t>(L.first[e]));
-                a.free_list[nfree + it] = *p;
-                *p = -1;
-            }
-            __syncthreads();
+        const int32_t g0 = max(t0, R.first[0]), g1 = min(t1, scan.cx);
+        for (int32_t it = g0 + tid; it < g1; it += kPagesThreads) {
+            const int e = find_item(R, kPagesThreads, it);
+            int32_t* p = a.table + static_cast<int64_t>(i * kPagesThreads + e) * a.max_pages + R.held[e] + (it - R.first[e]);
+            a.free_list[nfree + it] = *p;
+            *p = -1;
         }
     }
     if (!last_block(a.ticket)) return;
@@ -336,6 +383,90 @@ __global__ void __launch_bounds__(kPagesThreads) pages_shrink_kernel(const Pages
         else a.lens[b] = r.newlen;
     }
     if (tid == 0) *a.free_count = nfree + total;
+}
+
+// A decode step's extend: T tokens (at most kStepTokens) for every request, a
+// thread a request, one block.
+__global__ void __launch_bounds__(kStepThreads) pages_step_kernel(const PagesArgs a) {
+    __shared__ ScanBuf buf;
+    __shared__ int32_t s_fit;
+    const int tid = threadIdx.x, n = blockDim.x;
+    const int32_t nfree = *a.free_count;
+    const int rounds = (a.batch + n - 1) / n;
+    if (tid == 0) s_fit = 0;
+    Scan scan;
+    Ask r{};
+    int32_t upto = 0;
+    int64_t unused = 0;
+    for (int i = 0; i < rounds; ++i) {
+        r = ask_extend(a, i * n + tid);
+        upto = r.need;
+        scan.run<false>(buf, upto, unused);
+        if (scan.cx > nfree && r.need > 0 && upto <= nfree) atomicMax(&s_fit, upto);
+        else if (scan.cx <= nfree && tid == 0) atomicMax(&s_fit, scan.cx);
+    }
+    int32_t out = scan.cx;
+    if (scan.cx > nfree) {                                     // uniform
+        __syncthreads();
+        out = s_fit;
+    }
+    const int32_t base = nfree - out;
+    scan.reset();
+    for (int i = 0; i < rounds; ++i) {
+        const int b = i * n + tid;
+        if (rounds > 1) {
+            r = ask_extend(a, b);
+            upto = r.need;
+            scan.run<false>(buf, upto, unused);
+        }
+        if (b >= a.batch) continue;
+        if (r.bad == 0 && r.need > 0 && upto > out) r.bad = RSSM_DEV_PAGES_EMPTY;
+        const int32_t held = pages_of(a, max(r.len, 0));
+        int32_t* row = a.table + static_cast<int64_t>(b) * a.max_pages;
+        int32_t* slots = a.slots + static_cast<int64_t>(b) * a.T;
+        int32_t p = whole_pages(a, max(r.len, 0)), off = r.len - p * a.page_size, page = -1;
+        if (r.bad == 0 && off > 0) page = row[p];
+        for (int t = 0; t < a.T; ++t) {
+            if (r.bad == 0 && off == 0) {
+                page = a.free_list[base + upto - r.need + (p - held)];
+                row[p] = page;
+            }
+            slots[t] = r.bad || page < 0 ? -1 : page * a.page_size + off;
+            if (a.positions) a.positions[static_cast<int64_t>(b) * a.T + t] = r.bad ? -1 : r.len + t;
+            if (++off == a.page_size) {
+                off = 0;
+                ++p;
+            }
+        }
+        if (r.bad) report_error(a.err, r.bad, b, a.T);
+        else a.lens[b] = r.len + a.T;
+    }
+    if (tid == 0) *a.free_count = base;                        // every thread read it before the scan's barrier
+}
+
+// A decode step's rollback: at most a few pages a request, one block.
+__global__ void __launch_bounds__(kStepThreads) pages_step_back_kernel(const PagesArgs a) {
+    __shared__ ScanBuf buf;
+    const int tid = threadIdx.x, n = blockDim.x;
+    const int32_t nfree = *a.free_count;
+    Scan scan;
+    int64_t unused = 0;
+    for (int i = 0; i * n < a.batch; ++i) {
+        const int b = i * n + tid;
+        const Ask r = ask_shrink(a, b);
+        int32_t upto = r.count;
+        scan.run<false>(buf, upto, unused);
+        if (b >= a.batch) continue;
+        int32_t* row = a.table + static_cast<int64_t>(b) * a.max_pages + pages_of(a, max(r.newlen, 0));
+        for (int j = 0; j < r.count; ++j) {
+            const int32_t at = nfree + upto - r.count + j;
+            if (at < a.num_pages) a.free_list[at] = row[j];    // never past the stack's end
+            row[j] = -1;
+        }
+        if (r.bad) report_error(a.err, r.bad, b, a.keep[b]);
+        else a.lens[b] = r.newlen;
+    }
+    if (tid == 0) *a.free_count = min(nfree + scan.cx, a.num_pages);
 }
 
 __global__ void pages_init_kernel(int32_t* lens, int batch, int32_t* table, int64_t entries, int32_t* free_list,
@@ -399,27 +530,41 @@ PagesArgs pages_args(const rssm_pages* h) {
     a.page_size = h->cfg.page_size;
     a.num_pages = h->cfg.num_pages;
     a.max_pages = h->cfg.max_pages;
+    a.shift = -1;
+    if ((a.page_size & (a.page_size - 1)) == 0)
+        for (a.shift = 0; (1 << a.shift) < a.page_size; ++a.shift) {}
     return a;
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Blocks for `items` items at most: one per kTokensPerBlock, two per SM at most.
+// Blocks for `items` items at most: one per kItemsPerBlock, two per SM at most.
 cudaError_t pages_grid(int64_t items, int* blocks) {
     int sms = 0, smem = 0;
     const cudaError_t e = device_limits(&sms, &smem);
     if (e != cudaSuccess) return e;
-    const int64_t want = (items + kTokensPerBlock - 1) / kTokensPerBlock;
+    const int64_t want = (items + kItemsPerBlock - 1) / kItemsPerBlock;
     *blocks = static_cast<int>(want < 1 ? 1 : want > 2 * sms ? 2 * sms : want);
     return cudaSuccess;
 }
+
+// Threads of a single-block kernel: one a request, in whole warps.
+int step_threads(int batch) { return batch >= kStepThreads ? kStepThreads : (batch + 31) / 32 * 32; }
+
+// Single-block kernels stay below the others' cost up to this many requests
+// (8 rounds of a scan).
+constexpr int kStepBatch = 8 * kStepThreads;
 
 rssm_status pages_shrink(rssm_pages* h, int32_t T, const int32_t* keep, void* stream) {
     PagesArgs a = pages_args(h);
     a.T = T;
     a.keep = keep;
+    if (T > 0 && T <= kStepTokens && a.batch <= kStepBatch) {
+        pages_step_back_kernel<<<1, step_threads(a.batch), 0, static_cast<cudaStream_t>(stream)>>>(a);
+        return cudaGetLastError() == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
+    }
     // a rollback returns at most ceil(T / page_size) pages a request
-    const int64_t per = T > 0 ? (T + h->cfg.page_size - 1) / h->cfg.page_size : h->cfg.max_pages;
+    const int64_t per = T > 0 ? (static_cast<int64_t>(T) + h->cfg.page_size - 1) / h->cfg.page_size : h->cfg.max_pages;
     const int64_t items = per * h->cfg.batch;
     int blocks = 1;
     cudaError_t e = pages_grid(items < h->cfg.num_pages ? items : h->cfg.num_pages, &blocks);
@@ -479,6 +624,10 @@ rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, in
     a.positions = d_positions;
     a.max_tokens = max_tokens;
     a.wide = ((reinterpret_cast<uintptr_t>(d_slots) | reinterpret_cast<uintptr_t>(d_positions)) & 15u) == 0;
+    if (d_new == nullptr && T <= kStepTokens && a.batch <= kStepBatch) {
+        pages_step_kernel<<<1, step_threads(a.batch), 0, static_cast<cudaStream_t>(stream)>>>(a);
+        return cudaGetLastError() == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
+    }
     int blocks = 1;
     cudaError_t e = pages_grid(d_new ? max_tokens : static_cast<int64_t>(T) * h->cfg.batch, &blocks);
     if (e == cudaSuccess) {

@@ -139,6 +139,32 @@ def test_many_blocks_and_unaligned_lists(cuda_lib, offset):
         m.check(pt)
 
 
+@pytest.mark.parametrize("batch,T,ps", [(9000, 3, 16), (40, 17, 16), (40, 300, 1), (1500, 16, 5)])
+def test_uniform_steps_of_either_kind(cuda_lib, batch, T, ps):
+    """Uniform extends and rollbacks past the single-block kernels' batch and tokens, and below."""
+    most = 2 + 2 * T // ps
+    num = batch * (1 + 2 * T // ps) - 3              # the last requests of the second round get none
+    order = list(range(num))
+    random.Random(1).shuffle(order)
+    pt, m = rssm.PageTable(batch, ps, num, most, free=_i32(order)), Model(batch, ps, num, most, order)
+    slots, pos = (torch.empty(batch * T, dtype=torch.int32, device="cuda") for _ in range(2))
+    for step in range(3):
+        pt.extend(slots, T=T, positions=pos)
+        s, p, served = m.extend([T] * batch, batch * T)
+        assert slots.tolist() == s and pos.tolist() == p
+        err = pt.get_error()
+        assert (err[0] == 0) == all(served) and err[1] == served.count(False)
+        m.check(pt)
+        if step == 1:
+            acc = [(b * 7) % (T + 1) if served[b] else T for b in range(batch)]
+            pt.rollback(T, _i32(acc))
+            short = [n < T for n in m.lens]          # never served: refused, and unchanged
+            assert pt.get_error()[1] == sum(short)
+            m.cut([n if x else n - T + a for n, a, x in zip(m.lens, acc, short)])
+            m.check(pt)
+    assert pt.get_error()[0] == 0
+
+
 def test_a_rejected_draft_round_leaves_no_trace(cuda_lib):
     batch, ps = 100, 16
     pt = rssm.PageTable(batch, ps, 500, 8)
