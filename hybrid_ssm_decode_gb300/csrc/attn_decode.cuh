@@ -140,11 +140,11 @@ __device__ __forceinline__ uint32_t tf32(float x) {
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
 }
-// x = hi + lo to 22 bits. A non-finite x stays in hi alone.
+// x = hi + lo to 22 bits: hi rounded, so that lo has either sign and cutting it
+// off at TF32's bits leaves no bias.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
     hi = tf32(x);
-    const float d = x - __uint_as_float(hi);
-    lo = tf32(d == d ? d : 0.f);
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xFFFFE000u;
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -416,7 +416,7 @@ struct Warp {
             // columns at a time, rounded into s by FP32 adds, and the two small
             // products apart from them.
             const int r = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
-            float small[2][4] = {};
+            float small[2][2][4] = {};
 #pragma unroll 1
             for (int i0 = 0; i0 < D / 8; i0 += 4) {
                 float lead[2][4] = {};
@@ -431,8 +431,8 @@ struct Warp {
                     for (int j = 0; j < 4; ++j) split_tf32(__uint_as_float(b[j]), bh[j], bl[j]);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        mma_tf32(small[j], al, bh[2 * j], bh[2 * j + 1]);
-                        mma_tf32(small[j], ah, bl[2 * j], bl[2 * j + 1]);
+                        mma_tf32(small[0][j], al, bh[2 * j], bh[2 * j + 1]);
+                        mma_tf32(small[1][j], ah, bl[2 * j], bl[2 * j + 1]);
                         mma_tf32(lead[j], ah, bh[2 * j], bh[2 * j + 1]);
                     }
                 }
@@ -444,7 +444,7 @@ struct Warp {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) s[j][x] += small[j][x];
+                for (int x = 0; x < 4; ++x) s[j][x] += small[0][j][x] + small[1][j][x];
         }
     }
 
@@ -629,9 +629,79 @@ struct Warp {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) mma_bf16(o[i + j], w.lo[0], v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
             }
+        } else if constexpr (KV == kF32) {
+            // short chains, as in scores(), four tiles beside each other
+#pragma unroll
+            for (int i = 0; i < kTiles; i += 4) {
+                float p[4][4] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[2][4], vh[2][4], vl[2][4];
+                    values(vb, i / 2, h, v[0]);
+                    values(vb, i / 2 + 1, h, v[1]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) split_tf32(__uint_as_float(v[j >> 2][j & 3]), vh[j >> 2][j & 3], vl[j >> 2][j & 3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_tf32(p[j], w.lo[h], vh[j >> 1][2 * (j & 1)], vh[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_tf32(p[j], w.hi[h], vl[j >> 1][2 * (j & 1)], vl[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_tf32(p[j], w.hi[h], vh[j >> 1][2 * (j & 1)], vh[j >> 1][2 * (j & 1) + 1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[i + (j >> 2)][j & 3] += p[j >> 2][j & 3];
+            }
         } else {
             each_value(vb, [&](int t, int h, uint32_t b0, uint32_t b1) { product(o[t], w, h, b0, b1); });
         }
+    }
+
+    // Mends the values of a masked group, of which all rows see the tokens
+    // all_lo..all_hi and draft t those to first_hi + t. `poison`: a bit per draft
+    // and column, and a word that says whether any is set. Not inlined: it runs
+    // once or twice a request.
+    __device__ __noinline__ static void mend(uint32_t vb, int all_lo, int all_hi, int first_hi, int T, int window,
+                                             uint32_t* poison) {
+        const int lane = threadIdx.x & 31;
+        constexpr int kChunks = S::RB / 16, kPer = 16 / S::kEsz;
+#pragma unroll 1
+        for (int i = lane; i < kAttnGroup * kChunks; i += 32) {
+            const int r = i / kChunks;
+            if (r >= all_lo && r <= all_hi) continue;
+            const uint32_t at = vb + swz<S>(r, i % kChunks);
+            // the drafts that see token r: the later ones at the end, the earlier ones at the window's start
+            const int t0 = max(0, r - first_hi), t1 = window > 0 ? min(T, r - first_hi + window) : T;
+            if (t0 >= t1) {
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+                continue;
+            }
+#pragma unroll 1
+            for (int e = 0; e < kPer; ++e) {
+                uint32_t v = 0;
+                bool bad;
+                if constexpr (KV == kF32) {
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + 4 * e) : "memory");
+                    bad = (v & 0x7F800000u) == 0x7F800000u;
+                } else if constexpr (KV == kBF16) {
+                    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(at + 2 * e) : "memory");
+                    bad = (v & 0x7F80u) == 0x7F80u;
+                } else {
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at + e) : "memory");
+                    bad = (v & 0x7Fu) == 0x7Fu;
+                }
+                if (!bad) continue;
+                const int d = (i % kChunks) * kPer + e;
+                for (int t = t0; t < t1; ++t) atomicOr(poison + t * (D / 32) + d / 32, 1u << (d % 32));
+                poison[kMaxDraft * (D / 32)] = 1;
+                if constexpr (KV == kF32) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * e), "r"(0) : "memory");
+                else if constexpr (KV == kBF16)
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * e), "h"(static_cast<uint16_t>(0)) : "memory");
+                else asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + e), "r"(0) : "memory");
+            }
+        }
+        __syncwarp();
+        // the next copy into the slot is another proxy's write
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
 
     // NG groups whose tokens all rows see.
