@@ -3,17 +3,19 @@
 #include <new>
 
 #include "attn.h"
+#include "overlap.cuh"
 
 namespace rssm {
 namespace {
 
 // New tokens' keys and values to their slots: one thread per VEC elements of K or V.
 template <class TI, class TO, int VEC>
-__global__ void __launch_bounds__(256) attn_append_kernel(const TI* __restrict__ k, const TI* __restrict__ v, int64_t k_stride,
-                                                          int64_t v_stride, const int32_t* __restrict__ slots, TO* kc, TO* vc,
+__global__ void __launch_bounds__(256) attn_append_kernel(const TI* k, const TI* v, int64_t k_stride,
+                                                          int64_t v_stride, const int32_t* slots, TO* kc, TO* vc,
                                                           const float* __restrict__ k_scale,
                                                           const float* __restrict__ v_scale, int tokens, int heads, int dim,
                                                           int page_size, int num_pages, int64_t page_stride, int32_t* err) {
+    after_predecessor();
     const int per_head = dim / VEC, per_token = heads * per_head;
     const int64_t n = static_cast<int64_t>(tokens) * per_token;
     const bool is_v = blockIdx.y == 1;
@@ -25,7 +27,7 @@ __global__ void __launch_bounds__(256) attn_append_kernel(const TI* __restrict__
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int tok = static_cast<int>(i / per_token), e = static_cast<int>(i - static_cast<int64_t>(tok) * per_token);
         const int head = e / per_head, d = (e - head * per_head) * VEC;
-        const int32_t slot = __ldg(slots + tok);
+        const int32_t slot = slots[tok];
         if (slot < 0) continue;
         const int page = slot / page_size;
         if (page >= num_pages) {
@@ -171,13 +173,11 @@ cudaError_t launch_append(const rssm_attn* h, int tokens, const void* k, int64_t
     const dim3 grid(static_cast<unsigned>(want < 8 * 152 ? want : 8 * 152), 2);
     int32_t* err = reinterpret_cast<int32_t*>(h->base + h->lay.err);
     auto go = [&](auto kernel) {
-        kernel<<<grid, 256, 0, s>>>(static_cast<const TI*>(k), static_cast<const TI*>(v), ks, vs, slots,
+        return launch_overlapped(kernel, grid, 256, 0, s, static_cast<const TI*>(k), static_cast<const TI*>(v), ks, vs, slots,
                                     static_cast<TO*>(h->k_cache), static_cast<TO*>(h->v_cache), h->k_scale, h->v_scale,
                                     tokens, c.kv_heads, c.head_dim, c.page_size, c.num_pages, h->page_stride, err);
     };
-    if (wide) go(attn_append_kernel<TI, TO, kWide>);
-    else go(attn_append_kernel<TI, TO, 1>);
-    return cudaGetLastError();
+    return wide ? go(attn_append_kernel<TI, TO, kWide>) : go(attn_append_kernel<TI, TO, 1>);
 }
 
 }  // namespace

@@ -40,6 +40,7 @@
 #pragma once
 
 #include "attn.h"
+#include "overlap.cuh"
 
 namespace rssm {
 namespace attn {
@@ -204,7 +205,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
     Span s;
     const int most = a.max_pages * a.page_size;
-    int len = __ldg(a.lens + b);
+    const int len = __ldcg(a.lens + b);
     s.len = min(max(len, 0), most);
     const int64_t start = a.window > 0 ? static_cast<int64_t>(s.len) - a.T - a.window + 1 : 0;
     s.g0 = start > 0 ? static_cast<int>(start / kAttnGroup) : 0;
@@ -918,6 +919,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         fence_mbar_init();
     }
     __syncthreads();
+    after_predecessor();
 
     const int rows_all = a.T * a.group;
     int pos = 0, turn = 0;     // ring: the next group's slot, and how often the ring went round
@@ -925,6 +927,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
 
     if (warp == S::kConsumers) {
         // ---- producer ----
+        // what earlier kernels stored is read by copies, another proxy, from here on
+        asm volatile("fence.proxy.async.global;" ::: "memory");
         const uint32_t q_bytes = D * S::kQsz;
         Cursor cur;
         // The next part is found, and its first pages are looked up, before the
@@ -938,7 +942,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             const int tok = (base + lane) * kAttnGroup;
             const int at = tok / a.page_size;
             row = tok - at * a.page_size;
-            page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + at);
+            page = __ldcg(a.table + static_cast<int64_t>(b) * a.max_pages + at);
         };
         const auto find = [&]() -> bool {
             if (!cur.next(a)) return false;
@@ -971,7 +975,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
                 if (lane == 0) {
                     s_part[pq] = d;
                     if (d.at_start && d.pair == 0) {
-                        const int given = __ldg(a.lens + d.b);
+                        const int given = __ldcg(a.lens + d.b);
                         if (given != d.len) report_error(a.err, RSSM_DEV_ATTN_LEN, d.b, given);
                     }
                     mbar_arrive_expect_tx(qfull + pq, rows * q_bytes);
@@ -1214,8 +1218,7 @@ cudaError_t launch_shape(const AttnArgs& a, const CUtensorMap& k, const CUtensor
     e = cached_dyn_smem(lc, kernel, S::kSmem);
     if (e != cudaSuccess) return e;
     const int want = sms * S::kMinBlocks;
-    kernel<<<want < kAttnMaxGrid ? want : kAttnMaxGrid, S::kThreads, S::kSmem, s>>>(a, k, v);
-    return cudaGetLastError();
+    return launch_overlapped(kernel, want < kAttnMaxGrid ? want : kAttnMaxGrid, S::kThreads, S::kSmem, s, a, k, v);
 }
 
 template <int KV, int D>

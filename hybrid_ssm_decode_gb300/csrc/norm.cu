@@ -6,7 +6,7 @@
 // group of a row's columns (gated_norm) is held in registers, in FP32, from
 // its load through one or two sums of squares to its store. They are bound by
 // HBM for many rows and by latency for few.
-#include "common.cuh"
+#include "overlap.cuh"
 
 namespace rssm {
 namespace {
@@ -112,6 +112,7 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* s_red) {
 template <class TU, class TX, int VEC, int VPT>
 __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a, int tpr) {
     __shared__ float s_red[2][32];
+    after_predecessor();
     const int rows_per_block = blockDim.x / tpr;
     const int lane = threadIdx.x % tpr;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + threadIdx.x / tpr;
@@ -243,6 +244,7 @@ struct Raw {
 template <class T, int VEC, int VPT, int FIRST, int ACT>
 __global__ void __launch_bounds__(1024) gated_norm_kernel(const GatedNormArgs a, int tpr, uint32_t items) {
     __shared__ float s_red[2][32];
+    after_predecessor();
     const uint32_t per_block = blockDim.x / tpr, step = gridDim.x * per_block;
     const int lane = threadIdx.x % tpr;
     const uint32_t groups = a.groups;
@@ -369,15 +371,14 @@ template <class TU, class TX>
 cudaError_t launch_add(const AddNormArgs& a, int vec, const NormShape& s, cudaStream_t st) {
     const dim3 g(static_cast<unsigned>(s.blocks));
     if (vec == 8) {
-        if (s.vpt == 1) add_norm_kernel<TU, TX, 8, 1><<<g, s.threads, 0, st>>>(a, s.tpr);
-        else if (s.vpt == 2) add_norm_kernel<TU, TX, 8, 2><<<g, s.threads, 0, st>>>(a, s.tpr);
-        else add_norm_kernel<TU, TX, 8, 4><<<g, s.threads, 0, st>>>(a, s.tpr);
+        if (s.vpt == 1) return launch_overlapped(add_norm_kernel<TU, TX, 8, 1>, g, s.threads, 0, st, a, s.tpr);
+        else if (s.vpt == 2) return launch_overlapped(add_norm_kernel<TU, TX, 8, 2>, g, s.threads, 0, st, a, s.tpr);
+        else return launch_overlapped(add_norm_kernel<TU, TX, 8, 4>, g, s.threads, 0, st, a, s.tpr);
     } else {
-        if (s.vpt == 2) add_norm_kernel<TU, TX, 1, 2><<<g, s.threads, 0, st>>>(a, s.tpr);
-        else if (s.vpt == 8) add_norm_kernel<TU, TX, 1, 8><<<g, s.threads, 0, st>>>(a, s.tpr);
-        else add_norm_kernel<TU, TX, 1, 32><<<g, s.threads, 0, st>>>(a, s.tpr);
+        if (s.vpt == 2) return launch_overlapped(add_norm_kernel<TU, TX, 1, 2>, g, s.threads, 0, st, a, s.tpr);
+        else if (s.vpt == 8) return launch_overlapped(add_norm_kernel<TU, TX, 1, 8>, g, s.threads, 0, st, a, s.tpr);
+        else return launch_overlapped(add_norm_kernel<TU, TX, 1, 32>, g, s.threads, 0, st, a, s.tpr);
     }
-    return cudaGetLastError();
 }
 
 template <class T, int FIRST, int ACT>
@@ -389,15 +390,14 @@ cudaError_t launch_gated_as(const GatedNormArgs& a, int vec, const NormShape& s,
     const int64_t most = static_cast<int64_t>(sms) * (1024 / s.threads);
     const dim3 g(static_cast<unsigned>(s.blocks < most ? s.blocks : most));
     if (vec == 8) {
-        if (s.vpt == 1) gated_norm_kernel<T, 8, 1, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
-        else if (s.vpt == 2) gated_norm_kernel<T, 8, 2, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
-        else gated_norm_kernel<T, 8, 4, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
+        if (s.vpt == 1) return launch_overlapped(gated_norm_kernel<T, 8, 1, FIRST, ACT>, g, s.threads, 0, st, a, s.tpr, items);
+        else if (s.vpt == 2) return launch_overlapped(gated_norm_kernel<T, 8, 2, FIRST, ACT>, g, s.threads, 0, st, a, s.tpr, items);
+        else return launch_overlapped(gated_norm_kernel<T, 8, 4, FIRST, ACT>, g, s.threads, 0, st, a, s.tpr, items);
     } else {
-        if (s.vpt == 2) gated_norm_kernel<T, 1, 2, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
-        else if (s.vpt == 8) gated_norm_kernel<T, 1, 8, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
-        else gated_norm_kernel<T, 1, 32, FIRST, ACT><<<g, s.threads, 0, st>>>(a, s.tpr, items);
+        if (s.vpt == 2) return launch_overlapped(gated_norm_kernel<T, 1, 2, FIRST, ACT>, g, s.threads, 0, st, a, s.tpr, items);
+        else if (s.vpt == 8) return launch_overlapped(gated_norm_kernel<T, 1, 8, FIRST, ACT>, g, s.threads, 0, st, a, s.tpr, items);
+        else return launch_overlapped(gated_norm_kernel<T, 1, 32, FIRST, ACT>, g, s.threads, 0, st, a, s.tpr, items);
     }
-    return cudaGetLastError();
 }
 
 template <class T>
