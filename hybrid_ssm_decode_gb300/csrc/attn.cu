@@ -61,7 +61,7 @@ size_t up256(size_t v) { return (v + kAttnAlign - 1) / kAttnAlign * kAttnAlign; 
 
 // Regions of the workspace.
 struct AttnLayout {
-    size_t err, arrived, part_ml, part_o, total;
+    size_t err, arrived, arrived_round, part_ml, part_o, total;
 };
 
 int elem_size(int kv_dtype) { return kv_dtype == RSSM_F32 ? 4 : kv_dtype == RSSM_BF16 ? 2 : 1; }
@@ -103,6 +103,7 @@ AttnLayout attn_layout(const rssm_attn_config& c) {
     auto take = [&](size_t bytes) { const size_t o = off; off += up256(bytes); return o; };
     L.err = take(16);
     L.arrived = take(4 * static_cast<size_t>(c.batch) * c.kv_heads * attn_chunks(rows, c));
+    L.arrived_round = take(4 * 2 * static_cast<size_t>(kAttnMaxGrid));
     L.part_ml = take(parts * 8);
     L.part_o = take(parts * c.head_dim * 4);
     L.total = off;
@@ -273,6 +274,7 @@ rssm_status rssm_attn_decode(rssm_attn* h, int32_t T, const void* d_q, int64_t q
     a.v_scale = h->v_scale;
     a.err = reinterpret_cast<int32_t*>(h->base + h->lay.err);
     a.arrived = reinterpret_cast<uint32_t*>(h->base + h->lay.arrived);
+    a.arrived_round = reinterpret_cast<uint32_t*>(h->base + h->lay.arrived_round);
     a.part_ml = reinterpret_cast<float2*>(h->base + h->lay.part_ml);
     a.part_o = reinterpret_cast<float*>(h->base + h->lay.part_o);
     a.B = c.batch;

@@ -22,6 +22,7 @@ struct AttnArgs {
     const float* v_scale;
     int32_t* err;
     uint32_t* arrived;          // [B][kv_heads][chunks], 0 between launches
+    uint32_t* arrived_round;    // [2 blocks], by the slot of a round's first part, 0 between launches
     float2* part_ml;            // [2 blocks][rows]: maximum and sum of a part
     float* part_o;              // [2 blocks][rows][D]
     int B, q_heads, kv_heads, group, T, chunks;   // chunks: of the T*group query rows, per cache head

@@ -15,7 +15,10 @@
 // equal shares, one per block. A share may begin and end inside a request; those
 // at most two parts go to the workspace, and the last of a request's parts to
 // arrive joins them in the order of the tokens (no float atomics: reruns give the
-// same bits). SMs do not all see the same bandwidth: with equal shares the blocks
+// same bits). More than kJoin parts are joined in two steps, by rounds of kJoin
+// neighbours and then the rounds, so that few long requests do not wait for one
+// block to read hundreds of parts (FP8, 2 requests of 14k and 24k tokens, 15 rows
+// of 64: 46 -> 28 us; BF16, one request of 100k, 8 rows of 128: 81 -> 25 us). SMs do not all see the same bandwidth: with equal shares the blocks
 // of a launch end within 5 to 14 % of their mean. Small shares taken in turn from
 // the last sixth of the line lost more to the joins than they evened out (BF16,
 // 64 requests of 1000 to 9999 tokens, 32 rows of 256: 194 -> 258 us; FP8, 8
@@ -167,6 +170,14 @@ __device__ __forceinline__ uint32_t arrive_gpu(uint32_t* n) {
     uint32_t old;
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(n) : "memory");
     return old;
+}
+
+// Whether this arrival is the last, after `others` before it; then the counter is
+// back at zero.
+__device__ __forceinline__ bool arrive_last(uint32_t* n, int others) {
+    if (arrive_gpu(n) != static_cast<uint32_t>(others)) return false;
+    *n = 0;
+    return true;
 }
 
 // Whether `ok` holds for every thread at the named barrier.
@@ -810,79 +821,99 @@ __device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, 
 // Join the parts of a request and head: the consumer warps, once all have
 // arrived. Not inlined: it runs once or twice a block, and its registers are
 // not the stream's.
+constexpr int kJoin = 16;      // parts joined at a time
+
 template <int KV, class S>
-__device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, float* fw, float2* s_row) {
-    // Weights of the parts first (parts across the lanes, a warp a row at a
-    // time), then the outputs, with no product waiting for another.
+__device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, float* fw, float2* s_row, volatile int* s_last) {
     const int rows = min(S::kRows, a.T * a.group - part.row0);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int D = S::D, kThreads = S::kConsumers * 32;
+    static_assert((kAttnMaxGrid + kJoin - 1) / kJoin <= 32 && 32 <= S::OS, "a round of parts must fit a warp and the buffer");
     const int np = part.others + 1;
-    const auto part_at = [&](int p, int r) {
-        return (2 * static_cast<int64_t>(part.first + p) + (p == 0 ? 1 : 0)) * S::kRows + r;
-    };
-    // fw: [np][rows]
-    const bool fits = np * rows <= S::NB * S::kRows * S::OS;
-    for (int r = warp; r < rows; r += S::kConsumers) {
-        float M = -INFINITY, L = 0.f;
-        for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(a.part_ml + part_at(p, r)).x);
-        M = warp_max(M);
-        const float ref = M == -INFINITY ? 0.f : M;
-        for (int p = lane; p < np; p += 32) {
-            const float2 ml = __ldcg(a.part_ml + part_at(p, r));
-            const float fp = ex2(ml.x - ref);
-            L += ml.y * fp;
-            if (fits) fw[p * rows + r] = fp;
-        }
-        L = warp_sum(L);
-        if (lane == 0) s_row[r] = make_float2(M, L);
+    // this block's kJoin neighbours, and then one part for each such round; or all at once
+    int p0 = 0, step = 1, n = np;
+    bool final = np <= kJoin;
+    if (!final) {
+        p0 = (static_cast<int>(blockIdx.x) - part.first) / kJoin * kJoin;
+        n = min(kJoin, np - p0);
     }
-    named_sync(1, kThreads);
-    // 16 loads ahead: of one output where there is one a thread, else of four
-    const auto sums = [&](auto items_c, auto ahead_c) {
-        constexpr int kItems = decltype(items_c)::value, kAhead = decltype(ahead_c)::value;
-        const int items = rows * (D / 4);
-        for (int x0 = tid; x0 < items; x0 += kItems * kThreads) {
-            float4 acc[kItems];
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p0 = 0; p0 < np; p0 += kAhead) {
-                float4 v[kItems][kAhead];
-                float fp[kItems][kAhead];
-#pragma unroll
-                for (int i = 0; i < kItems; ++i)
-#pragma unroll
-                    for (int k = 0; k < kAhead; ++k) {
-                        const int x = x0 + i * kThreads, p = p0 + k;
-                        v[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        fp[i][k] = 0.f;
-                        if (x >= items || p >= np) continue;
-                        const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-                        v[i][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + part_at(p, r) * D + col));
-                        const float M = s_row[r].x;
-                        fp[i][k] = fits ? fw[p * rows + r] : ex2(__ldcg(a.part_ml + part_at(p, r)).x - (M == -INFINITY ? 0.f : M));
-                    }
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-                    for (int i = 0; i < kItems; ++i) {
-                        acc[i].x = fmaf(v[i][k].x, fp[i][k], acc[i].x);
-                        acc[i].y = fmaf(v[i][k].y, fp[i][k], acc[i].y);
-                        acc[i].z = fmaf(v[i][k].z, fp[i][k], acc[i].z);
-                        acc[i].w = fmaf(v[i][k].w, fp[i][k], acc[i].w);
-                    }
-            }
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int x = x0 + i * kThreads;
-                if (x >= items) break;
-                const int r = x / (D / 4);
-                put<KV, S>(a, part, r, (x % (D / 4)) * 4, acc[i], s_row[r].x, s_row[r].y);
-            }
+    for (;;) {
+        const auto part_at = [&](int i, int r) {              // part p0 + i step
+            const int p = p0 + i * step;
+            return (2 * static_cast<int64_t>(part.first + p) + (p == 0 ? 1 : 0)) * S::kRows + r;
+        };
+        // Weights of the parts first (parts across the lanes, a warp a row at a
+        // time), then the outputs, with no product waiting for another.
+        for (int r = warp; r < rows; r += S::kConsumers) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < n) ml = __ldcg(a.part_ml + part_at(lane, r));
+            const float M = warp_max(ml.x);
+            const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+            if (lane < n) fw[lane * rows + r] = f;            // [n][rows]
+            const float L = warp_sum(ml.y * f);
+            if (lane == 0) s_row[r] = make_float2(M, L);
         }
-    };
-    if (rows * (D / 4) <= kThreads) sums(Int<1>{}, Int<16>{});
-    else sums(Int<4>{}, Int<4>{});
+        named_sync(1, kThreads);
+        // 16 loads ahead: of one output where there is one a thread, else of four
+        const auto sums = [&](auto items_c, auto ahead_c) {
+            constexpr int kItems = decltype(items_c)::value, kAhead = decltype(ahead_c)::value;
+            const int items = rows * (D / 4);
+            for (int x0 = tid; x0 < items; x0 += kItems * kThreads) {
+                float4 acc[kItems];
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int q = 0; q < n; q += kAhead) {
+                    float4 v[kItems][kAhead];
+                    float fp[kItems][kAhead];
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) {
+                            const int x = x0 + i * kThreads;
+                            v[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            fp[i][k] = 0.f;
+                            if (x >= items || q + k >= n) continue;
+                            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+                            v[i][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + part_at(q + k, r) * D + col));
+                            fp[i][k] = fw[(q + k) * rows + r];
+                        }
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                        for (int i = 0; i < kItems; ++i) {
+                            acc[i].x = fmaf(v[i][k].x, fp[i][k], acc[i].x);
+                            acc[i].y = fmaf(v[i][k].y, fp[i][k], acc[i].y);
+                            acc[i].z = fmaf(v[i][k].z, fp[i][k], acc[i].z);
+                            acc[i].w = fmaf(v[i][k].w, fp[i][k], acc[i].w);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int x = x0 + i * kThreads;
+                    if (x >= items) break;
+                    const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+                    if (final) {
+                        put<KV, S>(a, part, r, col, acc[i], s_row[r].x, s_row[r].y);
+                    } else {
+                        // into the round's first part, which only this thread still reads here
+                        __stcg(reinterpret_cast<float4*>(a.part_o + part_at(0, r) * D + col), acc[i]);
+                        if (col == 0) __stcg(a.part_ml + part_at(0, r), s_row[r]);
+                    }
+                }
+            }
+        };
+        if (rows * (D / 4) <= kThreads) sums(Int<1>{}, Int<16>{});
+        else sums(Int<4>{}, Int<4>{});
+        if (final) return;
+        named_sync(1, kThreads);
+        if (tid == 0) *s_last = arrive_last(a.arrived + static_cast<int64_t>(part.b) * a.kv_heads * a.chunks + part.pair, (np - 1) / kJoin);
+        named_sync(1, kThreads);
+        if (!*s_last) return;
+        p0 = 0;
+        step = kJoin;
+        n = (np + kJoin - 1) / kJoin;
+        final = true;
+    }
 }
 
 // ---- the kernel --------------------------------------------------------------
@@ -1053,10 +1084,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     Part left;
     left.pair = -1;
     const auto count_left = [&] {                            // thread 0, after a block barrier
-        uint32_t* n = a.arrived + static_cast<int64_t>(left.b) * a.kv_heads * a.chunks + left.pair;
-        const bool last = arrive_gpu(n) == static_cast<uint32_t>(left.others);
-        if (last) *n = 0;
-        *s_last = last;
+        if (left.others < kJoin) {
+            *s_last = arrive_last(a.arrived + static_cast<int64_t>(left.b) * a.kv_heads * a.chunks + left.pair, left.others);
+        } else {
+            const int p = static_cast<int>(blockIdx.x) - left.first, p0 = p / kJoin * kJoin;
+            *s_last = arrive_last(a.arrived_round + 2 * (left.first + p0) + (p0 == 0 ? 1 : 0),
+                                  min(kJoin, left.others + 1 - p0) - 1);
+        }
     };
     for (;;) {
         const int pq = parts & 1;
@@ -1195,7 +1229,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         }
         if (left.pair >= 0) {
             named_sync(1, kThreads);                          // the buffers are read
-            if (*s_last) join_parts<KV, S>(a, left, merged, s_row);
+            if (*s_last) join_parts<KV, S>(a, left, merged, s_row, s_last);
         }
         left = part;
         if (part.others == 0) left.pair = -1;
@@ -1203,7 +1237,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     if (left.pair >= 0) {
         if (tid == 0) count_left();
         named_sync(1, kThreads);
-        if (*s_last) join_parts<KV, S>(a, left, merged, s_row);
+        if (*s_last) join_parts<KV, S>(a, left, merged, s_row, s_last);
     }
 }
 
