@@ -23,7 +23,8 @@ namespace rssm {
 namespace {
 
 constexpr int kPagesThreads = 512;      // of the kernels that share items out
-constexpr int kItemsPerBlock = 2048;    // four a thread
+constexpr int kItemsPerBlock = 2048;
+constexpr int kRun = 8;                 // tokens that a thread takes in a row
 constexpr int kStepThreads = 1024;      // most of the single-block kernels
 constexpr int kStepTokens = 16;         // most tokens a request that those take
 
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
     __syncthreads();
     const int32_t out = s_fit, base = nfree - out;
     const int64_t total = min(scan.cy, static_cast<int64_t>(a.max_tokens));
-    const int64_t per = ((total + gridDim.x - 1) / gridDim.x + 3) / 4 * 4;
+    const int64_t per = ((total + gridDim.x - 1) / gridDim.x + kRun - 1) / kRun * kRun;
     const int32_t t0 = static_cast<int32_t>(min(total, per * blockIdx.x)), t1 = static_cast<int32_t>(min(total, t0 + per));
 
     // The requests again, in order, now with what each one gets (with one round
@@ -249,73 +250,57 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
         const int32_t g0 = max(t0, R.first[0]), g1 = static_cast<int32_t>(min(static_cast<int64_t>(t1), rounds > 1 ? scan.cy : total));
         int e = -1;
         int32_t next = 0;
-        for (int64_t q8 = g0 / 4 * 4 + 4 * tid; q8 < g1; q8 += 4 * kPagesThreads) {
+        for (int64_t q8 = g0 / kRun * kRun + kRun * tid; q8 < g1; q8 += kRun * kPagesThreads) {
             const int32_t q = static_cast<int32_t>(q8);
-            // in a long prompt the next four tokens are the same request's, and mostly one page's
             if (max(q, g0) >= next || e < 0) {
                 e = find_item(R, kPagesThreads, max(q, g0));
                 next = e + 1 < kPagesThreads ? R.first[e + 1] : 0x7FFFFFFF;
             }
-            if (a.wide && q >= g0 && q <= g1 - 4 && q >= R.first[e] && q <= next - 4 && R.page[e] >= 0) {
+            // In a long prompt the next kRun tokens are the same request's, of one page or
+            // of two. (Every warp meets a page's end: the path must take it.)
+            if (a.wide && q >= g0 && q <= g1 - kRun && q >= R.first[e] && q <= next - kRun && R.page[e] >= 0 &&
+                a.page_size >= kRun) {
                 const int32_t pos = R.len[e] + (q - R.first[e]), p = whole_pages(a, pos), off = pos - p * a.page_size;
-                if (off <= a.page_size - 4) {
-                    const int32_t held = R.held[e];
-                    int32_t* at = a.table + static_cast<int64_t>(i * kPagesThreads + e) * a.max_pages + p;
-                    const int32_t page = p < held ? *at : a.free_list[base + R.page[e] + (p - held)];
-                    if (p >= held && off == 0) *at = page;
-                    const int32_t slot = page * a.page_size + off;
-                    *reinterpret_cast<int4*>(a.slots + q) = make_int4(slot, slot + 1, slot + 2, slot + 3);
-                    if (a.positions) *reinterpret_cast<int4*>(a.positions + q) = make_int4(pos, pos + 1, pos + 2, pos + 3);
-                    continue;
-                }
-            }
-            int32_t sl[4], po[4];
-            // a request's tokens one after another: a division and a look-up per page
-            int32_t pos = -1, off = 0, slot = -1;
+                const int32_t left = a.page_size - off;          // tokens to the page's end
+                const int32_t held = R.held[e], fresh = base + R.page[e] - held;
+                int32_t* row = a.table + static_cast<int64_t>(i * kPagesThreads + e) * a.max_pages + p;
+                const int32_t p1 = left < kRun ? p + 1 : p;
+                const int32_t id0 = p < held ? row[0] : a.free_list[fresh + p];
+                const int32_t id1 = p1 < held ? row[p1 - p] : a.free_list[fresh + p1];
+                // a fresh page's first token is a new one, so the page is entered with it
+                if (p >= held && off == 0) row[0] = id0;
+                if (p1 > p && p1 >= held) row[1] = id1;
+                const int32_t s0 = id0 * a.page_size + off, s1 = id1 * a.page_size - left;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sl[j] = po[j] = -1;
-                if (q8 + j < g0 || q8 + j >= g1) continue;
-                const int32_t it = q + j;
-                bool look = pos < 0;
-                while (next <= it && e + 1 < kPagesThreads) {
-                    ++e;
-                    next = e + 1 < kPagesThreads ? R.first[e + 1] : 0x7FFFFFFF;
-                    look = true;
+                for (int j = 0; j < kRun; j += 4) {
+                    *reinterpret_cast<int4*>(a.slots + q + j) =
+                        make_int4((j < left ? s0 : s1) + j, (j + 1 < left ? s0 : s1) + j + 1, (j + 2 < left ? s0 : s1) + j + 2,
+                                  (j + 3 < left ? s0 : s1) + j + 3);
+                    if (a.positions)
+                        *reinterpret_cast<int4*>(a.positions + q + j) = make_int4(pos + j, pos + j + 1, pos + j + 2, pos + j + 3);
                 }
-                const int32_t before = R.page[e];
-                if (before < 0) {
-                    pos = -1;
-                    continue;
+                continue;
+            }
+            // token by token
+            int cur = e;
+            int32_t upto_next = next;
+#pragma unroll 1
+            for (int32_t it = max(q, g0); it < g1 && it < q8 + kRun; ++it) {
+                while (upto_next <= it && cur + 1 < kPagesThreads) {
+                    ++cur;
+                    upto_next = cur + 1 < kPagesThreads ? R.first[cur + 1] : 0x7FFFFFFF;
                 }
-                if (look) {
-                    pos = R.len[e] + (it - R.first[e]);
-                    off = pos - whole_pages(a, pos) * a.page_size;
-                } else {
-                    ++pos;
-                    ++slot;
-                    if (++off == a.page_size) off = 0;
-                }
-                if (look || off == 0) {
-                    const int32_t p = whole_pages(a, pos), held = R.held[e];
-                    int32_t* at = a.table + static_cast<int64_t>(i * kPagesThreads + e) * a.max_pages + p;
-                    const int32_t page = p < held ? *at : a.free_list[base + before + (p - held)];
-                    if (p >= held && off == 0) *at = page;       // a fresh page's first token is a new one
+                int32_t slot = -1, pos = -1;
+                if (R.page[cur] >= 0) {
+                    pos = R.len[cur] + (it - R.first[cur]);
+                    const int32_t p = whole_pages(a, pos), off = pos - p * a.page_size, held = R.held[cur];
+                    int32_t* at = a.table + static_cast<int64_t>(i * kPagesThreads + cur) * a.max_pages + p;
+                    const int32_t page = p < held ? *at : a.free_list[base + R.page[cur] + (p - held)];
+                    if (p >= held && off == 0) *at = page;
                     slot = page * a.page_size + off;
                 }
-                sl[j] = slot;
-                po[j] = pos;
-            }
-            if (a.wide && q >= g0 && q + 4 <= g1) {
-                *reinterpret_cast<int4*>(a.slots + q) = make_int4(sl[0], sl[1], sl[2], sl[3]);
-                if (a.positions) *reinterpret_cast<int4*>(a.positions + q) = make_int4(po[0], po[1], po[2], po[3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (q + j < g0 || q + j >= g1) continue;
-                    a.slots[q + j] = sl[j];
-                    if (a.positions) a.positions[q + j] = po[j];
-                }
+                a.slots[it] = slot;
+                if (a.positions) a.positions[it] = pos;
             }
         }
     }
