@@ -22,7 +22,7 @@
 namespace rssm {
 namespace {
 
-constexpr int kPagesThreads = 512;      // of the kernels that share items out
+constexpr int kPagesThreads = 1024;     // most of the kernels that share items out; 512 where a round holds the batch
 constexpr int kItemsPerBlock = 2048;
 constexpr int kRun = 8;                 // tokens that a thread takes in a row
 constexpr int kStepThreads = 1024;      // most of the single-block kernels
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
     __shared__ ScanBuf buf;
     __shared__ int32_t s_fit;
     __shared__ Round R;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, nthr = blockDim.x;
     const int32_t nfree = *a.free_count;
-    const int rounds = (a.batch + kPagesThreads - 1) / kPagesThreads;
+    const int rounds = (a.batch + nthr - 1) / nthr;
 
     // Total tokens, and the pages that go out: all that are asked for, or else
     // the largest scan value that the pool covers (the scan grows, so the requests
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
     int32_t upto = 0;
     int64_t tok_end = 0;
     for (int i = 0; i < rounds; ++i) {
-        extend_round(a, i * kPagesThreads + tid, buf, scan, r, upto, tok_end);
+        extend_round(a, i * nthr + tid, buf, scan, r, upto, tok_end);
         if (scan.cx > nfree && r.need > 0 && upto <= nfree) atomicMax(&s_fit, upto);
         else if (scan.cx <= nfree && tid == 0) atomicMax(&s_fit, scan.cx);
     }
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
     for (int i = 0; i < rounds; ++i) {
         if (rounds > 1) {
             __syncthreads();                                   // the round before is used up
-            extend_round(a, i * kPagesThreads + tid, buf, scan, r, upto, tok_end);
+            extend_round(a, i * nthr + tid, buf, scan, r, upto, tok_end);
         }
         if (r.bad == 0 && r.need > 0 && upto > out) r.bad = RSSM_DEV_PAGES_EMPTY;
         R.first[tid] = static_cast<int32_t>(min(tok_end - r.count, static_cast<int64_t>(0x7FFFFFFF)));
@@ -250,11 +250,11 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
         const int32_t g0 = max(t0, R.first[0]), g1 = static_cast<int32_t>(min(static_cast<int64_t>(t1), rounds > 1 ? scan.cy : total));
         int e = -1;
         int32_t next = 0;
-        for (int64_t q8 = g0 / kRun * kRun + kRun * tid; q8 < g1; q8 += kRun * kPagesThreads) {
+        for (int64_t q8 = g0 / kRun * kRun + kRun * tid; q8 < g1; q8 += kRun * nthr) {
             const int32_t q = static_cast<int32_t>(q8);
             if (max(q, g0) >= next || e < 0) {
-                e = find_item(R, kPagesThreads, max(q, g0));
-                next = e + 1 < kPagesThreads ? R.first[e + 1] : 0x7FFFFFFF;
+                e = find_item(R, nthr, max(q, g0));
+                next = e + 1 < nthr ? R.first[e + 1] : 0x7FFFFFFF;
             }
             // In a long prompt the next kRun tokens are the same request's, of one page or
             // of two. (Every warp meets a page's end: the path must take it.)
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
                 const int32_t pos = R.len[e] + (q - R.first[e]), p = whole_pages(a, pos), off = pos - p * a.page_size;
                 const int32_t left = a.page_size - off;          // tokens to the page's end
                 const int32_t held = R.held[e], fresh = base + R.page[e] - held;
-                int32_t* row = a.table + static_cast<int64_t>(i * kPagesThreads + e) * a.max_pages + p;
+                int32_t* row = a.table + static_cast<int64_t>(i * nthr + e) * a.max_pages + p;
                 const int32_t p1 = left < kRun ? p + 1 : p;
                 const int32_t id0 = p < held ? row[0] : a.free_list[fresh + p];
                 const int32_t id1 = p1 < held ? row[p1 - p] : a.free_list[fresh + p1];
@@ -286,15 +286,15 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
             int32_t upto_next = next;
 #pragma unroll 1
             for (int32_t it = max(q, g0); it < g1 && it < q8 + kRun; ++it) {
-                while (upto_next <= it && cur + 1 < kPagesThreads) {
+                while (upto_next <= it && cur + 1 < nthr) {
                     ++cur;
-                    upto_next = cur + 1 < kPagesThreads ? R.first[cur + 1] : 0x7FFFFFFF;
+                    upto_next = cur + 1 < nthr ? R.first[cur + 1] : 0x7FFFFFFF;
                 }
                 int32_t slot = -1, pos = -1;
                 if (R.page[cur] >= 0) {
                     pos = R.len[cur] + (it - R.first[cur]);
                     const int32_t p = whole_pages(a, pos), off = pos - p * a.page_size, held = R.held[cur];
-                    int32_t* at = a.table + static_cast<int64_t>(i * kPagesThreads + cur) * a.max_pages + p;
+                    int32_t* at = a.table + static_cast<int64_t>(i * nthr + cur) * a.max_pages + p;
                     const int32_t page = p < held ? *at : a.free_list[base + R.page[cur] + (p - held)];
                     if (p >= held && off == 0) *at = page;
                     slot = page * a.page_size + off;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
     // The new lengths and the free count, by the last block.
     scan.reset();
     for (int i = 0; i < rounds; ++i) {
-        const int b = i * kPagesThreads + tid;
+        const int b = i * nthr + tid;
         if (rounds > 1) {
             extend_round(a, b, buf, scan, r, upto, tok_end);
             if (r.bad == 0 && r.need > 0 && upto > out) r.bad = RSSM_DEV_PAGES_EMPTY;
@@ -324,15 +324,15 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
 __global__ void __launch_bounds__(kPagesThreads) pages_shrink_kernel(const PagesArgs a) {
     __shared__ ScanBuf buf;
     __shared__ Round R;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, nthr = blockDim.x;
     const int32_t nfree = *a.free_count;
-    const int rounds = (a.batch + kPagesThreads - 1) / kPagesThreads;
+    const int rounds = (a.batch + nthr - 1) / nthr;
     Scan scan;
     Ask r{};
     int32_t upto = 0;
     int64_t unused = 0;
     for (int i = 0; i < rounds; ++i) {
-        r = ask_shrink(a, i * kPagesThreads + tid);
+        r = ask_shrink(a, i * nthr + tid);
         upto = r.count;
         scan.run<false>(buf, upto, unused);
     }
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_shrink_kernel(const Pages
     for (int i = 0; i < rounds; ++i) {
         if (rounds > 1) {
             __syncthreads();                                   // the round before is used up
-            r = ask_shrink(a, i * kPagesThreads + tid);
+            r = ask_shrink(a, i * nthr + tid);
             upto = r.count;
             scan.run<false>(buf, upto, unused);
         }
@@ -352,16 +352,16 @@ __global__ void __launch_bounds__(kPagesThreads) pages_shrink_kernel(const Pages
         R.held[tid] = pages_of(a, max(r.newlen, 0));
         __syncthreads();
         const int32_t g0 = max(t0, R.first[0]), g1 = min(t1, scan.cx);
-        for (int32_t it = g0 + tid; it < g1; it += kPagesThreads) {
-            const int e = find_item(R, kPagesThreads, it);
-            int32_t* p = a.table + static_cast<int64_t>(i * kPagesThreads + e) * a.max_pages + R.held[e] + (it - R.first[e]);
+        for (int32_t it = g0 + tid; it < g1; it += nthr) {
+            const int e = find_item(R, nthr, it);
+            int32_t* p = a.table + static_cast<int64_t>(i * nthr + e) * a.max_pages + R.held[e] + (it - R.first[e]);
             a.free_list[nfree + it] = *p;
             *p = -1;
         }
     }
     if (!last_block(a.ticket)) return;
     for (int i = 0; i < rounds; ++i) {
-        const int b = i * kPagesThreads + tid;
+        const int b = i * nthr + tid;
         if (rounds > 1) r = ask_shrink(a, b);
         if (b >= a.batch) continue;
         if (r.bad) report_error(a.err, r.bad, b, a.keep[b]);
@@ -535,6 +535,8 @@ cudaError_t pages_grid(int64_t items, int* blocks) {
     return cudaSuccess;
 }
 
+int pages_threads(int batch) { return batch <= kPagesThreads / 2 ? kPagesThreads / 2 : kPagesThreads; }
+
 // Threads of a single-block kernel: one a request, in whole warps.
 int step_threads(int batch) { return batch >= kStepThreads ? kStepThreads : (batch + 31) / 32 * 32; }
 
@@ -555,7 +557,7 @@ rssm_status pages_shrink(rssm_pages* h, int32_t T, const int32_t* keep, void* st
     int blocks = 1;
     cudaError_t e = pages_grid(items < h->cfg.num_pages ? items : h->cfg.num_pages, &blocks);
     if (e == cudaSuccess) {
-        pages_shrink_kernel<<<blocks, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        pages_shrink_kernel<<<blocks, pages_threads(a.batch), 0, static_cast<cudaStream_t>(stream)>>>(a);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
@@ -618,7 +620,7 @@ rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, in
     // a plain launch: beside the end of a shrink, the blocks that come early crowd
     // onto the SMs that are free (29 -> 39 us for 256 prompts)
     if (e == cudaSuccess) {
-        pages_extend_kernel<<<blocks, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        pages_extend_kernel<<<blocks, pages_threads(a.batch), 0, static_cast<cudaStream_t>(stream)>>>(a);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
