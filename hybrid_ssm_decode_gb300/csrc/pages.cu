@@ -8,7 +8,7 @@
 //
 // A decode step (the same few tokens for every request) is a single block, a
 // thread a request: bound by latency, of which a scan is one barrier. Prompts and
-// ended requests take a block per 2048 items, up to two per SM: every block makes
+// ended requests take a block per 1024 items, up to two per SM: every block makes
 // the whole scan for itself, which costs it one pass over 8 bytes a request from L2,
 // and then takes an equal share of the items. So one launch does it without any
 // block waiting for another; the last block to have read the lengths (a ticket)
@@ -23,7 +23,11 @@ namespace rssm {
 namespace {
 
 constexpr int kPagesThreads = 1024;     // most of the kernels that share items out; 512 where a round holds the batch
-constexpr int kItemsPerBlock = 2048;
+constexpr int kItemsPerBlock = 1024;
+// Unused shared memory of the kernels that share items out, so that no SM takes more
+// than two of their blocks: beside the end of the kernel before, early blocks would
+// crowd onto the SMs that are free (256 prompts: 39 us; plain launches 26; this 23).
+constexpr int kSpread = 88 * 1024;
 constexpr int kRun = 8;                 // tokens that a thread takes in a row
 constexpr int kStepThreads = 1024;      // most of the single-block kernels
 constexpr int kStepTokens = 16;         // most tokens a request that those take
@@ -210,6 +214,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
     __shared__ ScanBuf buf;
     __shared__ int32_t s_fit;
     __shared__ Round R;
+    after_predecessor();
     const int tid = threadIdx.x, nthr = blockDim.x;
     const int32_t nfree = *a.free_count;
     const int rounds = (a.batch + nthr - 1) / nthr;
@@ -324,6 +329,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
 __global__ void __launch_bounds__(kPagesThreads) pages_shrink_kernel(const PagesArgs a) {
     __shared__ ScanBuf buf;
     __shared__ Round R;
+    after_predecessor();
     const int tid = threadIdx.x, nthr = blockDim.x;
     const int32_t nfree = *a.free_count;
     const int rounds = (a.batch + nthr - 1) / nthr;
@@ -557,8 +563,9 @@ rssm_status pages_shrink(rssm_pages* h, int32_t T, const int32_t* keep, void* st
     int blocks = 1;
     cudaError_t e = pages_grid(items < h->cfg.num_pages ? items : h->cfg.num_pages, &blocks);
     if (e == cudaSuccess) {
-        pages_shrink_kernel<<<blocks, pages_threads(a.batch), 0, static_cast<cudaStream_t>(stream)>>>(a);
-        e = cudaGetLastError();
+        static LaunchCache lc;
+        e = cached_dyn_smem(lc, pages_shrink_kernel, kSpread);
+        if (e == cudaSuccess) e = launch_overlapped(pages_shrink_kernel, blocks, pages_threads(a.batch), kSpread, static_cast<cudaStream_t>(stream), a);
     }
     return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }
@@ -617,11 +624,10 @@ rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, in
     }
     int blocks = 1;
     cudaError_t e = pages_grid(d_new ? max_tokens : static_cast<int64_t>(T) * h->cfg.batch, &blocks);
-    // a plain launch: beside the end of a shrink, the blocks that come early crowd
-    // onto the SMs that are free (29 -> 39 us for 256 prompts)
     if (e == cudaSuccess) {
-        pages_extend_kernel<<<blocks, pages_threads(a.batch), 0, static_cast<cudaStream_t>(stream)>>>(a);
-        e = cudaGetLastError();
+        static LaunchCache lc;
+        e = cached_dyn_smem(lc, pages_extend_kernel, kSpread);
+        if (e == cudaSuccess) e = launch_overlapped(pages_extend_kernel, blocks, pages_threads(a.batch), kSpread, static_cast<cudaStream_t>(stream), a);
     }
     return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }
