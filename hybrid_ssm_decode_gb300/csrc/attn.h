@@ -10,6 +10,7 @@ namespace rssm {
 constexpr int kAttnMaxGrid = 304;    // blocks of one launch at most: two per SM
 constexpr int kAttnGroup = 16;       // tokens that one warp takes at a time
 constexpr int kAttnUnit = 4;         // groups in the unit by which work is shared out
+constexpr int kEvenUnits = 8;        // units a block below which few requests are cut evenly (attn_decode.cuh)
 
 struct AttnArgs {
     const void* q;

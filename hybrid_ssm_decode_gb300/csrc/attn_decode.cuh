@@ -237,6 +237,8 @@ struct Cursor {
     Span sp;
     int pair, u0, u1;            // the current part
     bool fresh;
+    bool even, only;             // requests cut evenly; the block's one part is not taken yet
+    int first, others;           // then: the block of its request's first part, the parts beside it
 
     // False for a block without a share.
     __device__ __forceinline__ bool start(const AttnArgs& a, int lane) {
@@ -254,8 +256,46 @@ struct Cursor {
             if (lane >= o) incl += n;
         }
         total = __shfl_sync(0xffffffffu, incl, 31) * heads;
-        grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-        const int c = blockIdx.x;
+        const int c = blockIdx.x, blocks = gridDim.x;
+        even = only = false;
+        // Little work for few requests: a share that ends inside one request and begins
+        // the next costs a second part, so every request and head is cut into even
+        // parts of its own, a block each. (FP32, 4 requests of 8 heads of up to 2047
+        // tokens: 18.2 -> 15.7 us; BF16, 4 of up to 4000: 17.6 -> 14.6. With more
+        // units a block the parts' unevenness costs more than the second part: 8
+        // requests of 128k over 8 heads would take parts of 455 units against 383.)
+        if (a.B <= 32 && 2 * a.B * heads <= blocks && total < kEvenUnits * blocks) {
+            const int units = static_cast<int>(mine);
+            int size = static_cast<int>((total + blocks - 1) / blocks);   // units of a part
+            // at most twice that and one: parts <= total / size + requests and heads <= blocks
+            int n = (units + size - 1) / size;
+            while (__reduce_add_sync(0xffffffffu, n) * heads > blocks) {
+                ++size;
+                n = (units + size - 1) / size;
+            }
+            int upto = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const unsigned has = __ballot_sync(0xffffffffu, n > 0 && (upto - n) * heads <= c);
+            const int src = 31 - __clz(has);
+            const int parts = __shfl_sync(0xffffffffu, n, src), r = c - __shfl_sync(0xffffffffu, upto - n, src) * heads;
+            if (c >= __shfl_sync(0xffffffffu, upto, 31) * heads) return false;
+            b = src;
+            sp = span_of(a, b);
+            pair = r / parts;
+            const int i = r - pair * parts;
+            first = c - i;
+            others = parts - 1;
+            u0 = i * size;
+            u1 = min(sp.units, u0 + size);
+            w = w1 = 0;
+            even = only = true;
+            return true;
+        }
+        grid = static_cast<int>(min(static_cast<int64_t>(blocks), total));
         if (c >= grid) return false;
         w = total * c / grid;
         w1 = total * (c + 1) / grid;
@@ -291,6 +331,10 @@ struct Cursor {
     // The next part of the share; false at its end. Parts after the first begin
     // with a request's first unit.
     __device__ __forceinline__ bool next(const AttnArgs& a) {
+        if (only) {
+            only = false;
+            return true;
+        }
         if (w >= w1) return false;
         if (fresh) {
             const int64_t r = w - base;
@@ -992,7 +1036,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             nd.pair = cur.pair;
             nd.first = nd.others = 0;
             nd.at_start = cur.u0 == 0;
-            if (cur.u1 - cur.u0 < cur.sp.units) {
+            if (cur.even) {
+                nd.first = cur.first;
+                nd.others = cur.others;
+            } else if (cur.u1 - cur.u0 < cur.sp.units) {
                 const int64_t first = cur.base + static_cast<int64_t>(cur.pair) * cur.sp.units;
                 nd.first = cur.owner(first);
                 nd.others = cur.owner(first + cur.sp.units - 1) - nd.first;
