@@ -230,6 +230,9 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
     return s;
 }
 
+// The first position that a token at position p sees (window 0: from the start).
+__device__ __forceinline__ int window_start(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
+
 // Walks the parts of the block's share; one warp.
 struct Cursor {
     int64_t total, w, w1, base;  // units: in all, next, end, before request b
@@ -717,54 +720,6 @@ struct Warp {
         }
     }
 
-    // Mends the values of a masked group, of which all rows see the tokens
-    // all_lo..all_hi and draft t those to first_hi + t. `poison`: a bit per draft
-    // and column, and a word that says whether any is set. Not inlined: it runs
-    // once or twice a request.
-    __device__ __noinline__ static void mend(uint32_t vb, int all_lo, int all_hi, int first_hi, int T, int window,
-                                             uint32_t* poison) {
-        const int lane = threadIdx.x & 31;
-        constexpr int kChunks = S::RB / 16, kPer = 16 / S::kEsz;
-#pragma unroll 1
-        for (int i = lane; i < kAttnGroup * kChunks; i += 32) {
-            const int r = i / kChunks;
-            if (r >= all_lo && r <= all_hi) continue;
-            const uint32_t at = vb + swz<S>(r, i % kChunks);
-            // the drafts that see token r: the later ones at the end, the earlier ones at the window's start
-            const int t0 = max(0, r - first_hi), t1 = window > 0 ? min(T, r - first_hi + window) : T;
-            if (t0 >= t1) {
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
-                continue;
-            }
-#pragma unroll 1
-            for (int e = 0; e < kPer; ++e) {
-                uint32_t v = 0;
-                bool bad;
-                if constexpr (KV == kF32) {
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + 4 * e) : "memory");
-                    bad = (v & 0x7F800000u) == 0x7F800000u;
-                } else if constexpr (KV == kBF16) {
-                    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(at + 2 * e) : "memory");
-                    bad = (v & 0x7F80u) == 0x7F80u;
-                } else {
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at + e) : "memory");
-                    bad = (v & 0x7Fu) == 0x7Fu;
-                }
-                if (!bad) continue;
-                const int d = (i % kChunks) * kPer + e;
-                for (int t = t0; t < t1; ++t) atomicOr(poison + t * (D / 32) + d / 32, 1u << (d % 32));
-                poison[kMaxDraft * (D / 32)] = 1;
-                if constexpr (KV == kF32) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * e), "r"(0) : "memory");
-                else if constexpr (KV == kBF16)
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * e), "h"(static_cast<uint16_t>(0)) : "memory");
-                else asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + e), "r"(0) : "memory");
-            }
-        }
-        __syncwarp();
-        // the next copy into the slot is another proxy's write
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-
     // NG groups whose tokens all rows see.
     template <int NG>
     __device__ __forceinline__ void step(const uint32_t (&kb)[NG], const uint32_t (&vb)[NG]) {
@@ -812,7 +767,7 @@ struct Warp {
         // by draft, with only that draft's tokens in place, into its rows alone
         for (int t = 0; t < T; ++t) {
             const int p = len - T + t;
-            const int a0 = window > 0 ? max(0, p - window + 1) - tok0 : 0, a1 = p - tok0;
+            const int a0 = window_start(p, window) - tok0, a1 = p - tok0;
             each_value(vb, [&](int tile, int h, uint32_t b0, uint32_t b1) {
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
                 product(acc, w, h, cut(b0, h, 0, a0, a1), cut(b1, h, 1, a0, a1));
@@ -1161,11 +1116,11 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             const int r = min(row0 + wm * 16 + wp.g + 8 * x, rows_all - 1);
             draft[x] = r / a.group;
             see_hi[x] = len - a.T + draft[x];
-            see_lo[x] = a.window > 0 ? max(0, see_hi[x] - a.window + 1) : 0;
+            see_lo[x] = window_start(see_hi[x], a.window);
         }
         const int all_hi = len - a.T;                             // the last token that all drafts see
-        const int all_lo = a.window > 0 ? max(0, len - a.window) : 0;   // and the first
-        const int some_lo = a.window > 0 ? max(0, len - a.T - a.window + 1) : 0;
+        const int all_lo = window_start(len - 1, a.window);         // and the first
+        const int some_lo = window_start(len - a.T, a.window);
         wp.reset();
         wp.load_q(qbuf + (pq * S::kRows + wm * 16) * S::QS, a.scale_log2, KV == kFP8 ? __ldg(a.k_scale + head) : 1.f);
         if (KV != kF32) {

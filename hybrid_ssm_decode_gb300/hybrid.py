@@ -83,6 +83,10 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+def _cuda(device, name):
+    _need(device.type == "cuda", f"{name}: on {device}, must be a CUDA device")
+
+
 def _on(t, device, name):
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, must be on {device}")
@@ -109,6 +113,7 @@ class PageTable:
         self.layout = _r.rssm_pages_layout_for(self.cfg)
         self.workspace = torch.empty(self.layout.total_bytes, dtype=torch.uint8, device=device)
         self.device = self.workspace.device
+        _cuda(self.device, "device")
         if free is not None:
             _ints(free, num_pages, self.device, "free")
         self.handle = _r.rssm_pages_create(self.cfg, self.workspace, self.layout.total_bytes, free, stream)
@@ -232,6 +237,7 @@ class Attention:
         _need(k_cache.dim() == 4, "k_cache: must be [num_pages][kv_heads][page_size][head_dim]")
         pages, heads, ps, dim = k_cache.shape
         self.device = k_cache.device
+        _cuda(self.device, "k_cache")
         for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
             _on(c, self.device, name)
             _need(c.dtype == k_cache.dtype and c.shape == k_cache.shape, f"{name}: k_cache and v_cache must be alike")
@@ -368,6 +374,7 @@ def _check_add(n_out, u, w, x, u_out, w_post, gate, scale, eps, w_offset):
     dim = u.shape[-1]
     rows = u.numel() // dim if dim else 0
     dev = u.device
+    _cuda(dev, "u")
     cfg = _r.AddNormConfig(rows=rows, dim=dim, res_dtype=_dtype(u, "u"), eps=eps, scale=scale, w_offset=w_offset,
                            u_stride=_rows(u, rows, dim, dev, "u"))
     kind = None
@@ -422,6 +429,7 @@ def _check_gated(out, y, z, w, group, norm_first, act, eps, w_offset):
     dim = y.shape[-1]
     rows = y.numel() // dim if dim else 0
     dev = y.device
+    _cuda(dev, "y")
     d = _dtype(y, "y")
     _need(z.dtype == y.dtype and out.dtype == y.dtype, "z and out: must have y's dtype")
     group = dim if group is None else group

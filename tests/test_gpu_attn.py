@@ -140,6 +140,12 @@ def test_windows(cuda_lib, kv, window, T):
     c.check(c.run())
 
 
+def test_a_window_longer_than_any_request(cuda_lib):
+    c = Case([1, 40, 300], T=3, q_heads=4, kv_heads=2, dim=64, seed=12)
+    for window in (300, 2 ** 31 - 1):
+        c.check(c.run(c.layer(window=window)))
+
+
 @pytest.mark.parametrize("lens,kv_heads,ps,kv", [
     ([20000], 1, 16, "bf16"), ([30001, 3], 2, 64, "fp8"), ([1], 1, 16, "bf16"), ([5000, 1, 0, 7777], 3, 48, "bf16"),
     ([3000] * 5, 2, 128, "f32"), ([(i * 37) % 200 for i in range(700)], 2, 16, "bf16"), ([0] * 40, 2, 16, "fp8")])

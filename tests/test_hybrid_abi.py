@@ -149,3 +149,18 @@ def test_norm_host_errors(lib):
     for k in ("y", "z", "w", "o"):
         assert gated(**{k: None}) == INVALID
     assert gated(rows=0, y=None, z=None, w=None, o=None) == OK
+
+
+def test_binding_refuses_cpu_tensors(lib):
+    """The checks come before any call of the library."""
+    import torch
+    x, w = torch.zeros(2, 64), torch.ones(64)
+    with pytest.raises(ValueError):
+        rssm.add_norm(x, x, w)
+    with pytest.raises(ValueError):
+        rssm.gated_norm(x, x, x, w)
+    cache = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        rssm.Attention(cache, cache, batch=1, q_heads=2, max_pages=2)
+    with pytest.raises(ValueError):
+        rssm.PageTable(2, 16, 8, 2, device="cpu")
