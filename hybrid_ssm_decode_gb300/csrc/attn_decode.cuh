@@ -630,10 +630,11 @@ struct Warp {
             return v & ((t >= lo && t <= hi ? 0x0000FFFFu : 0u) | (t + 1 >= lo && t + 1 <= hi ? 0xFFFF0000u : 0u));
         }
     }
-    __device__ __forceinline__ bool not_finite(uint32_t v) const {
+    // Of a word of the cache.
+    __device__ __forceinline__ static bool stored_not_finite(uint32_t v) {
         if constexpr (KV == kF32) return (v & 0x7F800000u) == 0x7F800000u;
-        const uint32_t e = KV == kBF16 ? 0x7F807F80u : 0x7C007C00u, one = KV == kBF16 ? 0x00800080u : 0x04000400u;
-        return (((v & e) + one) & 0x80008000u) != 0;
+        if constexpr (KV == kBF16) return (((v & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
+        return (((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;       // E4M3: 0x7F alone
     }
 
     // Running maximum and sum over the scores of 8 N tokens, which become their
@@ -736,9 +737,10 @@ struct Warp {
     }
 
     // One group of which rows g and g + 8 see the tokens lo[x]..hi[x] (0..15) and
-    // some row of the block any_lo..any_hi; tok0 is its first token's position.
+    // some row of the block any_lo..any_hi, all of them all_lo..all_hi; tok0 is its
+    // first token's position.
     __device__ __forceinline__ void step_masked(uint32_t kb, uint32_t vb, const int (&lo)[2], const int (&hi)[2], int any_lo,
-                                                int any_hi, int T, int tok0, int len, int window, const int (&draft)[2]) {
+                                                int any_hi, int all_lo, int all_hi, int T, int tok0, int len, int window, const int (&draft)[2]) {
         float s[2][4];
         scores(kb, s);
 #pragma unroll
@@ -752,9 +754,17 @@ struct Warp {
         const Weights w = weights(s);
         bool bad = false;
         if (T > 1) {
-            each_value(vb, [&](int, int h, uint32_t b0, uint32_t b1) {
-                bad = bad || not_finite(cut(b0, h, 0, any_lo, any_hi)) || not_finite(cut(b1, h, 1, any_lo, any_hi));
-            });
+            // the tokens that some drafts see and others do not, at most T - 1 at either end
+            constexpr int kChunks = S::RB / 16;
+            const int a0 = max(any_lo, 0), na = max(0, min(all_lo, kAttnGroup) - a0);
+            const int b0 = max(max(all_hi + 1, 0), a0 + na), nb = max(0, min(any_hi, kAttnGroup - 1) + 1 - b0);
+            for (int i = lane; i < (na + nb) * kChunks; i += 32) {
+                const int n = i / kChunks, r = n < na ? a0 + n : b0 + n - na;
+                uint32_t v[4];
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(vb + swz<S>(r, i % kChunks)));
+                bad = bad || stored_not_finite(v[0]) || stored_not_finite(v[1]) || stored_not_finite(v[2]) || stored_not_finite(v[3]);
+            }
             bad = __any_sync(0xffffffffu, bad);
         }
         if (!bad) {
@@ -1166,7 +1176,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             } else if (ok) {
                 const int tok = (g0 + k) * kAttnGroup;
                 const int lo[2] = {see_lo[0] - tok, see_lo[1] - tok}, hi[2] = {see_hi[0] - tok, see_hi[1] - tok};
-                wp.step_masked(kb, vb, lo, hi, some_lo - tok, len - 1 - tok, a.T, tok, len, a.window, draft);
+                wp.step_masked(kb, vb, lo, hi, some_lo - tok, len - 1 - tok, all_lo - tok, all_hi - tok, a.T, tok, len, a.window, draft);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(done);
