@@ -7,7 +7,8 @@ fallback: ``load()`` raises if the library has not been built.
 The functions keep the C names (``rssm_create``, ``rssm_decode_step``, ...)
 and take torch CUDA tensors, or raw device addresses, where the C ABI takes
 device pointers. ``Layer`` bundles a workspace tensor and a handle for
-convenience.
+convenience. The attention side of a hybrid decode step is in ``hybrid``:
+``PageTable``, ``Attention``, ``add_norm`` and ``gated_norm``.
 """
 from __future__ import annotations
 

@@ -6,7 +6,7 @@
 // work on the scan's items (tokens, or pages going back). The order of the pages
 // is that of the requests whatever the launch.
 //
-// A decode step (the same few tokens for every request) is a single block, a
+// A decode step (the same few tokens for every request; step_takes) is a single block, a
 // thread a request: bound by latency, of which a scan is one barrier. Prompts and
 // ended requests take a block per 1024 items, up to two per SM: every block makes
 // the whole scan for itself, which costs it one pass over 8 bytes a request from L2,
@@ -546,15 +546,19 @@ int pages_threads(int batch) { return batch <= kPagesThreads / 2 ? kPagesThreads
 // Threads of a single-block kernel: one a request, in whole warps.
 int step_threads(int batch) { return batch >= kStepThreads ? kStepThreads : (batch + 31) / 32 * 32; }
 
-// Single-block kernels stay below the others' cost up to this many requests
-// (8 rounds of a scan).
-constexpr int kStepBatch = 8 * kStepThreads;
+// Whether the single-block kernels take T tokens for every request: an extend and a
+// rollback take them about 2.8 + 1.2 T us for every 1024 requests, and the
+// others 7 to 8 us (1024 requests: T = 1 4.0 against 9.0, T = 8 11.8 against
+// 7.6; 8192: T = 1 23 against 55; 64: T = 16 4.8 against 5.9).
+bool step_takes(int32_t T, int32_t batch) {
+    return T <= kStepTokens && T * (batch < kStepThreads ? batch : kStepThreads) <= 4 * kStepThreads;
+}
 
 rssm_status pages_shrink(rssm_pages* h, int32_t T, const int32_t* keep, void* stream) {
     PagesArgs a = pages_args(h);
     a.T = T;
     a.keep = keep;
-    if (T > 0 && T <= kStepTokens && a.batch <= kStepBatch) {
+    if (T > 0 && step_takes(T, a.batch)) {
         return launch_overlapped(pages_step_back_kernel, 1, step_threads(a.batch), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
     }
     // a rollback returns at most ceil(T / page_size) pages a request
@@ -619,7 +623,7 @@ rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, in
     a.positions = d_positions;
     a.max_tokens = max_tokens;
     a.wide = ((reinterpret_cast<uintptr_t>(d_slots) | reinterpret_cast<uintptr_t>(d_positions)) & 15u) == 0;
-    if (d_new == nullptr && T <= kStepTokens && a.batch <= kStepBatch) {
+    if (d_new == nullptr && step_takes(T, a.batch)) {
         return launch_overlapped(pages_step_kernel, 1, step_threads(a.batch), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
     }
     int blocks = 1;

@@ -139,7 +139,7 @@ def test_many_blocks_and_unaligned_lists(cuda_lib, offset):
         m.check(pt)
 
 
-@pytest.mark.parametrize("batch,T,ps", [(9000, 3, 16), (40, 17, 16), (40, 300, 1), (1500, 16, 5)])
+@pytest.mark.parametrize("batch,T,ps", [(9000, 3, 16), (9000, 6, 16), (40, 17, 16), (40, 300, 1), (1500, 16, 5), (300, 13, 4)])
 def test_uniform_steps_of_either_kind(cuda_lib, batch, T, ps):
     """Uniform extends and rollbacks past the single-block kernels' batch and tokens, and below."""
     most = 2 + 2 * T // ps
