@@ -59,7 +59,9 @@ __global__ void __launch_bounds__(256) attn_append_kernel(const TI* k, const TI*
 constexpr size_t kAttnAlign = 256;
 size_t up256(size_t v) { return (v + kAttnAlign - 1) / kAttnAlign * kAttnAlign; }
 
-// Regions of the workspace.
+// Regions of the workspace. The error word and the counters, which every call leaves at
+// zero, have one size and one place whatever the configuration, and the parts, which a
+// call leaves as they fall, lie behind them: layers of any shapes may share a workspace.
 struct AttnLayout {
     size_t err, arrived, arrived_round, part_ml, part_o, total;
 };
@@ -102,7 +104,7 @@ AttnLayout attn_layout(const rssm_attn_config& c) {
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off += up256(bytes); return o; };
     L.err = take(16);
-    L.arrived = take(4 * static_cast<size_t>(c.batch) * c.kv_heads * attn_chunks(rows, c));
+    L.arrived = take(4 * static_cast<size_t>(kAttnMaxGrid));
     L.arrived_round = take(4 * 2 * static_cast<size_t>(kAttnMaxGrid));
     L.part_ml = take(parts * 8);
     L.part_o = take(parts * c.head_dim * 4);

@@ -22,7 +22,7 @@ struct AttnArgs {
     const float* k_scale;       // [kv_heads], FP8 caches
     const float* v_scale;
     int32_t* err;
-    uint32_t* arrived;          // [B][kv_heads][chunks], 0 between launches
+    uint32_t* arrived;          // [blocks], by the block of the request and head's first part, 0 between launches
     uint32_t* arrived_round;    // [2 blocks], by the slot of a round's first part, 0 between launches
     float2* part_ml;            // [2 blocks][rows]: maximum and sum of a part
     float* part_o;              // [2 blocks][rows][D]

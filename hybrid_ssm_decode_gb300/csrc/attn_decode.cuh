@@ -920,7 +920,7 @@ __device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, floa
         else sums(Int<4>{}, Int<4>{});
         if (final) return;
         named_sync(1, kThreads);
-        if (tid == 0) *s_last = arrive_last(a.arrived + static_cast<int64_t>(part.b) * a.kv_heads * a.chunks + part.pair, (np - 1) / kJoin);
+        if (tid == 0) *s_last = arrive_last(a.arrived + part.first, (np - 1) / kJoin);
         named_sync(1, kThreads);
         if (!*s_last) return;
         p0 = 0;
@@ -1100,9 +1100,11 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     // block), and if it was the request's last, it is joined after that part.
     Part left;
     left.pair = -1;
+    // A split request and head is known by the block of its first part: that part ends
+    // its block's share, so no block has two such.
     const auto count_left = [&] {                            // thread 0, after a block barrier
         if (left.others < kJoin) {
-            *s_last = arrive_last(a.arrived + static_cast<int64_t>(left.b) * a.kv_heads * a.chunks + left.pair, left.others);
+            *s_last = arrive_last(a.arrived + left.first, left.others);
         } else {
             const int p = static_cast<int>(blockIdx.x) - left.first, p0 = p / kJoin * kJoin;
             *s_last = arrive_last(a.arrived_round + 2 * (left.first + p0) + (p0 == 0 ? 1 : 0),

@@ -628,8 +628,9 @@ rssm_status rssm_attn_workspace_size(const rssm_attn_config* cfg, size_t* bytes)
  *   d_k_scale, d_v_scale  RSSM_KV_FP8: FP32 [kv_heads], finite and > 0; the cache
  *                         stands for code*scale. NULL otherwise. Must outlive the handle.
  *   d_workspace           256-byte aligned. The layers of one stream may share one
- *                         workspace (same or larger size): a call leaves it as it
- *                         found it. Zeroed here, on `stream`.
+ *                         workspace as large as the largest asks for, whatever their
+ *                         configurations. Its error word and counters are zeroed
+ *                         here, on `stream`; a call leaves the counters at zero.
  * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY, CUDA. */
 rssm_status rssm_attn_create(const rssm_attn_config* cfg, void* d_k_cache, void* d_v_cache,
                              const float* d_k_scale, const float* d_v_scale, void* d_workspace,

@@ -346,6 +346,31 @@ def test_shared_workspace_streams_and_graphs(cuda_lib):
         a.tokens = full
 
 
+@pytest.mark.parametrize("one,two", [
+    (dict(q_heads=32, kv_heads=2), dict(q_heads=32, kv_heads=8)),
+    (dict(lens=64), dict(lens=256)),
+    (dict(q_heads=16, kv_heads=1, T=4), dict(q_heads=8, kv_heads=8)),
+    (dict(lens=3, long=9000), dict(lens=300, kv_heads=4))])
+def test_layers_of_other_shapes_on_one_workspace(cuda_lib, one, two):
+    """Layers that differ in cache heads, batch or drafts, with requests split over
+    blocks, called in turn on one workspace: each as on its own."""
+    def case(seed, lens=256, long=90, **kw):
+        n = [(i * 37 + seed) % long + 1 for i in range(lens - 1)] + [long * 3]
+        return Case(n, **{**dict(q_heads=4, kv_heads=2, dim=64, seed=seed), **kw})
+
+    a, b = case(1, **one), case(2, **two)
+    alone = [c.run() for c in (a, b)]
+    for c, got in zip((a, b), alone):
+        c.check(got)
+    ws = torch.empty(max(rssm.rssm_attn_workspace_size(c.layer().cfg) for c in (a, b)), dtype=torch.uint8, device="cuda")
+    layers = [c.layer(workspace=ws) for c in (a, b)]
+    for _ in range(3):
+        for c, layer, want in zip((a, b), layers, alone):
+            out, lse = c.run(layer)
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+            assert layer.get_error() == (0, 0, 0, 0)
+
+
 def test_fewer_drafts_than_the_most(cuda_lib):
     c = Case([90, 33], T=1, q_heads=16, kv_heads=2, dim=128, seed=3)
     c.check(c.run(c.layer(max_draft=8)))

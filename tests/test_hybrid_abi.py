@@ -98,6 +98,18 @@ def test_attention_config(lib, kw, status):
     assert (n.value > 0) == (status == OK)
 
 
+def test_attention_workspaces_are_laid_out_alike(lib):
+    """What a call must leave at zero lies at the same place for every layer, so
+    that layers can share a workspace: no region before the parts, whose size
+    goes by the rows that a block takes, grows with the batch, heads or drafts."""
+    def size(**kw):
+        return rssm.rssm_attn_workspace_size(_attn(**kw))
+
+    for shapes in ((dict(), dict(batch=4096), dict(q_heads=64, kv_heads=64), dict(q_heads=16, kv_heads=1), dict(max_draft=4)),
+                   (dict(q_heads=32, kv_heads=1, max_draft=8), dict(batch=500, q_heads=64, kv_heads=1))):
+        assert len({size(**kw) for kw in shapes}) == 1, shapes
+
+
 def test_attention_host_errors(lib):
     cfg, h = _attn(), ctypes.c_void_p(0)
     need = rssm.rssm_attn_workspace_size(cfg)
