@@ -92,7 +92,7 @@ class PagesConfig(ctypes.Structure):
 
 
 class PagesLayout(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_size_t) for n in ("lens", "table", "free", "free_count", "err", "total_bytes")]
+    _fields_ = [(n, ctypes.c_size_t) for n in ("lens", "table", "free", "free_count", "err", "refused", "total_bytes")]
 
 
 class AttnConfig(ctypes.Structure):

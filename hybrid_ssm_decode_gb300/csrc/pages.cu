@@ -38,6 +38,7 @@ struct PagesArgs {
     int32_t* free_list;
     int32_t* free_count;
     int32_t* err;
+    int32_t* refused;     // [batch]: the request's last extend was refused
     uint32_t* ticket;
     int32_t batch, page_size, num_pages, max_pages;
     int32_t shift;        // log2(page_size), or -1: a division costs 20 instructions
@@ -143,8 +144,10 @@ __device__ __forceinline__ Ask ask_shrink(const PagesArgs& a, int b) {
     const int64_t most = static_cast<int64_t>(a.max_pages) * a.page_size;
     if (r.len < 0 || r.len > most) r.bad = RSSM_DEV_PAGES_COUNT;
     else if (a.T > 0) {
+        // drafts that were never let in are not there to be taken back
+        const bool none = a.refused[b] != 0;
         if (k < 0 || k > a.T || a.T > r.len) r.bad = RSSM_DEV_PAGES_COUNT;
-        else r.newlen = r.len - a.T + k;
+        else if (!none) r.newlen = r.len - a.T + k;
     } else {
         if (k < 0) r.bad = RSSM_DEV_PAGES_COUNT;
         else r.newlen = min(r.len, k);
@@ -321,6 +324,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
         if (b < a.batch) {
             if (r.bad) report_error(a.err, r.bad, b, a.d_new ? a.d_new[b] : a.T);
             else if (r.count > 0) a.lens[b] = r.len + r.count;
+            if (r.bad || r.count > 0) a.refused[b] = r.bad != 0;
         }
     }
     if (tid == 0) *a.free_count = base;
@@ -432,6 +436,7 @@ __global__ void __launch_bounds__(kStepThreads) pages_step_kernel(const PagesArg
         }
         if (r.bad) report_error(a.err, r.bad, b, a.T);
         else a.lens[b] = r.len + a.T;
+        a.refused[b] = r.bad != 0;
     }
     if (tid == 0) *a.free_count = base;                        // every thread read it before the scan's barrier
 }
@@ -464,12 +469,12 @@ __global__ void __launch_bounds__(kStepThreads) pages_step_back_kernel(const Pag
 
 __global__ void pages_init_kernel(int32_t* lens, int batch, int32_t* table, int64_t entries, int32_t* free_list,
                                   const int32_t* free0, int num_pages, int32_t* free_count, int32_t* err,
-                                  uint32_t* ticket) {
+                                  int32_t* refused, uint32_t* ticket) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int64_t n = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = t; i < entries; i += n) table[i] = -1;
     for (int64_t i = t; i < num_pages; i += n) free_list[i] = free0 ? free0[i] : static_cast<int32_t>(i);
-    for (int64_t i = t; i < batch; i += n) lens[i] = 0;
+    for (int64_t i = t; i < batch; i += n) lens[i] = refused[i] = 0;
     if (t == 0) {
         *free_count = num_pages;
         *ticket = 0;
@@ -494,6 +499,7 @@ rssm_status pages_layout(const rssm_pages_config* c, rssm_pages_layout* L) {
     L->free = take(4 * static_cast<size_t>(c->num_pages));
     L->free_count = take(kPagesAlign);    // the count, and the ticket 128 bytes on
     L->err = take(16);
+    L->refused = take(4 * static_cast<size_t>(c->batch));
     L->total_bytes = off;
     return RSSM_OK;
 }
@@ -519,6 +525,7 @@ PagesArgs pages_args(const rssm_pages* h) {
     a.free_count = reinterpret_cast<int32_t*>(h->base + h->lay.free_count);
     a.ticket = reinterpret_cast<uint32_t*>(h->base + h->lay.free_count + 128);
     a.err = reinterpret_cast<int32_t*>(h->base + h->lay.err);
+    a.refused = reinterpret_cast<int32_t*>(h->base + h->lay.refused);
     a.batch = h->cfg.batch;
     a.page_size = h->cfg.page_size;
     a.num_pages = h->cfg.num_pages;
@@ -601,7 +608,7 @@ rssm_status rssm_pages_create(const rssm_pages_config* cfg, void* d_workspace, s
     const PagesArgs a = pages_args(h);
     pages_init_kernel<<<256, 256, 0, static_cast<cudaStream_t>(stream)>>>(
         a.lens, a.batch, a.table, static_cast<int64_t>(a.batch) * a.max_pages, a.free_list, d_free0, a.num_pages,
-        a.free_count, a.err, a.ticket);
+        a.free_count, a.err, a.refused, a.ticket);
     if (cudaGetLastError() != cudaSuccess) {
         delete h;
         return RSSM_ERR_CUDA;

@@ -102,8 +102,9 @@ def _ints(t, n, device, name):
 class PageTable:
     """The pages of a batch of requests (rssm_pages_*).
 
-    `lens`, `table` and `free_count` are views of the workspace, which the
-    library alone writes: they are read where an attention layer wants them.
+    `lens`, `table`, `free_count` and `refused` are views of the workspace, which
+    the library alone writes: they are read where an attention layer wants them.
+    `refused` (int32 [batch]) is 1 for a request whose last extend found no room.
     """
 
     def __init__(self, batch, page_size, num_pages, max_pages, free=None, device="cuda", stream=None):
@@ -130,6 +131,7 @@ class PageTable:
         self.lens = view(lay.lens, batch)
         self.table = view(lay.table, batch, max_pages)
         self.free_count = view(lay.free_count, 1)
+        self.refused = view(lay.refused, batch)
 
     def close(self):
         if self.handle:
@@ -163,7 +165,8 @@ class PageTable:
             _r._check("rssm_pages_extend", st)
 
     def rollback(self, T, accepted, stream=None):
-        """Of the last T tokens of request b, accepted[b] stay."""
+        """Of the last T tokens of request b, accepted[b] stay; a request whose
+        extend was refused stays as it is."""
         self._counts(accepted, "accepted")
         st = self._fn.rssm_pages_rollback(self.handle, T, accepted.data_ptr(), _stream_of(stream, self.device.index))
         if st:

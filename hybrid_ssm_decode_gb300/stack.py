@@ -248,7 +248,10 @@ class HybridStack:
     def step(self, u):
         """One decode step for u [B][d_model], or a round of T drafts a request for
         [B][T][d_model] (float32); returns the final norm's output, bf16, of the
-        same shape. A round of T > 1 drafts must be followed by verify."""
+        same shape. A round of T > 1 drafts must be followed by verify. Where the
+        page table refuses a request (errors, pages.refused), its output is of no
+        use: verify turns a round's drafts down everywhere, but a single step's
+        token has gone into its SSM layers, and the request must be ended."""
         import torch
         import torch.nn.functional as F
         s = self.shape
@@ -276,10 +279,12 @@ class HybridStack:
         return final.view(u.shape)
 
     def verify(self, T, accepted):
-        """After a round of T > 1 drafts: accepted[b] of them stay (device int32)."""
+        """After a round of T > 1 drafts: accepted[b] of them stay (device int32);
+        none of a request that the page table refused."""
+        kept = accepted * (1 - self.pages.refused)
         for layer, kind in zip(self.layers, self.shape.pattern):
             if kind == "M":
-                layer.verify_rollback(accepted)
+                layer.verify_rollback(kept)
         self.pages.rollback(T, accepted)
 
     def errors(self):

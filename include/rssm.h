@@ -521,7 +521,9 @@ enum {
  *   rollback, truncate   the pages past ceil(len'_b/page_size) go back:
  *             free[free_count + e_b + j] = table[b][held'_b + j], table entry = -1.
  * The order is that of the requests, whatever the launch, so a rollback undoes
- * the extend before it to the last entry, and reruns give the same pages. */
+ * the extend before it to the last entry, and reruns give the same pages. A
+ * request that the extend refused has nothing to undo: the table keeps a mark of
+ * it, and the rollback leaves the request as it is. */
 typedef struct {
     int32_t batch;      /* requests, >= 1                              */
     int32_t page_size;  /* tokens per page, >= 1                       */
@@ -532,9 +534,11 @@ typedef struct {
 /* Byte offsets of the regions in the page table's workspace:
  *   lens int32 [batch]; table int32 [batch][max_pages], -1 where no page is
  *   held; free int32 [num_pages], the stack, of which the first free_count
- *   entries are free pages; free_count int32 [1]; err int32 [4]. */
+ *   entries are free pages; free_count int32 [1]; err int32 [4]; refused int32
+ *   [batch], 1 where the last extend that asked for tokens of the request (a
+ *   count of 0 does not) was refused. */
 typedef struct {
-    size_t lens, table, free, free_count, err;
+    size_t lens, table, free, free_count, err, refused;
     size_t total_bytes;
 } rssm_pages_layout;
 
@@ -561,7 +565,7 @@ rssm_status rssm_pages_create(const rssm_pages_config* cfg, void* d_workspace, s
  *                its request.
  * A request that cannot be served (no page left, row full, count < 0, slots
  * short) is left unchanged, its tokens' slots and positions are -1, and the
- * error word is set; the others are served. Entries past the last token are
+ * error word and its mark are set; the others are served. Entries past the last token are
  * not written. d_slots and d_positions: 4-byte aligned.
  * Errors: INVALID_ARG (null, T, max_tokens < batch*T where d_new is NULL), CUDA. */
 rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, int32_t* d_slots,
@@ -571,7 +575,9 @@ rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, in
  * request b, d_accepted[b] (device int32 [batch], 0..T) stay. The counterpart of
  * rssm_verify_rollback for the attention layers' cache: only lengths and pages
  * move. A count out of 0..T, or T above the request's length, leaves the request
- * unchanged and sets RSSM_DEV_PAGES_COUNT. Errors: INVALID_ARG, CUDA. */
+ * unchanged and sets RSSM_DEV_PAGES_COUNT. A request whose mark is set is left
+ * unchanged too: its drafts never came in, as its extend reported.
+ * Errors: INVALID_ARG, CUDA. */
 rssm_status rssm_pages_rollback(rssm_pages* h, int32_t T, const int32_t* d_accepted, void* stream);
 
 /* Cut request b to min(len_b, d_keep[b]) tokens (device int32 [batch]); 0 ends a

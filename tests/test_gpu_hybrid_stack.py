@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 import torch
 
+import hybrid_ssm_decode_gb300 as rssm
 import synth
 from _gpu import TOL_LOW, vec_err
 from hybrid_ssm_decode_gb300.stack import HybridShape, HybridStack
@@ -113,6 +114,31 @@ def test_draft_rounds_match_single_steps(cuda_lib, kv):
     assert all(e[0] == 0 for s in (a, b) for e in s.errors())
     a.close()
     b.close()
+
+
+def test_a_refused_round_leaves_no_trace(cuda_lib):
+    """A request that finds the pool empty in one round, beside others that do
+    not, goes on as one whose drafts of that round were all turned down."""
+    T = 3
+    tight, wide = (HybridStack(HybridShape(**{**SHAPE.__dict__, "max_draft": T, "num_pages": n}), seed=4) for n in (5, 40))
+
+    def i32(*v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+    for i, u in enumerate(_inputs(9, 17, T)):
+        if i == 6:                                 # the first request ends: there is room again
+            for s in (tight, wide):
+                s.pages.truncate(i32(0, 99, 99))
+        a, b = tight.step(u), wide.step(u)
+        refused = i == 5                           # from 15 to 18 tokens: three pages more, two left
+        assert tight.pages.refused.tolist() == [0, 0, int(refused)]
+        assert torch.equal(a[:2], b[:2]) and (refused or torch.equal(a[2], b[2]))
+        tight.verify(T, i32(3, 3, 3))
+        wide.verify(T, i32(3, 3, 0 if refused else 3))
+        assert tight.pages.lens.tolist() == wide.pages.lens.tolist()
+    assert [e[:2] for e in tight.errors()][0] == (rssm.RSSM_DEV_PAGES_EMPTY, 1)
+    tight.close()
+    wide.close()
 
 
 def test_requests_come_and_go(cuda_lib):

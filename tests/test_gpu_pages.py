@@ -213,6 +213,59 @@ def test_refused_requests_stay_as_they_were(cuda_lib):
     m.check(pt)
 
 
+@pytest.mark.parametrize("batch,T,ragged", [(3, 4, False), (3, 4, True), (3, 40, False), (1500, 3, False), (1500, 3, True),
+                                            (1500, 20, False), (1100, 6, False)])
+def test_a_refused_request_is_not_rolled_back(cuda_lib, batch, T, ragged):
+    """The pool gives out in the middle of a batch: a rollback of the whole round
+    leaves every request as it was before, the refused ones with all their tokens."""
+    ps = 4
+    lens = [T + b % 5 for b in range(batch)]
+    held = [-(-n // ps) for n in lens]
+    need = [-(-(n + T) // ps) - h for n, h in zip(lens, held)]
+    late = [need[b] > 0 and b > batch // 2 for b in range(batch)]
+    num = sum(held) + sum(need[:batch // 2 + 1])
+    pt = rssm.PageTable(batch, ps, num, 2 + 3 * T // ps)
+    slots = torch.empty(sum(lens) + batch * T, dtype=torch.int32, device="cuda")
+
+    def state():
+        return pt.lens.tolist(), pt.table.tolist(), pt.free_count.tolist()
+
+    def go():
+        pt.extend(slots, **(dict(new=_i32([T] * batch)) if ragged else dict(T=T)))
+
+    pt.extend(slots, new=_i32(lens))
+    before = state()
+    go()
+    assert pt.refused.tolist() == [int(x) for x in late]
+    assert pt.get_error()[:2] == (rssm.RSSM_DEV_PAGES_EMPTY, sum(late))
+    pt.extend(slots, new=_i32([0] * batch))          # asks for nothing: changes nothing
+    pt.rollback(T, _i32([0] * batch))
+    assert state() == before and pt.get_error()[0] == 0
+    # drafts that stay, and room for the late ones once the first request has left
+    go()
+    pt.rollback(T, _i32([b % (T + 1) for b in range(batch)]))
+    assert pt.lens.tolist() == [n if x else n + b % (T + 1) for b, (n, x) in enumerate(zip(lens, late))]
+    pt.truncate(_i32([0 if b <= batch // 2 else 10 ** 6 for b in range(batch)]))
+    pt.get_error()
+    go()
+    assert not any(pt.refused.tolist()) and pt.get_error()[0] == 0
+    grown = pt.lens.tolist()
+    pt.rollback(T, _i32([1] * batch))
+    assert pt.lens.tolist() == [n - T + 1 for n in grown]
+
+
+def test_refusals_of_each_kind_are_marked(cuda_lib):
+    pt = rssm.PageTable(4, 16, 6, 2)
+    slots = torch.empty(64, dtype=torch.int32, device="cuda")
+    pt.extend(slots, new=_i32([16, 16, 1, 1]))
+    pt.extend(slots, new=_i32([0, 17, -1, 0]))       # past its row; a negative count
+    assert pt.refused.tolist() == [0, 1, 1, 0]
+    pt.extend(slots[:4], new=_i32([0, 0, 4, 1]))     # slots for the third alone
+    assert pt.refused.tolist() == [0, 1, 0, 1]
+    pt.rollback(1, _i32([0, 0, 0, 0]))
+    assert pt.lens.tolist() == [15, 16, 4, 1]
+
+
 def test_binding_refuses(cuda_lib):
     pt = rssm.PageTable(4, 16, 8, 2)
     good = torch.empty(8, dtype=torch.int32, device="cuda")
