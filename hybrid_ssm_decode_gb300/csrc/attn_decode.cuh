@@ -43,7 +43,9 @@
 // Matrix instructions. m16n8k16 on BF16 caches, with 2^(s-m) split into two
 // BF16 terms, so that the outputs carry only their own rounding; on FP8 caches the codes
 // widen exactly to FP16 (Q scaled per row by a power of two into FP16's range;
-// 2^(s-m) rounded to FP16's 11 bits), and on FP32 caches m16n8k8 on TF32 with both
+// 2^(s-m+15) rounded to FP16's 11 bits, so that only weights below 2^-29 of the largest
+// lose some of them and only those below 2^-40 vanish: a long tail under one large
+// score counts), and on FP32 caches m16n8k8 on TF32 with both
 // operands split in two (three products; what is left out is below 2^-21).
 #pragma once
 
@@ -383,6 +385,7 @@ struct Warp {
     static constexpr int D = S::D;
     static constexpr int kQRegs = KV == kF32 ? 1 : D / 16;
     static constexpr int kTiles = D / 8;
+    static constexpr float kUp = KV == kFP8 ? 15.f : 0.f;   // weights, and l and o with them, are 2^kUp times as large
     float o[kTiles][4];
     float m[2], l[2];            // rows lane/4 and lane/4 + 8; l is this lane's columns only
     uint32_t qf[kQRegs][4];
@@ -667,7 +670,7 @@ struct Warp {
                 o[i][3] *= f[1];
             }
         }
-        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        const float ref[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - kUp, (m[1] == -INFINITY ? 0.f : m[1]) - kUp};
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -821,15 +824,19 @@ template <int KV, class S>
 __device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, int col, float4 v, float M, float L) {
     const int t = (part.row0 + r) / a.group, j = (part.row0 + r) % a.group;
     const int64_t at = (static_cast<int64_t>(part.b) * a.T + t) * a.q_heads + part.head * a.group + j;
-    const float inv = L == 0.f ? 0.f : (KV == kFP8 ? __ldg(a.v_scale + part.head) : 1.f) / L;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+    if (KV == kFP8) {
+        const float s = __ldg(a.v_scale + part.head);
+        v.x *= s; v.y *= s; v.z *= s; v.w *= s;
+    }
     if (KV == kF32) {
         *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * S::D + col) = v;
     } else {
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * S::D + col) =
             make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     }
-    if (a.lse != nullptr && col == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    if (a.lse != nullptr && col == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + (log2f(L) - Warp<KV, S>::kUp)) * 0.69314718055994531f;
 }
 
 // Join the parts of a request and head: the consumer warps, once all have

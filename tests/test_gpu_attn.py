@@ -204,6 +204,39 @@ def test_fp8_query_range(cuda_lib, mag):
     assert bool(((out >= (want - lim).to(out.dtype)) & (out <= (want + lim).to(out.dtype))).all())
 
 
+@pytest.mark.parametrize("dim,T,lens", [(64, 1, [5000, 64]), (128, 1, [20000]), (256, 4, [3000, 100])])
+def test_fp8_small_weights(cuda_lib, dim, T, lens):
+    """A long tail under a few large scores: every 16th token scores 18 above the
+    others and has value 0, so the output is made of weights of e^-18 = 2^-26 of
+    the largest alone. Each is within 2^-12 of itself, and so is their sum, as
+    all values are positive; the division adds less than as much again."""
+    B, ps = len(lens), 16
+    held = [-(-n // ps) for n in lens]
+    k, v = torch.zeros((sum(held), 1, ps, dim)), torch.ones((sum(held), 1, ps, dim))
+    k[:, :, 0, 0] = 18
+    v[:, :, 0] = 0
+    table = torch.full((B, max(held)), -1, dtype=torch.int32)
+    for b, h in enumerate(held):
+        table[b, :h] = torch.arange(h) + sum(held[:b])
+    one = torch.ones(1, device="cuda")
+    kc, vc = (x.cuda().to(torch.float8_e4m3fn) for x in (k, v))
+    layer = rssm.Attention(kc, vc, batch=B, q_heads=1, max_pages=max(held), max_draft=T, scale=1.0, k_scale=one, v_scale=one)
+    q = torch.zeros((B, T, 1, dim), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    layer.decode(out, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), table.cuda(), T=T, lse=lse)
+    out, lse = out.cpu(), lse.cpu()
+    for b, n in enumerate(lens):
+        for t in range(T):
+            seen = n - T + t + 1
+            large = -(-seen // ps)
+            tail = (seen - large) * math.exp(-18.0)
+            want = torch.tensor(tail / (large + tail), dtype=torch.float64)
+            lo, hi = ((want * (1 + e)).to(out.dtype) for e in (-2.0 ** -11, 2.0 ** -11))
+            assert bool(((out[b, t] >= lo) & (out[b, t] <= hi)).all()), (float(out[b, t, 0, 0]), float(want))
+            assert abs(float(lse[b, t, 0]) - (18 + math.log(large + tail))) < 2.0 ** -14
+
+
 @pytest.mark.parametrize("kv", ["bf16", "f32", "fp8"])
 @pytest.mark.parametrize("what", [float("inf"), float("nan")])
 def test_unseen_values_that_are_not_finite(cuda_lib, kv, what):
