@@ -601,7 +601,8 @@ rssm_status rssm_pages_destroy(rssm_pages* h);
  * over the positions it sees. Query head h reads cache head h/(q_heads/kv_heads).
  * A token that sees nothing (p < 0), or only scores of -inf, has out = 0 and
  * lse = -inf. Nothing that a token does not see reaches its output, NaN and
- * infinities included. */
+ * infinities included; an infinite value that it does see makes its output NaN or
+ * infinite (over FP32 caches values from (1 - 2^-12) 2^128 on count as infinite). */
 enum { RSSM_KV_FP8 = 4 };   /* kv_dtype: E4M3 codes, one FP32 scale per cache head for K and for V */
 
 typedef struct {

@@ -237,6 +237,32 @@ def test_fp8_small_weights(cuda_lib, dim, T, lens):
             assert abs(float(lse[b, t, 0]) - (18 + math.log(large + tail))) < 2.0 ** -14
 
 
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("what", ["one", "all", "query", "lowest"])
+def test_scores_of_minus_infinity(cuda_lib, kv, dim, what):
+    """Keys that a row sees with a score of -inf, or of the type's lowest value,
+    weigh nothing; a row that sees no others is empty."""
+    c = Case([41, 16], q_heads=4, kv_heads=2, dim=dim, kv=kv, poison=False, seed=dim)
+    c.q[..., 5] = c.q[..., 5].abs() + 0.5
+    low = {"lowest": torch.finfo(c.io).min}.get(what, -math.inf)
+    at = {"one": [7, 20], "lowest": [7, 20], "all": range(41), "query": range(41)}[what]
+    for b, n in enumerate(c.lens):
+        k = c.tokens[b][0]
+        for i in at:
+            if i < n:
+                new = -k[i, :, 5].abs() - 0.25 if what == "query" else torch.full((2,), low, dtype=torch.float64)
+                k[i, :, 5] = new
+                c.k_cache[c.table[b, i // 16], :, i % 16, 5] = new.to(c.io).cuda()
+    if what == "query":
+        c.q[..., 5] = math.inf
+    out, lse = c.run()
+    if what in ("all", "query"):
+        assert not bool(out.any()) and bool((lse == -math.inf).all())
+    else:
+        c.check((out, lse))
+
+
 @pytest.mark.parametrize("kv", ["bf16", "f32", "fp8"])
 @pytest.mark.parametrize("what", [float("inf"), float("nan")])
 def test_unseen_values_that_are_not_finite(cuda_lib, kv, what):
