@@ -12,9 +12,8 @@ namespace {
 template <class TI, class TO, int VEC>
 __global__ void __launch_bounds__(256) attn_append_kernel(const TI* k, const TI* v, int64_t k_stride,
                                                           int64_t v_stride, const int32_t* slots, TO* kc, TO* vc,
-                                                          const float* __restrict__ k_scale,
-                                                          const float* __restrict__ v_scale, int tokens, int heads, int dim,
-                                                          int page_size, int num_pages, int64_t page_stride, int32_t* err) {
+                                                          const float* k_scale, const float* v_scale, int tokens,
+                                                          int heads, int dim, int page_size, int num_pages, int64_t page_stride, int32_t* err) {
     after_predecessor();
     const int per_head = dim / VEC, per_token = heads * per_head;
     const int64_t n = static_cast<int64_t>(tokens) * per_token;
@@ -40,7 +39,7 @@ __global__ void __launch_bounds__(256) attn_append_kernel(const TI* k, const TI*
             if constexpr (VEC == 1) *to = *reinterpret_cast<const TO*>(from);
             else *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
         } else {
-            const float s = __ldg(scale + head);
+            const float s = scale[head];
             if constexpr (VEC == 1) {
                 *to = static_cast<TO>(e4m3x2(__fdiv_rn(to_f(*from), s), 0.f) & 0xFF);
             } else {

@@ -855,16 +855,15 @@ struct Warp {
 };
 
 // Outputs of row r of a part, columns col..col + 3, from the sums v under maximum
-// M and total L.
+// M and total L; vs: FP8, the scale of the head's values.
 template <int KV, class S>
-__device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, int col, float4 v, float M, float L) {
+__device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, int col, float4 v, float M, float L, float vs) {
     const int t = (part.row0 + r) / a.group, j = (part.row0 + r) % a.group;
     const int64_t at = (static_cast<int64_t>(part.b) * a.T + t) * a.q_heads + part.head * a.group + j;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
     if (KV == kFP8) {
-        const float s = __ldg(a.v_scale + part.head);
-        v.x *= s; v.y *= s; v.z *= s; v.w *= s;
+        v.x *= vs; v.y *= vs; v.z *= vs; v.w *= vs;
     }
     if (KV == kF32) {
         *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * S::D + col) = v;
@@ -887,6 +886,7 @@ __device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, floa
     constexpr int D = S::D, kThreads = S::kConsumers * 32;
     static_assert((kAttnMaxGrid + kJoin - 1) / kJoin <= 32 && 32 <= S::OS, "a round of parts must fit a warp and the buffer");
     const int np = part.others + 1;
+    const float vs = KV == kFP8 ? __ldcg(a.v_scale + part.head) : 1.f;
     // this block's kJoin neighbours, and then one part for each such round; or all at once
     int p0 = 0, step = 1, n = np;
     bool final = np <= kJoin;
@@ -950,7 +950,7 @@ __device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, floa
                     if (x >= items) break;
                     const int r = x / (D / 4), col = (x % (D / 4)) * 4;
                     if (final) {
-                        put<KV, S>(a, part, r, col, acc[i], s_row[r].x, s_row[r].y);
+                        put<KV, S>(a, part, r, col, acc[i], s_row[r].x, s_row[r].y, vs);
                     } else {
                         // into the round's first part, which only this thread still reads here
                         __stcg(reinterpret_cast<float4*>(a.part_o + part_at(0, r) * D + col), acc[i]);
@@ -1183,7 +1183,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         const int all_lo = window_start(len - 1, a.window);         // and the first
         const int some_lo = window_start(len - a.T, a.window);
         wp.reset();
-        wp.load_q(qbuf + (pq * S::kRows + wm * 16) * S::QS, a.scale_log2, KV == kFP8 ? __ldg(a.k_scale + head) : 1.f);
+        wp.load_q(qbuf + (pq * S::kRows + wm * 16) * S::QS, a.scale_log2, KV == kFP8 ? __ldcg(a.k_scale + head) : 1.f);
         if (KV != kF32) {
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty + pq);
@@ -1241,6 +1241,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             if (lane == 0) mbar_arrive(qempty + pq);
         }
         ++parts;
+        const float vs = KV == kFP8 ? __ldcg(a.v_scale + head) : 1.f;   // there once the warps are joined
 
         // ---- join the warps of each row ----
 #pragma unroll
@@ -1285,7 +1286,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         if (part.others == 0) {
             for (int x = tid; x < rows * (D / 4); x += kThreads) {
                 const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-                put<KV, S>(a, part, r, col, sum_of(r, col), s_row[r].x, s_row[r].y);
+                put<KV, S>(a, part, r, col, sum_of(r, col), s_row[r].x, s_row[r].y, vs);
             }
         } else {
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + part.at_start;

@@ -40,7 +40,7 @@ __device__ __forceinline__ void ld32(float (&v)[8], const float* p) {
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(p) : "memory");
 }
 __device__ __forceinline__ void ld32_keep(float (&v)[8], const float* p) {
-    asm("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(p));
 }
 __device__ __forceinline__ void st32(float* p, const float (&v)[8]) {
@@ -68,11 +68,11 @@ __device__ __forceinline__ void load_vec(float (&v)[VEC], const __nv_bfloat16* p
         v[0] = __bfloat162float(*p);
     }
 }
-// Weights stay in cache: every row reads them.
+// Weights stay in cache: every row reads them. p: from past_wait().
 template <int VEC>
 __device__ __forceinline__ void load_w(float (&v)[VEC], const float* p) {
     if constexpr (VEC == 8) ld32_keep(v, p);
-    else v[0] = __ldg(p);
+    else asm("ld.global.f32 %0, [%1];" : "=f"(v[0]) : "l"(p));
 }
 template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a, int
     const int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + threadIdx.x / tpr;
     const bool live = row < a.rows;
     const int nvec = a.dim / VEC;
+    const float *w_post = past_wait(a.w_post), *w_norm = past_wait(a.w);
     const TU* u = static_cast<const TU*>(a.u) + (live ? row : 0) * a.u_stride;
     const TX* x = static_cast<const TX*>(a.x) + (live ? row : 0) * a.x_stride;
     const TX* gt = static_cast<const TX*>(a.gate) + (live ? row : 0) * a.gate_stride;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a, int
     }
     if (a.x != nullptr) {
         float r = 1.f;
-        if (a.w_post != nullptr) {
+        if (w_post != nullptr) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
@@ -149,9 +150,9 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a, int
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * tpr;
             if (!live || c >= nvec) continue;
-            if (a.w_post != nullptr) {
+            if (w_post != nullptr) {
                 float w[VEC];
-                load_w<VEC>(w, a.w_post + c * VEC);
+                load_w<VEC>(w, w_post + c * VEC);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) xv[i][e] *= r * (a.w_off + w[e]);
             }
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a, int
         const int c = lane + i * tpr;
         if (!live || c >= nvec) continue;
         float w[VEC];
-        load_w<VEC>(w, a.w + c * VEC);
+        load_w<VEC>(w, w_norm + c * VEC);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) w[e] = uv[i][e] * r * (a.w_off + w[e]);
         store_vec<VEC>(no + static_cast<int64_t>(c) * VEC, w);
@@ -254,13 +255,14 @@ __global__ void __launch_bounds__(1024) gated_norm_kernel(const GatedNormArgs a,
     const uint32_t step_row = step / groups, step_col = step - step_row * groups;
     const int nvec = a.group / VEC;
     const bool shared_w = a.w_dim == a.group;
+    const float* w_all = past_wait(a.w);
     float wv[VPT][VEC];
     if (shared_w) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * tpr;
             if (c >= nvec) continue;
-            load_w<VEC>(wv[i], a.w + c * VEC);
+            load_w<VEC>(wv[i], w_all + c * VEC);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) wv[i][e] += a.w_off;
         }
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(1024) gated_norm_kernel(const GatedNormArgs a,
             const int c = lane + i * tpr;
             if (!live || c >= nvec) continue;
             float w[VEC];
-            if (!shared_w) load_w<VEC>(w, a.w + at + c * VEC);
+            if (!shared_w) load_w<VEC>(w, w_all + at + c * VEC);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 v[i][e] *= r * (shared_w ? wv[i][e] : a.w_off + w[e]);

@@ -7,8 +7,10 @@
 // memory, until it has ended and its writes are visible, so nothing is reordered.
 // Every thread waits, the idle ones too: a kernel of this kind therefore never
 // ends before the one in front of it, and whatever follows it finds both done.
-// What an earlier kernel of this kind may write is not read through the
-// non-coherent path, since a block can be there before the write is.
+// What an earlier kernel may write (weights and scales too) is not read through the
+// non-coherent path, since a block can be there before the write is, and no load
+// may move in front of the wait: it is volatile or a plain access, or its pointer
+// comes from past_wait().
 #pragma once
 
 #include "common.cuh"
@@ -19,6 +21,13 @@ namespace rssm {
 __device__ __forceinline__ void after_predecessor() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// p, known only after the wait, for loads that may otherwise move freely.
+template <class T>
+__device__ __forceinline__ const T* past_wait(const T* p) {
+    asm volatile("" : "+l"(p));
+    return p;
 }
 
 template <class... P, class... A>

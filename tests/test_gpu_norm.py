@@ -159,6 +159,47 @@ def test_norms_on_another_stream_and_in_a_graph(cuda_lib):
     assert torch.equal(n1, n2)
 
 
+def test_weights_written_by_the_call_in_front(cuda_lib):
+    """A norm whose weights, and an attention whose scales, an overlapped call has
+    just written, again and again over the same addresses, in and out of a graph."""
+    g = _gen(5)
+    dim, n = 4096, 40
+    src = [_randn(g, 1, dim).abs() + 0.1 for _ in range(n)]
+    ones, u = torch.ones(dim, device="cuda"), _randn(g, 300, dim).to(BF16)
+    w, outs = torch.zeros(1, dim, device="cuda"), [torch.empty_like(u) for _ in range(n)]
+    k8 = _randn(g, 4, 8, 16, 64).to(torch.float8_e4m3fn)
+    scale, heads = torch.ones(1, 8, device="cuda"), [(s[:, :8] * 0.01).contiguous() for s in src]
+    layer = rssm.Attention(k8, k8, batch=4, q_heads=8, max_pages=1, k_scale=scale.view(8), v_scale=scale.view(8))
+    q = _randn(g, 4, 1, 8, 64).to(BF16)
+    lens, table = (torch.full((4,), 16, dtype=torch.int32, device="cuda"), torch.arange(4, dtype=torch.int32, device="cuda"))
+    att = [torch.empty_like(q) for _ in range(n)]
+
+    def chain(sync):
+        for s, h, o, a in zip(src, heads, outs, att):
+            rssm.add_norm(w, s, ones)
+            sync()
+            rssm.add_norm(o, u, w.view(dim))
+            rssm.gated_norm(o, o, u, w.view(dim), group=1024)
+            rssm.add_norm(None, h, None, x=h, u_out=scale)
+            sync()
+            layer.decode(a, q, lens, table)
+            sync()
+
+    chain(torch.cuda.synchronize)
+    want = [[t.clone() for t in ts] for ts in (outs, att)]
+    assert not torch.equal(want[0][0], want[0][1]) and not torch.equal(want[1][0], want[1][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(lambda: None)
+    for go in (lambda: chain(lambda: None), graph.replay):
+        for _ in range(3):
+            for t in outs + att + [w, scale]:
+                t.fill_(1)
+            go()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs + att, want[0] + want[1]))
+
+
 def test_binding_refuses(cuda_lib):
     u = torch.zeros(4, 64, device="cuda")
     w = torch.ones(64, device="cuda")

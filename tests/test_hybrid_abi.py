@@ -44,6 +44,17 @@ def test_struct_layouts_match_header(tmp_path):
         assert got[("const", c)] == getattr(rssm, c), c
 
 
+def test_overlapped_kernels_read_coherently():
+    """A kernel that takes its place beside the one in front of it may find data
+    that is not written yet in the read-only path: its sources use none."""
+    csrc = os.path.join(ROOT, "hybrid_ssm_decode_gb300", "csrc")
+    for name in ("norm.cu", "attn.cu", "attn_decode.cuh", "pages.cu", "overlap.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        for word in ("__ldg(", "ld.global.nc", "__restrict__"):
+            assert word not in text, f"{name}: {word}"
+
+
 def test_pages_layout(lib):
     lay = rssm.rssm_pages_layout_for(rssm.PagesConfig(100, 16, 5000, 70))
     assert lay.lens == 0 and lay.table >= 400 and lay.free >= lay.table + 4 * 7000
