@@ -102,7 +102,7 @@ AttnLayout attn_layout(const rssm_attn_config& c) {
     const size_t parts = 2 * static_cast<size_t>(kAttnMaxGrid) * attn_block_rows(rows, c.kv_dtype, c.head_dim);
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off += up256(bytes); return o; };
-    L.err = take(16);
+    L.err = take(20);                     // the error word, and whether any wait ran out
     L.arrived = take(4 * static_cast<size_t>(kAttnMaxGrid));
     L.arrived_round = take(4 * 2 * static_cast<size_t>(kAttnMaxGrid));
     L.part_ml = take(parts * 8);
@@ -299,9 +299,14 @@ rssm_status rssm_attn_get_error(rssm_attn* h, int32_t* err4, void* stream) {
     if (h == nullptr || err4 == nullptr) return RSSM_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* dev = h->base + h->lay.err;
-    cudaError_t e = cudaMemcpyAsync(err4, dev, 16, cudaMemcpyDeviceToHost, s);
+    int32_t word[5];
+    cudaError_t e = cudaMemcpyAsync(word, dev, sizeof(word), cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(dev, 0, 16, s);
+    if (e == cudaSuccess) {
+        std::memcpy(err4, word, 16);
+        // a call that gave up has not counted all its parts: the counters too go back to zero
+        e = cudaMemsetAsync(dev, 0, word[4] != 0 ? h->lay.part_ml : sizeof(word), s);
+    }
     return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }
 

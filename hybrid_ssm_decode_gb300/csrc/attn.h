@@ -21,7 +21,7 @@ struct AttnArgs {
     float* lse;                 // [B][T][q_heads] or null
     const float* k_scale;       // [kv_heads], FP8 caches
     const float* v_scale;
-    int32_t* err;
+    int32_t* err;               // error word [4]; [4]: a wait ran out, and the counters are not at zero
     uint32_t* arrived;          // [blocks], by the block of the request and head's first part, 0 between launches
     uint32_t* arrived_round;    // [2 blocks], by the slot of a round's first part, 0 between launches
     float2* part_ml;            // [2 blocks][rows]: maximum and sum of a part

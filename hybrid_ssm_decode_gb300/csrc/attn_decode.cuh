@@ -211,6 +211,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             *dead = 1;
             report_error(err, RSSM_DEV_TIMEOUT, -1, 0);
+            err[4] = 1;
             return false;
         }
     }

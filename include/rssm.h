@@ -667,7 +667,10 @@ rssm_status rssm_attn_decode(rssm_attn* h, int32_t T, const void* d_q, int64_t q
                              const int32_t* d_table, void* d_out, float* d_lse, void* stream);
 
 /* As rssm_pages_get_error, for the layer's workspace (code, count, request or
- * token, value; for RSSM_DEV_TIMEOUT the tile is -1). */
+ * token, value; for RSSM_DEV_TIMEOUT the tile is -1). After a wait ran out, the
+ * outputs of that call and of every later one on the workspace are undefined
+ * until this function has been called, on the layers' stream: it puts the
+ * workspace in order again, whatever code stands in the error word. */
 rssm_status rssm_attn_get_error(rssm_attn* h, int32_t* err4, void* stream);
 
 /* Free the host handle; caches and workspace stay the caller's. */

@@ -430,6 +430,28 @@ def test_layers_of_other_shapes_on_one_workspace(cuda_lib, one, two):
             assert layer.get_error() == (0, 0, 0, 0)
 
 
+@pytest.mark.parametrize("first", [rssm.RSSM_DEV_TIMEOUT, rssm.RSSM_DEV_ATTN_LEN])
+def test_workspace_after_a_wait_ran_out(cuda_lib, first):
+    """What a call that gave up leaves (its mark beside the error word, whatever
+    code came first, and counters between zero and their last value) is cleared
+    by get_error; the state is written by the host, no wait runs out here."""
+    c = Case([3000, 200, 77], q_heads=4, kv_heads=2, dim=64, seed=7)
+    layer = c.layer()
+    want = c.run(layer)
+    words = layer.workspace.view(torch.int32)
+    counters = slice(64, 64 + 3 * 304)             # behind the error word's 256 bytes: a count per block, two per round
+    torch.cuda.synchronize()
+    assert not bool(words[counters].any())
+    words[:5] = torch.tensor([first, 3, -1, 0, 1], dtype=torch.int32)
+    words[counters] = 1
+    assert layer.get_error() == (first, 3, -1, 0)
+    torch.cuda.synchronize()
+    assert not bool(words[:64 + 3 * 304].any())
+    got = c.run(layer)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert layer.get_error() == (0, 0, 0, 0)
+
+
 def test_fewer_drafts_than_the_most(cuda_lib):
     c = Case([90, 33], T=1, q_heads=16, kv_heads=2, dim=128, seed=3)
     c.check(c.run(c.layer(max_draft=8)))
