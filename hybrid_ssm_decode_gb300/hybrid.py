@@ -246,6 +246,7 @@ class Attention:
             _need(c.dtype == k_cache.dtype and c.shape == k_cache.shape, f"{name}: k_cache and v_cache must be alike")
             _need(c.stride()[1:] == (ps * dim, dim, 1), f"{name}: a page must be dense")
         _need(k_cache.stride(0) == v_cache.stride(0) or pages == 1, "k_cache and v_cache: page strides differ")
+        _need(k_cache.stride(0) >= heads * ps * dim or pages == 1, "k_cache and v_cache: pages overlap")
         fp8 = kv == _r.RSSM_KV_FP8
         for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             _need((s is not None) == fp8, f"{name}: given for float8 caches, and only for them")

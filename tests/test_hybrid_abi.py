@@ -174,6 +174,24 @@ def test_norm_host_errors(lib):
     assert gated(rows=0, y=None, z=None, w=None, o=None) == OK
 
 
+def _any_device(monkeypatch):
+    """Lets CPU tensors past the device check: what comes next is tested."""
+    monkeypatch.setattr(rssm.hybrid, "_cuda", lambda device, name: None)
+
+
+def test_binding_refuses_pages_that_overlap(lib, monkeypatch):
+    """A cache expanded over its pages has stride 0, which the library takes for
+    a dense cache of that many pages; so do pages closer than their size."""
+    import torch
+    _any_device(monkeypatch)
+    one = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16)
+    close = torch.zeros(20000, dtype=torch.bfloat16).as_strided((4, 2, 16, 64), (1024, 1024, 64, 1))
+    dense = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    for k, v in ((one.expand(4, 2, 16, 64),) * 2, (close, close), (dense, one.expand(4, 2, 16, 64))):
+        with pytest.raises(ValueError):
+            rssm.Attention(k, v, batch=1, q_heads=2, max_pages=2)
+
+
 def test_binding_refuses_cpu_tensors(lib):
     """The checks come before any call of the library."""
     import torch
