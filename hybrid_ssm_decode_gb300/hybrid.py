@@ -262,6 +262,7 @@ class Attention:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         _on(workspace, self.device, "workspace")
+        _need(workspace.is_contiguous(), "workspace: must be dense")
         self.workspace = workspace
         self._tensors = (k_cache, v_cache, k_scale, v_scale)
         self._seen = {}

@@ -192,6 +192,17 @@ def test_binding_refuses_pages_that_overlap(lib, monkeypatch):
             rssm.Attention(k, v, batch=1, q_heads=2, max_pages=2)
 
 
+def test_binding_refuses_a_workspace_that_is_not_dense(lib, monkeypatch):
+    """Its size is taken for the bytes behind its address."""
+    import torch
+    _any_device(monkeypatch)
+    cache = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    need = rssm.rssm_attn_workspace_size(_attn(batch=1, q_heads=2, head_dim=64, num_pages=4, max_pages=2))
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            rssm.Attention(cache, cache, batch=1, q_heads=2, max_pages=2, workspace=ws)
+
+
 def test_binding_refuses_cpu_tensors(lib):
     """The checks come before any call of the library."""
     import torch
