@@ -2,9 +2,9 @@
 table of a batch (``PageTable``), an attention layer over a paged cache
 (``Attention``), and the norms around a block (``add_norm``, ``gated_norm``).
 
-Each call checks its tensors' type, device, shape and strides, and then makes
-one call of the C ABI (include/rssm.h) on the given stream, or torch's current
-one. Nothing here synchronises or copies; a ValueError names the argument that
+Each call checks its tensors' type, device (the current one), shape and strides,
+and then makes one call of the C ABI (include/rssm.h) on the given stream, or torch's
+current one. Nothing here synchronises or copies; a ValueError names the argument that
 does not fit, and an RssmError a status of the library.
 
 A decode step makes these calls by the dozen, and a kernel of theirs takes a few
@@ -44,20 +44,29 @@ def _raw_stream(device_index):
     return torch.cuda.current_stream(device_index).cuda_stream
 
 
+def _current_device():
+    return _torch().cuda.current_device()
+
+
 def _stream_of(stream, device_index):
+    """The stream of a call on tensors of a device, which has to be the current
+    one: the library launches there."""
+    if device_index != _current_device():
+        raise ValueError(f"tensors on cuda:{device_index}, but the current device is cuda:{_current_device()}")
     if stream is None:
         return _raw_stream(device_index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _bind():
-    """The library's functions and torch's raw-stream query, once both are loaded."""
-    global _lib, _raw_stream
+    """The library's functions and torch's raw queries, once both are loaded."""
+    global _lib, _raw_stream, _current_device
     if _lib is None:
         _lib = _r.load()
         raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:
             _raw_stream = raw
+        _current_device = getattr(_torch()._C, "_cuda_getDevice", _current_device)
     return _lib
 
 
@@ -117,7 +126,9 @@ class PageTable:
         _cuda(self.device, "device")
         if free is not None:
             _ints(free, num_pages, self.device, "free")
-        self.handle = _r.rssm_pages_create(self.cfg, self.workspace, self.layout.total_bytes, free, stream)
+        self._fn = _bind()
+        self.handle = _r.rssm_pages_create(self.cfg, self.workspace, self.layout.total_bytes, free,
+                                           _stream_of(stream, self.device.index))
         lay = self.layout
 
         def view(off, *shape):
@@ -127,7 +138,6 @@ class PageTable:
             return self.workspace[off:off + 4 * n].view(torch.int32).view(*shape)
 
         self._seen = {}
-        self._fn = _bind()
         self.lens = view(lay.lens, batch)
         self.table = view(lay.table, batch, max_pages)
         self.free_count = view(lay.free_count, 1)
@@ -186,7 +196,7 @@ class PageTable:
             _keep(self._seen, key, True)
 
     def get_error(self, stream=None):
-        return _r.rssm_pages_get_error(self.handle, stream)
+        return _r.rssm_pages_get_error(self.handle, _stream_of(stream, self.device.index))
 
 
 def _tokens(t, n, heads, dim, dtype, device, name):
@@ -268,7 +278,8 @@ class Attention:
         self._seen = {}
         self._fn = _bind()
         self.handle = _r.rssm_attn_create(self.cfg, k_cache, v_cache, k_scale, v_scale, workspace,
-                                          workspace.numel() * workspace.element_size(), stream)
+                                          workspace.numel() * workspace.element_size(),
+                                          _stream_of(stream, self.device.index))
 
     def close(self):
         if self.handle:
@@ -326,7 +337,7 @@ class Attention:
         return step
 
     def get_error(self, stream=None):
-        return _r.rssm_attn_get_error(self.handle, stream)
+        return _r.rssm_attn_get_error(self.handle, _stream_of(stream, self.device.index))
 
 
 def _rows(t, rows, dim, device, name):

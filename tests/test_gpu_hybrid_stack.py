@@ -158,6 +158,30 @@ def test_requests_come_and_go(cuda_lib):
     fresh.close()
 
 
+def test_calls_refuse_a_device_that_is_not_current(cuda_lib, monkeypatch):
+    """Every call, with signatures seen before and new ones; nothing is launched."""
+    bf16 = torch.bfloat16
+    pages = rssm.PageTable(2, 16, 8, 2)
+    cache = torch.zeros((8, 2, 16, 64), dtype=bf16, device="cuda")
+    attn = rssm.Attention(cache, cache, batch=2, q_heads=2, max_pages=2)
+    one, x, w = torch.ones(2, dtype=torch.int32, device="cuda"), torch.ones((2, 2, 64), dtype=bf16, device="cuda"), torch.ones(64, device="cuda")
+    row = x[:, 0].contiguous()
+    calls = [lambda: pages.extend(one.clone(), T=1), lambda: pages.rollback(1, one), lambda: pages.truncate(one), lambda: pages.get_error(),
+             lambda: attn.append(x, x, one), lambda: attn.decode(torch.empty_like(x).view(2, 1, 2, 64), x, one, pages.table),
+             lambda: attn.get_error(), lambda: rssm.add_norm(row.clone(), row, w), lambda: rssm.gated_norm(row.clone(), row, row, w),
+             lambda: rssm.PageTable(2, 16, 8, 2), lambda: rssm.Attention(cache, cache, batch=2, q_heads=2, max_pages=2)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    before = pages.workspace.clone()
+    monkeypatch.setattr(rssm.hybrid, "_current_device", lambda: torch.cuda.current_device() + 1, raising=False)
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(before, pages.workspace)
+
+
 def test_refuses_a_bad_shape(cuda_lib):
     with pytest.raises(ValueError):
         HybridStack(HybridShape(pattern="MX", batch=1))

@@ -203,6 +203,16 @@ def test_binding_refuses_a_workspace_that_is_not_dense(lib, monkeypatch):
             rssm.Attention(cache, cache, batch=1, q_heads=2, max_pages=2, workspace=ws)
 
 
+def test_binding_refuses_a_device_that_is_not_current(monkeypatch):
+    """A launch goes to the current device, whatever the tensors' own: the check
+    that every call makes as it takes its stream."""
+    monkeypatch.setattr(rssm.hybrid, "_current_device", lambda: 1, raising=False)
+    for stream in (None, 64):
+        with pytest.raises(ValueError):
+            rssm.hybrid._stream_of(stream, 0)
+    assert rssm.hybrid._stream_of(64, 1) == 64
+
+
 def test_binding_refuses_cpu_tensors(lib):
     """The checks come before any call of the library."""
     import torch
