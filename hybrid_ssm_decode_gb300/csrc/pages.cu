@@ -619,7 +619,7 @@ rssm_status rssm_pages_create(const rssm_pages_config* cfg, void* d_workspace, s
 
 rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, int32_t* d_slots,
                               int32_t* d_positions, int32_t max_tokens, void* stream) {
-    if (h == nullptr || d_slots == nullptr || max_tokens < 0) return RSSM_ERR_INVALID_ARG;
+    if (h == nullptr || max_tokens < 0 || (d_slots == nullptr && max_tokens > 0)) return RSSM_ERR_INVALID_ARG;
     if (!aligned4(d_slots) || !aligned4(d_positions) || !aligned4(d_new)) return RSSM_ERR_INVALID_ARG;
     if (d_new == nullptr ? (T < 1 || static_cast<int64_t>(T) * h->cfg.batch > max_tokens) : T != 0)
         return RSSM_ERR_INVALID_ARG;

@@ -558,9 +558,9 @@ rssm_status rssm_pages_create(const rssm_pages_config* cfg, void* d_workspace, s
 /* Room for more tokens, and where they go.
  *   T, d_new     d_new == NULL: T >= 1 tokens for every request; else T = 0 and
  *                d_new is device int32 [batch] (0 leaves a request as it is).
- *   d_slots      device int32 [max_tokens]: slot of every new token, request
- *                after request (request b's first token at the sum of new over the
- *                requests before it; T tokens each: [batch][T]).
+ *   d_slots      device int32 [max_tokens] (NULL where that is 0): slot of every
+ *                new token, request after request (request b's first token at the
+ *                sum of new over the requests before it; T tokens each: [batch][T]).
  *   d_positions  NULL or device int32 [max_tokens]: each new token's position in
  *                its request.
  * A request that cannot be served (no page left, row full, count < 0, slots

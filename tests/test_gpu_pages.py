@@ -266,6 +266,14 @@ def test_refusals_of_each_kind_are_marked(cuda_lib):
     assert pt.lens.tolist() == [15, 16, 4, 1]
 
 
+def test_extend_by_nothing(cuda_lib):
+    """No slots, and counts that are all 0."""
+    pt = rssm.PageTable(4, 16, 8, 2)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    pt.extend(none, new=_i32([0, 0, 0, 0]), positions=none)
+    assert pt.get_error()[0] == 0 and pt.lens.tolist() == [0] * 4
+
+
 def test_binding_refuses(cuda_lib):
     pt = rssm.PageTable(4, 16, 8, 2)
     good = torch.empty(8, dtype=torch.int32, device="cuda")
