@@ -203,7 +203,7 @@ __device__ __forceinline__ void extend_round(const PagesArgs& a, int b, ScanBuf&
     const Scan before = scan;
     scan.run<true>(buf, upto, tok_end);
     if (scan.cy <= a.max_tokens) return;                       // uniform: the lists hold every token so far
-    if (r.bad == 0 && tok_end > a.max_tokens) {
+    if (r.bad == 0 && r.count > 0 && tok_end > a.max_tokens) {
         r.bad = RSSM_DEV_PAGES_SLOTS;
         r.need = 0;
     }

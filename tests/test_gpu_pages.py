@@ -274,6 +274,20 @@ def test_extend_by_nothing(cuda_lib):
     assert pt.get_error()[0] == 0 and pt.lens.tolist() == [0] * 4
 
 
+def test_a_request_that_asks_for_nothing_is_not_refused(cuda_lib):
+    """Behind requests that the slot list cannot hold, and an empty pool."""
+    pt = rssm.PageTable(4, 16, 2, 2)
+    slots = torch.empty(3, dtype=torch.int32, device="cuda")
+    pt.extend(slots, new=_i32([2, 2, 0, 1]))
+    assert pt.get_error()[:2] == (rssm.RSSM_DEV_PAGES_SLOTS, 2)
+    assert pt.refused.tolist() == [0, 1, 0, 1] and pt.lens.tolist() == [2, 0, 0, 0]
+    pt.extend(torch.empty(0, dtype=torch.int32, device="cuda"), new=_i32([0, 1, 0, 1]))
+    assert pt.get_error()[:2] == (rssm.RSSM_DEV_PAGES_SLOTS, 2)
+    pt.extend(torch.empty(40, dtype=torch.int32, device="cuda"), new=_i32([0, 16, 0, 16]))
+    assert pt.get_error() == (rssm.RSSM_DEV_PAGES_EMPTY, 1, 3, 16)
+    assert pt.refused.tolist() == [0, 0, 0, 1] and pt.lens.tolist() == [2, 16, 0, 0]
+
+
 def test_binding_refuses(cuda_lib):
     pt = rssm.PageTable(4, 16, 8, 2)
     good = torch.empty(8, dtype=torch.int32, device="cuda")
