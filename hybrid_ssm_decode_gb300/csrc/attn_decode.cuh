@@ -416,7 +416,7 @@ struct Warp {
             for (int k = 0; k < kQRegs; ++k) ldsm4(qf[k], at + k * 32);
         } else {
             // columns permuted within 16 so that a lane's four K codes are its
-            // own; each row scaled by a power of two so that its largest value
+            // own; each row scaled by a power of two so that its largest finite value
             // lies in [2^14, 2^15)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -425,13 +425,13 @@ struct Warp {
 #pragma unroll
                 for (int k = 0; k < kQRegs; ++k) {
                     const float4 v = load4(reinterpret_cast<const __nv_bfloat16*>(row + k * 32 + c * 8));
-                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                    for (const float x : {v.x, v.y, v.z, v.w}) mx = fabsf(x) < INFINITY ? fmaxf(mx, fabsf(x)) : mx;
                 }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                // e with mx in [2^e, 2^(e+1)); zero, subnormal and non-finite rows stay as they are
+                // e with mx in [2^e, 2^(e+1)); rows without a normal number stay as they are
                 int e = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFF) - 127;
-                if (e > 127 || e < -126) e = 14;
+                if (e < -126) e = 14;
                 const int up = 14 - e, half = up / 2;        // 2^up may pass FP32: two factors
                 const float f1 = pow2(half), f2 = pow2(up - half);
                 mul[h] = scale_log2 * kscale * pow2(-half) * pow2(half - up);

@@ -204,6 +204,20 @@ def test_fp8_query_range(cuda_lib, mag):
     assert bool(((out >= (want - lim).to(out.dtype)) & (out <= (want + lim).to(out.dtype))).all())
 
 
+@pytest.mark.parametrize("mag", [1.0, 1e6, 1e30])
+def test_fp8_infinite_query(cuda_lib, mag):
+    """Beside an infinite query element the others, whatever their size, stay
+    finite: a row whose scores are all -inf is empty."""
+    c = Case([50], q_heads=4, kv_heads=2, dim=64, kv="fp8", seed=4)
+    raw = c.k_cache.view(torch.uint8)
+    raw[c.table[0, :4].long()] |= 0x80                         # keys below zero, one dimension apart from it
+    raw[..., 5].clamp_(min=0x88)
+    c.q = (c.q.float().abs() * mag).neg().to(torch.bfloat16)   # finite terms above zero
+    c.q[..., 5] = math.inf
+    out, lse = c.run()
+    assert not bool(out.any()) and bool((lse == -math.inf).all())
+
+
 @pytest.mark.parametrize("dim,T,lens", [(64, 1, [5000, 64]), (128, 1, [20000]), (256, 4, [3000, 100])])
 def test_fp8_small_weights(cuda_lib, dim, T, lens):
     """A long tail under a few large scores: every 16th token scores 18 above the
