@@ -3,16 +3,19 @@
 // SSM mixer, fused with its gate).
 //
 // Both read each input once and write each output once: a row (add_norm) or a
-// group of a row's columns (gated_norm) is held in registers, in FP32, from
-// its load through one or two sums of squares to its store. They are bound by
-// HBM for many rows (add_norm 6.3 TB/s, gated_norm 5.8) and by latency for few (one row of 4096: 2.1 us
-// from a CUDA graph).
+// group of a row's columns (gated_norm) is held by the threads of a block, in FP32, from
+// its load through one or two sums of squares to its store: in registers up to 8192
+// columns read 8 at a time, or read one by one. What is longer spills, most of a
+// thread's share above 8192 columns one by one (0.9 to 2 KB a thread) and above 16384
+// 8 at a time (0.2 to 1.1 KB; gated_norm loses up to 0.35 KB from 8192 on). They are
+// bound by HBM for many rows (add_norm 6.3 TB/s, gated_norm 5.8) and by latency for few
+// (one row of 4096: 2.1 us from a CUDA graph).
 #include "overlap.cuh"
 
 namespace rssm {
 namespace {
 
-constexpr int kMaxNormDim = 32768;   // columns that the threads of one block hold in registers
+constexpr int kMaxNormDim = 32768;   // columns that the threads of one block hold
 
 struct AddNormArgs {
     const void *u, *x, *gate;
@@ -195,8 +198,9 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a, int
 }
 
 // act(z). FP32 keeps the exact exponential and division; for BF16 their
-// approximations, within 2^-20, are far inside the rounding and a quarter of the
-// instructions.
+// approximations are far inside the rounding and a quarter of the instructions: within
+// 2^-20 for |z| <= 8, and, as the rounded product with log2 e grows, within 2^-17 as
+// long as the sigmoid is a normal number (z > -87; it is 0 from there on).
 template <class T, int ACT>
 __device__ __forceinline__ float gate_of(float z) {
     if (sizeof(T) == 4) return (ACT == RSSM_GATE_SILU ? z : 1.f) / (1.f + expf(-z));
@@ -206,11 +210,6 @@ __device__ __forceinline__ float gate_of(float z) {
     return ACT == RSSM_GATE_SILU ? z * r : r;
 }
 
-// Short groups are bound by instructions before memory: one group a thread cost 39
-// an element and 84 us over 16384 rows of 32 BF16 groups of 128. So a thread takes
-// several groups, with the weights of its columns in registers where all groups
-// share them (80 us), and loads the next group beside the sums of this one, which
-// doubles what is under way at 4 blocks of 256 an SM (70 us, 5.7 TB/s).
 // VEC elements as they are stored, so that a load can be long under way before
 // the values are widened.
 template <class T, int VEC>
@@ -243,6 +242,11 @@ struct Raw {
     }
 };
 
+// Short groups are bound by instructions before memory: one group a thread cost 39
+// an element and 84 us over 16384 rows of 32 BF16 groups of 128. So a thread takes
+// several groups, with the weights of its columns in registers where all groups
+// share them (80 us), and loads the next group beside the sums of this one, which
+// doubles what is under way at 4 blocks of 256 an SM (69 us, 5.8 TB/s).
 template <class T, int VEC, int VPT, int FIRST, int ACT>
 __global__ void __launch_bounds__(1024) gated_norm_kernel(const GatedNormArgs a, int tpr, uint32_t items) {
     __shared__ float s_red[2][32];

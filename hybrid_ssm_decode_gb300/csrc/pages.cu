@@ -26,7 +26,8 @@ constexpr int kPagesThreads = 1024;     // most of the kernels that share items 
 constexpr int kItemsPerBlock = 1024;
 // Unused shared memory of the kernels that share items out, so that no SM takes more
 // than two of their blocks: beside the end of the kernel before, early blocks would
-// crowd onto the SMs that are free (256 prompts: 39 us; plain launches 26; this 23).
+// crowd onto the SMs that are free (256 prompts after as many leave: 39 us; plain
+// launches 26; this 21.5).
 constexpr int kSpread = 88 * 1024;
 constexpr int kRun = 8;                 // tokens that a thread takes in a row
 constexpr int kStepThreads = 1024;      // most of the single-block kernels

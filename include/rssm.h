@@ -565,7 +565,9 @@ rssm_status rssm_pages_create(const rssm_pages_config* cfg, void* d_workspace, s
  *                its request.
  * A request that cannot be served (no page left, row full, count < 0, slots
  * short) is left unchanged, its tokens' slots and positions are -1, and the
- * error word and its mark are set; the others are served. Entries past the last token are
+ * error word and its mark are set; the others are served. (Pages go out in the
+ * order of the requests: behind the first that the pool cannot cover, no request
+ * that needs a page gets one, though it were fewer than are left.) Entries past the last token are
  * not written. d_slots and d_positions: 4-byte aligned.
  * Errors: INVALID_ARG (null, T, max_tokens < batch*T where d_new is NULL), CUDA. */
 rssm_status rssm_pages_extend(rssm_pages* h, int32_t T, const int32_t* d_new, int32_t* d_slots,
