@@ -8,7 +8,8 @@ The functions keep the C names (``rssm_create``, ``rssm_decode_step``, ...)
 and take torch CUDA tensors, or raw device addresses, where the C ABI takes
 device pointers. ``Layer`` bundles a workspace tensor and a handle for
 convenience. The attention side of a hybrid decode step is in ``hybrid``:
-``PageTable``, ``Attention``, ``add_norm`` and ``gated_norm``.
+``PageTable``, ``Attention``, ``Rope``, ``rotary``, ``add_norm`` and
+``gated_norm``.
 """
 from __future__ import annotations
 
@@ -43,9 +44,12 @@ READ_FMT = {"none": RSSM_READ_NONE, "fp8": RSSM_READ_FP8, "nvfp4": RSSM_READ_NVF
 DTYPE = {"f32": RSSM_F32, "bf16": RSSM_BF16}
 RSSM_DEV_PAGES_EMPTY, RSSM_DEV_PAGES_ROW, RSSM_DEV_PAGES_COUNT, RSSM_DEV_PAGES_SLOTS, RSSM_DEV_ATTN_LEN, \
     RSSM_DEV_ATTN_PAGE, RSSM_DEV_ATTN_SLOT = range(16, 23)
-RSSM_KV_FP8 = 4
+RSSM_KV_FP8, RSSM_KV_NVFP4 = 4, 5
 RSSM_GATE_SILU, RSSM_GATE_SIGMOID = 1, 2
 GATE = {"silu": RSSM_GATE_SILU, "sigmoid": RSSM_GATE_SIGMOID}
+RSSM_ROPE_PLAIN, RSSM_ROPE_LINEAR, RSSM_ROPE_NTK, RSSM_ROPE_YARN, RSSM_ROPE_WAVELENGTH = range(5)
+ROPE = {"none": RSSM_ROPE_PLAIN, "linear": RSSM_ROPE_LINEAR, "ntk": RSSM_ROPE_NTK, "yarn": RSSM_ROPE_YARN,
+        "wavelength": RSSM_ROPE_WAVELENGTH}
 
 
 class RssmError(RuntimeError):
@@ -87,6 +91,14 @@ def _f32(*names):
     return [(n, ctypes.c_float) for n in names]
 
 
+def _f64(*names):
+    return [(n, ctypes.c_double) for n in names]
+
+
+def _ptr(*names):
+    return [(n, ctypes.c_void_p) for n in names]
+
+
 class PagesConfig(ctypes.Structure):
     _fields_ = _i32("batch", "page_size", "num_pages", "max_pages")
 
@@ -98,6 +110,20 @@ class PagesLayout(ctypes.Structure):
 class AttnConfig(ctypes.Structure):
     _fields_ = (_i32("batch", "q_heads", "kv_heads", "head_dim", "page_size", "num_pages", "max_pages", "max_draft",
                      "in_dtype", "kv_dtype", "window") + _f32("scale") + _i64("page_stride"))
+
+
+class AttnRotary(ctypes.Structure):
+    _fields_ = (_i32("rotary_dim", "interleaved") + _f32("gain") + _ptr("d_turns", "d_positions", "d_q", "d_q_out")
+                + _i64("q_stride", "q_out_stride"))
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = _i32("rotary_dim", "scaling") + _f64("base", "factor", "original", "fast", "slow", "gain")
+
+
+class RotaryConfig(ctypes.Structure):
+    _fields_ = (_i64("tokens") + _i32("heads", "dim", "rotary_dim", "interleaved", "dtype") + _f32("gain")
+                + _i64("x_stride", "out_stride"))
 
 
 class AddNormConfig(ctypes.Structure):
@@ -205,9 +231,15 @@ def load():
             "rssm_attn_workspace_size": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(sz)], i32),
             "rssm_attn_create": ([ctypes.POINTER(AttnConfig), p, p, p, p, p, sz, p, ctypes.POINTER(p)], i32),
             "rssm_attn_append": ([p, i32, p, i64, p, i64, p, p], i32),
+            "rssm_attn_append_rotary": ([p, i32, p, i64, p, i64, p, ctypes.POINTER(AttnRotary), p], i32),
+            "rssm_attn_read": ([p, i32, p, p, i64, p, i64, p], i32),
             "rssm_attn_decode": ([p, i32, p, i64, p, p, p, p, p], i32),
             "rssm_attn_get_error": ([p, ctypes.POINTER(i32), p], i32),
             "rssm_attn_destroy": ([p], i32),
+            "rssm_rope_frequencies": ([ctypes.POINTER(RopeConfig), ctypes.POINTER(ctypes.c_double),
+                                       ctypes.POINTER(ctypes.c_float)], i32),
+            "rssm_rope_turns": ([i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_uint64)], i32),
+            "rssm_rotary": ([ctypes.POINTER(RotaryConfig), p, p, p, p, p], i32),
             "rssm_add_norm": ([ctypes.POINTER(AddNormConfig), p, p, p, p, p, p, p, p], i32),
             "rssm_gated_norm": ([ctypes.POINTER(GatedNormConfig), p, p, p, p, p], i32),
         }
@@ -405,6 +437,18 @@ def rssm_attn_append(handle: int, tokens: int, k, k_stride: int, v, v_stride: in
                                                        _addr(slots), _stream(stream)))
 
 
+def rssm_attn_append_rotary(handle: int, tokens: int, k, k_stride: int, v, v_stride: int, slots, rotary: AttnRotary,
+                            stream=None) -> None:
+    _check("rssm_attn_append_rotary",
+           load().rssm_attn_append_rotary(handle, tokens, _addr(k), k_stride, _addr(v), v_stride, _addr(slots),
+                                          ctypes.byref(rotary), _stream(stream)))
+
+
+def rssm_attn_read(handle: int, tokens: int, slots, k, k_stride: int, v, v_stride: int, stream=None) -> None:
+    _check("rssm_attn_read", load().rssm_attn_read(handle, tokens, _addr(slots), _addr(k), k_stride, _addr(v), v_stride,
+                                                   _stream(stream)))
+
+
 def rssm_attn_decode(handle: int, T: int, q, q_stride: int, lens, table, out, lse=None, stream=None) -> None:
     _check("rssm_attn_decode", load().rssm_attn_decode(handle, T, _addr(q), q_stride, _addr(lens), _addr(table),
                                                        _addr(out), _addr(lse), _stream(stream)))
@@ -418,6 +462,26 @@ def rssm_attn_get_error(handle: int, stream=None) -> tuple:
 
 def rssm_attn_destroy(handle: int) -> None:
     _check("rssm_attn_destroy", load().rssm_attn_destroy(handle))
+
+
+def rssm_rope_frequencies(cfg: RopeConfig) -> tuple:
+    """(frequencies, gain) of a configuration: rotary_dim/2 doubles, and a float."""
+    freq, gain = (ctypes.c_double * max(1, cfg.rotary_dim // 2))(), ctypes.c_float(0)
+    _check("rssm_rope_frequencies", load().rssm_rope_frequencies(ctypes.byref(cfg), freq, ctypes.byref(gain)))
+    return list(freq), gain.value
+
+
+def rssm_rope_turns(freq) -> list:
+    """Frequencies (radians a position) as whole numbers of 2^-64 turns a position."""
+    n = len(freq)
+    out = (ctypes.c_uint64 * max(1, n))()
+    _check("rssm_rope_turns", load().rssm_rope_turns(n, (ctypes.c_double * max(1, n))(*freq), out))
+    return list(out)
+
+
+def rssm_rotary(cfg: RotaryConfig, x, positions, turns, out, stream=None) -> None:
+    _check("rssm_rotary", load().rssm_rotary(ctypes.byref(cfg), _addr(x), _addr(positions), _addr(turns), _addr(out),
+                                             _stream(stream)))
 
 
 def rssm_add_norm(cfg: AddNormConfig, u, x, w_post, gate, w, u_out, n_out, stream=None) -> None:
@@ -525,4 +589,4 @@ class Layer:
 # --------------------------------------------------------------------------
 # convenience: the attention side on torch tensors (hybrid.py)
 # --------------------------------------------------------------------------
-from .hybrid import Attention, PageTable, add_norm, gated_norm  # noqa: E402
+from .hybrid import Attention, PageTable, Rope, add_norm, gated_norm, rotary  # noqa: E402

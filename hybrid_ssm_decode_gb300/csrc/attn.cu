@@ -65,7 +65,12 @@ struct AttnLayout {
     size_t err, arrived, arrived_round, part_ml, part_o, total;
 };
 
+// Of a cache's element; NVFP4 caches count bytes.
 int elem_size(int kv_dtype) { return kv_dtype == RSSM_F32 ? 4 : kv_dtype == RSSM_BF16 ? 2 : 1; }
+bool scaled(int kv_dtype) { return kv_dtype == RSSM_KV_FP8 || kv_dtype == RSSM_KV_NVFP4; }
+int64_t page_elems(const rssm_attn_config& c) {
+    return static_cast<int64_t>(c.kv_heads) * c.page_size * (kv_row_bytes(c.kv_dtype, c.head_dim) / elem_size(c.kv_dtype));
+}
 
 rssm_status attn_check(const rssm_attn_config* c) {
     if (c == nullptr || c->batch < 1 || c->q_heads < 1 || c->kv_heads < 1 || c->head_dim < 1 || c->page_size < 1 ||
@@ -73,14 +78,14 @@ rssm_status attn_check(const rssm_attn_config* c) {
         return RSSM_ERR_INVALID_ARG;
     if (c->q_heads % c->kv_heads != 0) return RSSM_ERR_INVALID_ARG;
     if (c->in_dtype != RSSM_F32 && c->in_dtype != RSSM_BF16) return RSSM_ERR_INVALID_ARG;
-    if (c->kv_dtype != RSSM_F32 && c->kv_dtype != RSSM_BF16 && c->kv_dtype != RSSM_KV_FP8) return RSSM_ERR_INVALID_ARG;
+    if (c->kv_dtype != RSSM_F32 && c->kv_dtype != RSSM_BF16 && !scaled(c->kv_dtype)) return RSSM_ERR_INVALID_ARG;
     if (!(c->scale == c->scale) || c->scale - c->scale != 0.f) return RSSM_ERR_INVALID_ARG;   // NaN, infinite
     if (static_cast<int64_t>(c->num_pages) * c->page_size > 0x7FFFFFFF ||
         static_cast<int64_t>(c->max_pages) * c->page_size > 0x7FFFFFFF ||
         static_cast<int64_t>(c->batch) * c->max_pages > 0x7FFFFFFF ||
         static_cast<int64_t>(c->batch) * c->q_heads * c->max_draft > 0x7FFFFFFF)
         return RSSM_ERR_INVALID_ARG;
-    const int64_t page = static_cast<int64_t>(c->kv_heads) * c->page_size * c->head_dim;
+    const int64_t page = page_elems(*c);
     if (c->page_stride != 0 && (c->page_stride < page || (c->page_stride * elem_size(c->kv_dtype)) % 16 != 0 ||
                                 c->page_stride >= (1ll << 38)))
         return RSSM_ERR_INVALID_ARG;
@@ -129,10 +134,21 @@ EncodeFn encode_fn() {
 
 // A cache as bytes [page][head][128-byte chunk of a token][token of the page][byte],
 // boxes of 16 tokens of one head: a slot's rows are 128 bytes (64 for FP8 heads
-// of 64) under the swizzle of that width.
+// of 64) under the swizzle of that width. NVFP4: groups of 16 tokens are one piece of
+// 9 head_dim bytes [page][head][group][row of up to 1152 bytes][8 bytes].
 bool encode_cache(CUtensorMap* m, void* base, const rssm_attn_config& c) {
     const EncodeFn fn = encode_fn();
     if (fn == nullptr) return false;
+    if (c.kv_dtype == RSSM_KV_NVFP4) {
+        const cuuint64_t gb = 9 * static_cast<cuuint64_t>(c.head_dim), cb = gb < 1152 ? gb : 1152, n = c.page_size / kAttnGroup;
+        const cuuint64_t page = c.page_stride ? c.page_stride : gb * n * c.kv_heads;
+        const cuuint64_t dims[5] = {cb / 8, gb / cb, n, static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.num_pages)};
+        const cuuint64_t strides[4] = {cb, gb, gb * n, page};
+        const cuuint32_t box[5] = {static_cast<cuuint32_t>(cb / 8), static_cast<cuuint32_t>(gb / cb), 1, 1, 1};
+        const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_INT64, 5, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
     const cuuint64_t es = elem_size(c.kv_dtype), rb = es * c.head_dim, cb = rb < 128 ? rb : 128;
     const cuuint64_t page = c.page_stride ? c.page_stride * es : rb * c.page_size * c.kv_heads;
     const cuuint64_t dims[5] = {cb, static_cast<cuuint64_t>(c.page_size), rb / cb, static_cast<cuuint64_t>(c.kv_heads),
@@ -182,6 +198,50 @@ cudaError_t launch_append(const rssm_attn* h, int tokens, const void* k, int64_t
     return wide ? go(attn_append_kernel<TI, TO, kWide>) : go(attn_append_kernel<TI, TO, 1>);
 }
 
+// What the writer and the reader of place.cu need of a layer.
+PlaceArgs place_args(const rssm_attn* h, int tokens, const void* k, int64_t ks, const void* v, int64_t vs, const int32_t* slots) {
+    const rssm_attn_config& c = h->cfg;
+    PlaceArgs a{};
+    a.k = k;
+    a.v = v;
+    a.k_stride = ks;
+    a.v_stride = vs;
+    a.slots = slots;
+    a.k_cache = static_cast<char*>(h->k_cache);
+    a.v_cache = static_cast<char*>(h->v_cache);
+    a.k_scale = h->k_scale;
+    a.v_scale = h->v_scale;
+    a.page_stride = h->page_stride * elem_size(c.kv_dtype);
+    a.tokens = tokens;
+    a.q_heads = c.q_heads;
+    a.heads = c.kv_heads;
+    a.dim = c.head_dim;
+    a.page_size = c.page_size;
+    a.num_pages = c.num_pages;
+    a.in_dtype = c.in_dtype;
+    a.kv_dtype = c.kv_dtype;
+    a.err = reinterpret_cast<int32_t*>(h->base + h->lay.err);
+    return a;
+}
+
+// place.cu counts a tile's units in 32 bits.
+constexpr int64_t kMaxPlaceRow = 1 << 24;
+
+// Checks of the tensors that an append or a read takes; strides of 0 are filled in.
+rssm_status check_tokens(const rssm_attn* h, int32_t tokens, const void* k, int64_t* ks, const void* v, int64_t* vs,
+                         const int32_t* slots) {
+    if (h == nullptr || tokens < 0) return RSSM_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(h->cfg.kv_heads) * h->cfg.head_dim;
+    if (*ks == 0) *ks = row;
+    if (*vs == 0) *vs = row;
+    if (*ks < row || *vs < row) return RSSM_ERR_INVALID_ARG;
+    if (tokens == 0) return RSSM_OK;
+    const uintptr_t es = h->cfg.in_dtype == RSSM_F32 ? 4 : 2;
+    if (k == nullptr || v == nullptr || slots == nullptr || !aligned(slots, 4) || !aligned(k, es) || !aligned(v, es))
+        return RSSM_ERR_INVALID_ARG;
+    return RSSM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -204,8 +264,8 @@ rssm_status rssm_attn_create(const rssm_attn_config* cfg, void* d_k_cache, void*
     if (d_k_cache == nullptr || d_v_cache == nullptr || !aligned(d_k_cache, 16) || !aligned(d_v_cache, 16) ||
         d_workspace == nullptr || !aligned(d_workspace, kAttnAlign))
         return RSSM_ERR_INVALID_ARG;
-    const bool fp8 = cfg->kv_dtype == RSSM_KV_FP8;
-    if ((d_k_scale != nullptr) != fp8 || (d_v_scale != nullptr) != fp8 || !aligned(d_k_scale, 4) || !aligned(d_v_scale, 4))
+    const bool sc = scaled(cfg->kv_dtype);
+    if ((d_k_scale != nullptr) != sc || (d_v_scale != nullptr) != sc || !aligned(d_k_scale, 4) || !aligned(d_v_scale, 4))
         return RSSM_ERR_INVALID_ARG;
     const AttnLayout L = attn_layout(*cfg);
     if (workspace_bytes < L.total) return RSSM_ERR_CAPACITY;
@@ -218,8 +278,7 @@ rssm_status rssm_attn_create(const rssm_attn_config* cfg, void* d_k_cache, void*
     h->v_cache = d_v_cache;
     h->k_scale = d_k_scale;
     h->v_scale = d_v_scale;
-    h->page_stride = cfg->page_stride ? cfg->page_stride
-                                      : static_cast<int64_t>(cfg->kv_heads) * cfg->page_size * cfg->head_dim;
+    h->page_stride = cfg->page_stride ? cfg->page_stride : page_elems(*cfg);
     if (h->cfg.scale == 0.f) h->cfg.scale = cfg->head_dim == 64 ? 0.125f : cfg->head_dim == 128 ? 0.08838834764831845f : 0.0625f;
     bool ok = encode_cache(&h->kmap, d_k_cache, *cfg) && encode_cache(&h->vmap, d_v_cache, *cfg);
     ok = ok && cudaMemsetAsync(h->base, 0, L.part_ml, static_cast<cudaStream_t>(stream)) == cudaSuccess;
@@ -233,23 +292,56 @@ rssm_status rssm_attn_create(const rssm_attn_config* cfg, void* d_k_cache, void*
 
 rssm_status rssm_attn_append(rssm_attn* h, int32_t tokens, const void* d_k, int64_t k_stride, const void* d_v,
                              int64_t v_stride, const int32_t* d_slots, void* stream) {
-    if (h == nullptr || tokens < 0) return RSSM_ERR_INVALID_ARG;
+    const rssm_status st = check_tokens(h, tokens, d_k, &k_stride, d_v, &v_stride, d_slots);
+    if (st != RSSM_OK || tokens == 0) return st;
     const rssm_attn_config& c = h->cfg;
-    const int64_t row = static_cast<int64_t>(c.kv_heads) * c.head_dim;
-    if (k_stride == 0) k_stride = row;
-    if (v_stride == 0) v_stride = row;
-    if (k_stride < row || v_stride < row) return RSSM_ERR_INVALID_ARG;
-    if (tokens == 0) return RSSM_OK;
-    const uintptr_t es = c.in_dtype == RSSM_F32 ? 4 : 2;
-    if (d_k == nullptr || d_v == nullptr || d_slots == nullptr || !aligned(d_slots, 4) || !aligned(d_k, es) || !aligned(d_v, es))
-        return RSSM_ERR_INVALID_ARG;
+    if (c.kv_dtype == RSSM_KV_NVFP4 && static_cast<int64_t>(c.kv_heads) * c.head_dim > kMaxPlaceRow) return RSSM_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (c.kv_dtype == RSSM_F32) e = launch_append<float, float>(h, tokens, d_k, k_stride, d_v, v_stride, d_slots, s);
     else if (c.kv_dtype == RSSM_BF16)
         e = launch_append<__nv_bfloat16, __nv_bfloat16>(h, tokens, d_k, k_stride, d_v, v_stride, d_slots, s);
+    else if (c.kv_dtype == RSSM_KV_NVFP4) e = place_launch(place_args(h, tokens, d_k, k_stride, d_v, v_stride, d_slots), s);
     else e = launch_append<__nv_bfloat16, uint8_t>(h, tokens, d_k, k_stride, d_v, v_stride, d_slots, s);
     return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
+}
+
+rssm_status rssm_attn_append_rotary(rssm_attn* h, int32_t tokens, const void* d_k, int64_t k_stride, const void* d_v,
+                                    int64_t v_stride, const int32_t* d_slots, const rssm_attn_rotary* r, void* stream) {
+    const rssm_status st = check_tokens(h, tokens, d_k, &k_stride, d_v, &v_stride, d_slots);
+    if (st != RSSM_OK) return st;
+    if (r == nullptr) return RSSM_ERR_INVALID_ARG;
+    const rssm_attn_config& c = h->cfg;
+    const int64_t row = static_cast<int64_t>(c.q_heads) * c.head_dim;
+    PlaceArgs a = place_args(h, tokens, d_k, k_stride, d_v, v_stride, d_slots);
+    a.q = r->d_q;
+    a.q_out = r->d_q_out;
+    a.q_stride = r->q_stride ? r->q_stride : row;
+    a.qo_stride = r->q_out_stride ? r->q_out_stride : row;
+    a.positions = r->d_positions;
+    a.turns = r->d_turns;
+    a.gain = r->gain;
+    a.rotary_dim = r->rotary_dim;
+    a.interleaved = r->interleaved;
+    if (a.rotary_dim < 2 || a.rotary_dim % 2 != 0 || a.rotary_dim > c.head_dim || a.interleaved < 0 || a.interleaved > 1 ||
+        !(a.gain - a.gain == 0.f) || a.q_stride < row || a.qo_stride < row || (a.q == nullptr) != (a.q_out == nullptr))
+        return RSSM_ERR_INVALID_ARG;
+    if (row > kMaxPlaceRow) return RSSM_ERR_UNSUPPORTED;
+    if (tokens == 0) return RSSM_OK;
+    const uintptr_t es = c.in_dtype == RSSM_F32 ? 4 : 2;
+    if (a.positions == nullptr || a.turns == nullptr || !aligned(a.positions, 4) || !aligned(a.turns, 8) || !aligned(a.q, es) ||
+        !aligned(a.q_out, es) || (a.q != nullptr && a.q_out == a.q && a.qo_stride != a.q_stride))
+        return RSSM_ERR_INVALID_ARG;
+    return place_launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
+}
+
+rssm_status rssm_attn_read(rssm_attn* h, int32_t tokens, const int32_t* d_slots, void* d_k, int64_t k_stride, void* d_v,
+                           int64_t v_stride, void* stream) {
+    const rssm_status st = check_tokens(h, tokens, d_k, &k_stride, d_v, &v_stride, d_slots);
+    if (st != RSSM_OK || tokens == 0) return st;
+    if (static_cast<int64_t>(h->cfg.kv_heads) * h->cfg.head_dim > kMaxPlaceRow) return RSSM_ERR_UNSUPPORTED;
+    return read_launch(place_args(h, tokens, d_k, k_stride, d_v, v_stride, d_slots), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? RSSM_OK : RSSM_ERR_CUDA;
 }
 
 rssm_status rssm_attn_decode(rssm_attn* h, int32_t T, const void* d_q, int64_t q_stride, const int32_t* d_lens,
@@ -291,7 +383,8 @@ rssm_status rssm_attn_decode(rssm_attn* h, int32_t T, const void* d_q, int64_t q
     a.window = c.window;
     a.scale_log2 = c.scale * 1.4426950408889634f;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const auto launch = c.kv_dtype == RSSM_F32 ? attn_launch_f32 : c.kv_dtype == RSSM_BF16 ? attn_launch_bf16 : attn_launch_fp8;
+    const auto launch = c.kv_dtype == RSSM_F32 ? attn_launch_f32 : c.kv_dtype == RSSM_BF16 ? attn_launch_bf16
+                      : c.kv_dtype == RSSM_KV_FP8 ? attn_launch_fp8 : attn_launch_nvfp4;
     return launch(a, c.head_dim, attn_block_rows(rows, c.kv_dtype, c.head_dim), h->kmap, h->vmap, s) == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }
 

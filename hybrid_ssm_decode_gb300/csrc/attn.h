@@ -19,7 +19,7 @@ struct AttnArgs {
     const int32_t* table;       // [B][max_pages]
     void* out;                  // [B][T][q_heads][D]
     float* lse;                 // [B][T][q_heads] or null
-    const float* k_scale;       // [kv_heads], FP8 caches
+    const float* k_scale;       // [kv_heads], FP8 and NVFP4 caches
     const float* v_scale;
     int32_t* err;               // error word [4]; [4]: a wait ran out, and the counters are not at zero
     uint32_t* arrived;          // [blocks], by the block of the request and head's first part, 0 between launches
@@ -32,14 +32,44 @@ struct AttnArgs {
 };
 
 // Query rows (drafts x heads of a cache head) that one block takes, for `rows` in
-// all: 16, 32 or 64. FP32 heads of 256 stop at 32: the ring's slots are 32 KB there.
+// all: 16, 32 or 64, and 8 over NVFP4 caches, whose kernel takes rows by eights. FP32
+// heads of 256 stop at 32: the ring's slots are 32 KB there.
 inline int attn_block_rows(int rows, int kv_dtype, int D) {
-    return rows <= 16 ? 16 : rows <= 32 || (kv_dtype == RSSM_F32 && D == 256) ? 32 : 64;
+    return kv_dtype == RSSM_KV_NVFP4 && rows <= 8 ? 8
+         : rows <= 16 ? 16 : rows <= 32 || (kv_dtype == RSSM_F32 && D == 256) ? 32 : 64;
 }
 
-// The kernels by cache type (attn_f32.cu, attn_bf16.cu, attn_fp8.cu).
+// The kernels by cache type (attn_f32.cu, attn_bf16.cu, attn_fp8.cu, attn_nvfp4.cu).
 cudaError_t attn_launch_f32(const AttnArgs& a, int D, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
 cudaError_t attn_launch_bf16(const AttnArgs& a, int D, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
 cudaError_t attn_launch_fp8(const AttnArgs& a, int D, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
+cudaError_t attn_launch_nvfp4(const AttnArgs& a, int D, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
+
+// Rotary positions of q and k, and keys and values to and from a cache (place.cu).
+struct PlaceArgs {
+    const void *k, *v;          // new tokens [tokens][heads][dim]
+    const void* q;              // with rotary positions: null, or queries [tokens][q_heads][dim] to rotate
+    void* q_out;
+    int64_t k_stride, v_stride, q_stride, qo_stride;
+    const int32_t* slots;
+    const int32_t* positions;   // rotary positions, one a token; null: none
+    const uint64_t* turns;      // [rotary_dim / 2]
+    float gain;
+    int rotary_dim, interleaved;
+    char *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    int64_t page_stride;        // bytes
+    int tokens, q_heads, heads, dim, page_size, num_pages;
+    int in_dtype, kv_dtype;
+    int32_t* err;
+};
+cudaError_t place_launch(const PlaceArgs& a, cudaStream_t s);
+
+// Tokens of a cache to k and v, which are written there.
+cudaError_t read_launch(const PlaceArgs& a, cudaStream_t s);
+
+inline int64_t kv_row_bytes(int kv_dtype, int64_t dim) {      // of a token and head
+    return kv_dtype == RSSM_F32 ? 4 * dim : kv_dtype == RSSM_BF16 ? 2 * dim : kv_dtype == RSSM_KV_FP8 ? dim : dim / 16 * 9;
+}
 
 }  // namespace rssm

@@ -55,7 +55,7 @@
 namespace rssm {
 namespace attn {
 
-enum { kF32 = 0, kBF16 = 1, kFP8 = 2 };
+enum { kF32 = 0, kBF16 = 1, kFP8 = 2, kNVFP4 = 3 };   // kNVFP4: attn_nvfp4.cuh
 
 template <int KV, int D_, int WM_>
 struct Shape {
@@ -65,6 +65,7 @@ struct Shape {
     // SM: nine warps put three on one of them and leave 168 a thread, which
     // heads of 256 do not fit (128 of them are the outputs); up to eight leave 255.
     static constexpr int NT = D == 256 ? (WM == 1 ? 4 : WM == 2 ? 3 : 1) : WM == 4 ? 2 : 4;
+    static constexpr int kWarpRows = 16;                 // rows that one warp takes
     static constexpr int kRows = 16 * WM;
     static constexpr int kConsumers = WM * NT;
     static constexpr int kThreads = (kConsumers + 1) * 32;
@@ -75,6 +76,7 @@ struct Shape {
     static constexpr int CH = RB / CB;
     static constexpr int kHalf = kAttnGroup * RB;        // K (or V) of a slot
     static constexpr int kSlot = 2 * kHalf;
+    static constexpr int kCopied = 2 * kHalf;            // bytes that the copies of a slot bring
     static constexpr int QS = D * kQsz + 16;             // bytes from one query row to the next
     static constexpr int OS = D + 8;                     // floats from one merged row to the next
     // Two blocks per SM where the registers allow it: one block's joins then
@@ -164,10 +166,10 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int row, int head, int page, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int row, int group, int head, int page, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4,%5,%6}], [%7];"
-        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(0), "r"(head), "r"(page), "r"(smem_u32(bar)) : "memory");
+        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(group), "r"(head), "r"(page), "r"(smem_u32(bar)) : "memory");
 }
 
 // 2^n for n in [-126, 127].
@@ -389,12 +391,24 @@ struct Warp {
     static constexpr int kQRegs = KV == kF32 ? 1 : D / 16;
     static constexpr int kTiles = D / 8;
     static constexpr float kUp = KV == kFP8 ? 15.f : 0.f;   // weights, and l and o with them, are 2^kUp times as large
+    static constexpr int kLaneRows = 2;
     float o[kTiles][4];
     float m[2], l[2];            // rows lane/4 and lane/4 + 8; l is this lane's columns only
     uint32_t qf[kQRegs][4];
     const float* qs;             // FP32: the query rows in shared memory
     float mul[2];                // score multiplier of the two rows
     int lane, g, c;
+
+    // The warp's row that the lane's x-th one is.
+    __device__ __forceinline__ int row(int x) const { return g + 8 * x; }
+    // The lanes of a row's columns: their sums joined, and the one that speaks for them.
+    __device__ __forceinline__ void join_columns(int x) {
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    }
+    __device__ __forceinline__ bool speaks() const { return c == 0; }
+    // The maximum under which row x's sums stand.
+    __device__ __forceinline__ float top(int x) const { return m[x]; }
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -828,10 +842,11 @@ struct Warp {
         }
     }
 
-    // The outputs times f[row] to rows g and g + 8 of a buffer (`to`: row g), or
+    // The outputs times f[row] to rows g and g + 8 of a buffer (`to`: row 0), or
     // added to what is there.
     template <bool kAdd>
     __device__ __forceinline__ void leave(float* to, const float (&f)[2]) const {
+        to += g * S::OS;
 #pragma unroll
         for (int i = 0; i < kTiles; i += 2)
 #pragma unroll
@@ -856,14 +871,14 @@ struct Warp {
 };
 
 // Outputs of row r of a part, columns col..col + 3, from the sums v under maximum
-// M and total L; vs: FP8, the scale of the head's values.
+// M and total L; vs: FP8 and NVFP4, the scale of the head's values.
 template <int KV, class S>
 __device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, int col, float4 v, float M, float L, float vs) {
     const int t = (part.row0 + r) / a.group, j = (part.row0 + r) % a.group;
     const int64_t at = (static_cast<int64_t>(part.b) * a.T + t) * a.q_heads + part.head * a.group + j;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-    if (KV == kFP8) {
+    if (KV == kFP8 || KV == kNVFP4) {
         v.x *= vs; v.y *= vs; v.z *= vs; v.w *= vs;
     }
     if (KV == kF32) {
@@ -887,7 +902,7 @@ __device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, floa
     constexpr int D = S::D, kThreads = S::kConsumers * 32;
     static_assert((kAttnMaxGrid + kJoin - 1) / kJoin <= 32 && 32 <= S::OS, "a round of parts must fit a warp and the buffer");
     const int np = part.others + 1;
-    const float vs = KV == kFP8 ? __ldcg(a.v_scale + part.head) : 1.f;
+    const float vs = KV == kFP8 || KV == kNVFP4 ? __ldcg(a.v_scale + part.head) : 1.f;
     // this block's kJoin neighbours, and then one part for each such round; or all at once
     int p0 = 0, step = 1, n = np;
     bool final = np <= kJoin;
@@ -1106,9 +1121,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
                         const int s = pos + lane - (wrap ? NS : 0), tn = turn + (wrap ? 1 : 0);
                         if ((tn == 0 || wait_phase(empty + s, (tn - 1) & 1, dead, a.err)) && !*dead) {
                             const uint32_t dst = smem_u32(slots + s * S::kSlot);
-                            mbar_arrive_expect_tx(full + s, S::kSlot);
-                            tma_load_5d(dst, &kmap, rw, d.head, pg, full + s);
-                            tma_load_5d(dst + S::kHalf, &vmap, rw, d.head, pg, full + s);
+                            const int tok = KV == kNVFP4 ? 0 : rw, grp = KV == kNVFP4 ? rw / kAttnGroup : 0;
+                            mbar_arrive_expect_tx(full + s, S::kCopied);
+                            tma_load_5d(dst, &kmap, tok, grp, d.head, pg, full + s);
+                            tma_load_5d(dst + S::kHalf, &vmap, tok, grp, d.head, pg, full + s);
                         }
                     }
                     __syncwarp();
@@ -1141,6 +1157,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     // ---- consumers ----
     constexpr int kThreads = S::kConsumers * 32;
     const int wm = warp / S::NT, wt = warp % S::NT;
+    constexpr int kLaneRows = Warp<KV, S>::kLaneRows;
     Warp<KV, S> wp;
     wp.lane = lane;
     wp.g = lane >> 2;
@@ -1171,11 +1188,11 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         if (left.pair >= 0 && tid == 0) count_left();
         const int head = part.head, row0 = part.row0, len = part.len;
         const int rows = min(S::kRows, rows_all - row0);
-        // what the warp's two rows see: [see_lo, see_hi]
-        int draft[2], see_lo[2], see_hi[2];
+        // what the lane's rows see: [see_lo, see_hi]
+        int draft[kLaneRows], see_lo[kLaneRows], see_hi[kLaneRows];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = min(row0 + wm * 16 + wp.g + 8 * x, rows_all - 1);
+        for (int x = 0; x < kLaneRows; ++x) {
+            const int r = min(row0 + wm * S::kWarpRows + wp.row(x), rows_all - 1);
             draft[x] = r / a.group;
             see_hi[x] = len - a.T + draft[x];
             see_lo[x] = window_start(see_hi[x], a.window);
@@ -1184,7 +1201,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         const int all_lo = window_start(len - 1, a.window);         // and the first
         const int some_lo = window_start(len - a.T, a.window);
         wp.reset();
-        wp.load_q(qbuf + (pq * S::kRows + wm * 16) * S::QS, a.scale_log2, KV == kFP8 ? __ldcg(a.k_scale + head) : 1.f);
+        wp.load_q(qbuf + (pq * S::kRows + wm * S::kWarpRows) * S::QS, a.scale_log2,
+                  KV == kFP8 || KV == kNVFP4 ? __ldcg(a.k_scale + head) : 1.f);
         if (KV != kF32) {
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty + pq);
@@ -1227,7 +1245,9 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
                 }
             } else if (ok) {
                 const int tok = (g0 + k) * kAttnGroup;
-                const int lo[2] = {see_lo[0] - tok, see_lo[1] - tok}, hi[2] = {see_hi[0] - tok, see_hi[1] - tok};
+                int lo[kLaneRows], hi[kLaneRows];
+#pragma unroll
+                for (int x = 0; x < kLaneRows; ++x) lo[x] = see_lo[x] - tok, hi[x] = see_hi[x] - tok;
                 wp.step_masked(kb, vb, lo, hi, some_lo - tok, len - 1 - tok, all_lo - tok, all_hi - tok, a.T, tok, len, a.window, draft);
             }
             __syncwarp();
@@ -1242,34 +1262,33 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             if (lane == 0) mbar_arrive(qempty + pq);
         }
         ++parts;
-        const float vs = KV == kFP8 ? __ldcg(a.v_scale + head) : 1.f;   // there once the warps are joined
+        const float vs = KV == kFP8 || KV == kNVFP4 ? __ldcg(a.v_scale + head) : 1.f;   // there once the warps are joined
 
         // ---- join the warps of each row ----
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            wp.l[x] += __shfl_xor_sync(0xffffffffu, wp.l[x], 1);
-            wp.l[x] += __shfl_xor_sync(0xffffffffu, wp.l[x], 2);
-            if (wp.c == 0) s_ml[wt * S::kRows + wm * 16 + wp.g + 8 * x] = make_float2(wp.m[x], wp.l[x]);
+        for (int x = 0; x < kLaneRows; ++x) {
+            wp.join_columns(x);
+            if (wp.speaks()) s_ml[wt * S::kRows + wm * S::kWarpRows + wp.row(x)] = make_float2(wp.top(x), wp.l[x]);
         }
         named_sync(1, kThreads);
-        float f[2];
+        float f[kLaneRows];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = wm * 16 + wp.g + 8 * x;
+        for (int x = 0; x < kLaneRows; ++x) {
+            const int r = wm * S::kWarpRows + wp.row(x);
             float M = -INFINITY, L = 0.f;
 #pragma unroll
             for (int w = 0; w < S::NT; ++w) M = fmaxf(M, s_ml[w * S::kRows + r].x);
             const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int w = 0; w < S::NT; ++w) L += s_ml[w * S::kRows + r].y * ex2(s_ml[w * S::kRows + r].x - ref);
-            f[x] = ex2(wp.m[x] - ref);
-            if (wt == 0 && wp.c == 0) s_row[r] = make_float2(M, L);
+            f[x] = ex2(wp.top(x) - ref);
+            if (wt == 0 && wp.speaks()) s_row[r] = make_float2(M, L);
         }
         // warp w into buffer w % NB, those of later rounds adding to it
 #pragma unroll 1
         for (int w = 0; w < S::NT; w += S::NB) {
             if (wt >= w && wt < w + S::NB) {
-                float* to = merged + ((wt - w) * S::kRows + wm * 16 + wp.g) * S::OS;
+                float* to = merged + ((wt - w) * S::kRows + wm * S::kWarpRows) * S::OS;
                 if (w == 0) wp.template leave<false>(to, f);
                 else wp.template leave<true>(to, f);
             }

@@ -1,6 +1,7 @@
 """The attention side of a hybrid decode step on torch CUDA tensors: the page
-table of a batch (``PageTable``), an attention layer over a paged cache
-(``Attention``), and the norms around a block (``add_norm``, ``gated_norm``).
+table of a batch (``PageTable``), rotary positions (``Rope``, ``rotary``), an
+attention layer over a paged cache (``Attention``), and the norms around a block
+(``add_norm``, ``gated_norm``).
 
 Each call checks its tensors' type, device (the current one), shape and strides,
 and then makes one call of the C ABI (include/rssm.h) on the given stream, or torch's
@@ -226,12 +227,86 @@ def _tokens(t, n, heads, dim, dtype, device, name):
     return heads * dim if step is None else step
 
 
+class Rope:
+    """Rotary positions of a model (rssm_rope_*): the frequencies of the pairs of a
+    head's first `rotary_dim` channels, on the device.
+
+    interleaved: pairs are channels 2i and 2i + 1; else i and i + rotary_dim / 2.
+    scaling: "none", "linear", "ntk", "yarn" or "wavelength" (include/rssm.h gives the
+    formulas), with `factor`, and for the last two `original`, the positions that the
+    model was trained on, and optionally fast and slow. gain: the factor on the
+    rotated channels; None: the scaling's own. inv_freq: the frequencies
+    themselves, radians a position, in the place of base and scaling.
+    """
+
+    def __init__(self, rotary_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=0, fast=0.0, slow=0.0,
+                 gain=None, inv_freq=None, device="cuda"):
+        torch = _torch()
+        _need(scaling in _r.ROPE, f"scaling: {scaling!r}, must be one of {sorted(_r.ROPE)}")
+        _need(2 <= rotary_dim <= 1024 and rotary_dim % 2 == 0, f"rotary_dim: {rotary_dim}, must be even, 2 to 1024")
+        _need(gain is None or (gain == gain and abs(gain) < 3e38), f"gain: {gain}, must be finite")
+        own = 1.0
+        if inv_freq is None:
+            inv_freq, own = _r.rssm_rope_frequencies(_r.RopeConfig(rotary_dim, _r.ROPE[scaling], base, factor, original,
+                                                                   fast, slow, 0.0))
+        else:
+            _need(scaling == "none", "inv_freq: given, so scaling must be none")
+            inv_freq = [float(w) for w in inv_freq]
+            _need(len(inv_freq) == rotary_dim // 2, f"inv_freq: {len(inv_freq)} frequencies, must be {rotary_dim // 2}")
+        self.rotary_dim, self.interleaved, self.frequencies = rotary_dim, bool(interleaved), inv_freq
+        self.gain = own if gain is None else float(gain)
+        turns = [t - (1 << 64) if t >> 63 else t for t in _r.rssm_rope_turns(inv_freq)]
+        self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
+        _cuda(self.turns.device, "device")
+
+
+_rotary_seen: dict = {}
+
+
+def rotary(out, x, positions, rope, stream=None):
+    """Rotary positions (rssm_rotary): x [tokens][heads][dim] with the first
+    rope.rotary_dim channels of every head turned by their token's position (int32
+    [tokens]), to out, alike in shape and type. float32 or bfloat16; x and out may
+    be slices of a wider projection, and out may be x."""
+    key = (_sig(out), _sig(x), _sig(positions), rope.rotary_dim, rope.interleaved, rope.gain, rope.turns.get_device())
+    cfg = _rotary_seen.get(key)
+    if cfg is None:
+        cfg = _keep(_rotary_seen, key, _check_rotary(out, x, positions, rope))
+    st = _lib.rssm_rotary(cfg, x.data_ptr(), positions.data_ptr(), rope.turns.data_ptr(), out.data_ptr(),
+                          _stream_of(stream, x.get_device()))
+    if st:
+        _r._check("rssm_rotary", st)
+
+
+def _check_rotary(out, x, positions, rope):
+    """The configuration struct of rotary, by reference."""
+    _bind()
+    dev = x.device
+    _cuda(dev, "x")
+    d = _dtype(x, "x")
+    _need(x.dim() >= 3, f"x: shape {tuple(x.shape)}, must be [tokens][heads][dim]")
+    heads, dim = x.shape[-2:]
+    _need(heads > 0 and dim > 0, f"x: shape {tuple(x.shape)}, must be [tokens][heads][dim]")
+    n = x.numel() // (heads * dim)
+    _need(rope.rotary_dim <= dim, f"rope: {rope.rotary_dim} rotated channels, x has {dim}")
+    _on(rope.turns, dev, "rope")
+    _ints(positions, n, dev, "positions")
+    _need(out.shape == x.shape, f"out: shape {tuple(out.shape)}, must be {tuple(x.shape)}")
+    return _by_ref(_r.RotaryConfig(tokens=n, heads=heads, dim=dim, rotary_dim=rope.rotary_dim,
+                                   interleaved=int(rope.interleaved), dtype=d, gain=rope.gain,
+                                   x_stride=_tokens(x, n, heads, dim, x.dtype, dev, "x"),
+                                   out_stride=_tokens(out, n, heads, dim, x.dtype, dev, "out")))
+
+
 class Attention:
     """One attention layer over paged caches [num_pages][kv_heads][page_size][head_dim]
     (rssm_attn_*): float32 caches with float32 inputs, bfloat16 or
     float8_e4m3fn ones with bfloat16 inputs; float8 caches need k_scale and
-    v_scale (float32 [kv_heads]). The caches may be slices of one tensor along
-    a page ([num_pages][2][kv_heads]...).
+    v_scale (float32 [kv_heads]). uint8 caches [num_pages][kv_heads][page_size]
+    [head_dim // 2 + head_dim // 16] hold NVFP4, four bits an element and a scale per
+    16, in an order of the library's own (append writes them, read gives their
+    values back); they need k_scale and v_scale too. The caches may be slices of one
+    tensor along a page ([num_pages][2][kv_heads]...).
 
     workspace: a uint8 tensor that layers on one stream share; None allocates
     one (`workspace_size` gives the bytes).
@@ -242,24 +317,28 @@ class Attention:
         torch = _torch()
         self.handle = 0
         kinds = {torch.float32: (_r.RSSM_F32, "f32"), torch.bfloat16: (_r.RSSM_BF16, "bf16"),
-                 torch.float8_e4m3fn: (_r.RSSM_KV_FP8, "bf16")}
+                 torch.float8_e4m3fn: (_r.RSSM_KV_FP8, "bf16"), torch.uint8: (_r.RSSM_KV_NVFP4, "bf16")}
         _need(k_cache.dtype in kinds, f"k_cache: dtype {k_cache.dtype}")
         kv, io = kinds[k_cache.dtype]
         io = in_dtype or io
         _need(io in _r.DTYPE, f"in_dtype: {io}")
         _need(k_cache.dim() == 4, "k_cache: must be [num_pages][kv_heads][page_size][head_dim]")
-        pages, heads, ps, dim = k_cache.shape
+        pages, heads, ps, row = k_cache.shape
+        dim = row
+        if kv == _r.RSSM_KV_NVFP4:
+            _need(row % 9 == 0, f"k_cache: rows of {row} bytes, must be head_dim // 2 + head_dim // 16")
+            dim = row // 9 * 16
         self.device = k_cache.device
         _cuda(self.device, "k_cache")
         for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
             _on(c, self.device, name)
             _need(c.dtype == k_cache.dtype and c.shape == k_cache.shape, f"{name}: k_cache and v_cache must be alike")
-            _need(c.stride()[1:] == (ps * dim, dim, 1), f"{name}: a page must be dense")
+            _need(c.stride()[1:] == (ps * row, row, 1), f"{name}: a page must be dense")
         _need(k_cache.stride(0) == v_cache.stride(0) or pages == 1, "k_cache and v_cache: page strides differ")
-        _need(k_cache.stride(0) >= heads * ps * dim or pages == 1, "k_cache and v_cache: pages overlap")
-        fp8 = kv == _r.RSSM_KV_FP8
+        _need(k_cache.stride(0) >= heads * ps * row or pages == 1, "k_cache and v_cache: pages overlap")
+        scaled = kv in (_r.RSSM_KV_FP8, _r.RSSM_KV_NVFP4)
         for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _need((s is not None) == fp8, f"{name}: given for float8 caches, and only for them")
+            _need((s is not None) == scaled, f"{name}: given for float8 and 4-bit caches, and only for them")
             if s is not None:
                 _on(s, self.device, name)
                 _need(s.dtype == torch.float32 and s.numel() == heads and s.is_contiguous(), f"{name}: must be {heads} dense float32")
@@ -292,20 +371,70 @@ class Attention:
         except Exception:
             pass
 
-    def append(self, k, v, slots, stream=None):
+    def append(self, k, v, slots, rope=None, positions=None, q=None, q_out=None, stream=None):
         """Write the new tokens' keys and values ([tokens][kv_heads][head_dim],
-        slices of a wider projection too) to their slots."""
-        key = (_sig(k), _sig(v), _sig(slots))
+        slices of a wider projection too) to their slots.
+
+        rope (a Rope, with positions int32 [tokens]): the keys are rotated on the way,
+        and so are, where given, the tokens' queries q ([tokens][q_heads][head_dim])
+        into q_out, which may be q; k is not changed."""
+        if rope is not None:
+            self._append_rotary(k, v, slots, rope, positions, q, q_out, stream)
+            return
+        key = (_sig(k), _sig(v), _sig(slots), positions is None, q is None, q_out is None)
         seen = self._seen.get(key)
         if seen is None:
-            c, n = self.cfg, slots.numel()
-            _ints(slots, n, self.device, "slots")
-            seen = _keep(self._seen, key, (n, _tokens(k, n, c.kv_heads, c.head_dim, self.dtype, self.device, "k"),
-                                           _tokens(v, n, c.kv_heads, c.head_dim, self.dtype, self.device, "v")))
+            _need(positions is None and q is None and q_out is None, "positions, q and q_out: go with rope")
+            seen = _keep(self._seen, key, self._check_tokens(k, v, slots))
         st = self._fn.rssm_attn_append(self.handle, seen[0], k.data_ptr(), seen[1], v.data_ptr(), seen[2],
                                        slots.data_ptr(), _stream_of(stream, self.device.index))
         if st:
             _r._check("rssm_attn_append", st)
+
+    def _check_tokens(self, k, v, slots):
+        """Tokens, and the elements between them in k and in v."""
+        c, n = self.cfg, slots.numel()
+        _ints(slots, n, self.device, "slots")
+        return (n, _tokens(k, n, c.kv_heads, c.head_dim, self.dtype, self.device, "k"),
+                _tokens(v, n, c.kv_heads, c.head_dim, self.dtype, self.device, "v"))
+
+    def _append_rotary(self, k, v, slots, rope, positions, q, q_out, stream):
+        key = (_sig(k), _sig(v), _sig(slots), _sig(positions), _sig(q), _sig(q_out), rope.rotary_dim, rope.interleaved, rope.gain,
+               rope.turns.get_device())
+        seen = self._seen.get(key)
+        if seen is None:
+            c = self.cfg
+            n, ks, vs = self._check_tokens(k, v, slots)
+            _need(positions is not None, "positions: must be given with rope")
+            _ints(positions, n, self.device, "positions")
+            _on(rope.turns, self.device, "rope")
+            _need(rope.rotary_dim <= c.head_dim, f"rope: {rope.rotary_dim} rotated channels, heads have {c.head_dim}")
+            _need((q is None) == (q_out is None), "q and q_out: go together")
+            qs = qo = 0
+            if q is not None:
+                qs = _tokens(q, n, c.q_heads, c.head_dim, self.dtype, self.device, "q")
+                qo = _tokens(q_out, n, c.q_heads, c.head_dim, self.dtype, self.device, "q_out")
+            seen = _keep(self._seen, key, (n, ks, vs, qs, qo))
+        n, ks, vs, qs, qo = seen
+        r = _r.AttnRotary(rope.rotary_dim, rope.interleaved, rope.gain, rope.turns.data_ptr(), positions.data_ptr(),
+                          None if q is None else q.data_ptr(), None if q is None else q_out.data_ptr(), qs, qo)
+        st = self._fn.rssm_attn_append_rotary(self.handle, n, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), _by_ref(r),
+                                              _stream_of(stream, self.device.index))
+        if st:
+            _r._check("rssm_attn_append_rotary", st)
+
+    def read(self, k, v, slots, stream=None):
+        """The keys and values that the cache holds in the given slots, to k and v
+        ([tokens][kv_heads][head_dim]); the rows of a negative slot are left as
+        they are."""
+        key = (_sig(k), _sig(v), _sig(slots), "read")
+        seen = self._seen.get(key)
+        if seen is None:
+            seen = _keep(self._seen, key, self._check_tokens(k, v, slots))
+        st = self._fn.rssm_attn_read(self.handle, seen[0], slots.data_ptr(), k.data_ptr(), seen[1], v.data_ptr(), seen[2],
+                                     _stream_of(stream, self.device.index))
+        if st:
+            _r._check("rssm_attn_read", st)
 
     def decode(self, out, q, lens, table, T=1, lse=None, stream=None):
         """The attention of T new tokens a request: q and out

@@ -604,8 +604,18 @@ rssm_status rssm_pages_destroy(rssm_pages* h);
  * A token that sees nothing (p < 0), or only scores of -inf, has out = 0 and
  * lse = -inf. Nothing that a token does not see reaches its output, NaN and
  * infinities included; an infinite value that it does see makes its output NaN or
- * infinite (over FP32 caches values from (1 - 2^-12) 2^128 on count as infinite). */
-enum { RSSM_KV_FP8 = 4 };   /* kv_dtype: E4M3 codes, one FP32 scale per cache head for K and for V */
+ * infinite (over FP32 caches values from (1 - 2^-12) 2^128 on count as infinite).
+ * Scores are FP32: one beyond its range is infinite, and one of +inf makes the
+ * output NaN. */
+enum {
+    RSSM_KV_FP8 = 4,    /* kv_dtype: E4M3 codes, one FP32 scale per cache head for K and for V */
+    RSSM_KV_NVFP4 = 5   /* kv_dtype: E2M1 codes in blocks of 16 channels, an E4M3 scale a block and
+                           one FP32 scale per cache head for K and for V. A cache is then
+                           uint8 [num_pages][kv_heads][page_size][9*head_dim/16]; 16 tokens of
+                           a page and head (tokens 0-15, 16-31, ...) are 9*head_dim bytes in an
+                           order of the library's own: rssm_attn_append writes them and
+                           rssm_attn_read gives their values. */
+};
 
 typedef struct {
     int32_t batch;
@@ -617,12 +627,13 @@ typedef struct {
     int32_t max_pages;  /* entries in a row of the page table                         */
     int32_t max_draft;  /* most new tokens per request and call, 1..8                 */
     int32_t in_dtype;   /* RSSM_F32 or RSSM_BF16: q, k, v, out                        */
-    int32_t kv_dtype;   /* RSSM_F32 (F32 inputs), RSSM_BF16 or RSSM_KV_FP8 (BF16 inputs) */
+    int32_t kv_dtype;   /* RSSM_F32 (F32 inputs), RSSM_BF16, RSSM_KV_FP8 or RSSM_KV_NVFP4 (BF16 inputs) */
     int32_t window;     /* 0: none                                                    */
     float scale;        /* 0: 1/sqrt(head_dim)                                        */
-    int64_t page_stride; /* elements from one page to the next, in both caches; 0:
-                            dense (kv_heads*page_size*head_dim). A multiple of 16
-                            bytes, so that K and V may lie in one array, page by page */
+    int64_t page_stride; /* elements (RSSM_KV_NVFP4: bytes) from one page to the next, in
+                            both caches; 0: dense (kv_heads*page_size*head_dim, or its
+                            9/16). A multiple of 16 bytes, so that K and V may lie in one
+                            array, page by page */
 } rssm_attn_config;
 
 typedef struct rssm_attn rssm_attn;
@@ -634,8 +645,9 @@ rssm_status rssm_attn_workspace_size(const rssm_attn_config* cfg, size_t* bytes)
 
 /* One attention layer on the caller's caches and workspace.
  *   d_k_cache, d_v_cache  16-byte aligned; must outlive the handle.
- *   d_k_scale, d_v_scale  RSSM_KV_FP8: FP32 [kv_heads], finite and > 0; the cache
- *                         stands for code*scale. NULL otherwise. Must outlive the handle.
+ *   d_k_scale, d_v_scale  RSSM_KV_FP8 and RSSM_KV_NVFP4: FP32 [kv_heads], finite and > 0;
+ *                         the cache stands for code*scale, or code*block scale*scale. NULL
+ *                         otherwise. Must outlive the handle.
  *   d_workspace           256-byte aligned. The layers of one stream may share one
  *                         workspace as large as the largest asks for, whatever their
  *                         configurations. Its error word and counters are zeroed
@@ -650,10 +662,46 @@ rssm_status rssm_attn_create(const rssm_attn_config* cfg, void* d_k_cache, void*
  *              k_stride / v_stride elements apart (0: dense).
  *   d_slots    int32 [tokens] as rssm_pages_extend gives them; a negative one is
  *              skipped, one past the cache is skipped and reported.
- * RSSM_KV_FP8 stores E4M3(x / scale), to nearest even, at most +-448.
- * Errors: INVALID_ARG (null, tokens < 0, a stride below the row), CUDA. */
+ * RSSM_KV_FP8 stores E4M3(x / scale), to nearest even, at most +-448. RSSM_KV_NVFP4
+ * stores, with m the largest magnitude of a token's 16 channels of a block, the block
+ * scale b = E4M3(m * (1 / (6 scale))), at most 448, and the codes E2M1(x * (1 / (b scale))),
+ * at most +-6, to nearest even, in FP32 (b = 0: zeros). A NaN makes b NaN, and so the 16
+ * values; an infinity is held as the largest value.
+ * A slot twice in one call: one of its tokens stays, which is not said (NVFP4: each
+ * block of 16 channels may be another's).
+ * Errors: INVALID_ARG (null, tokens < 0, a stride below the row), UNSUPPORTED (NVFP4
+ * rows of more than 2^24 elements), CUDA. */
 rssm_status rssm_attn_append(rssm_attn* h, int32_t tokens, const void* d_k, int64_t k_stride, const void* d_v,
                              int64_t v_stride, const int32_t* d_slots, void* stream);
+
+/* Rotary positions on the way to the cache (rssm_attn_append_rotary). */
+typedef struct {
+    int32_t rotary_dim;         /* the first channels of a head, even, 2..head_dim        */
+    int32_t interleaved;        /* pairs: 0 channels i and i + rotary_dim/2, 1 2i and 2i + 1 */
+    float gain;                 /* on the rotated channels, finite                        */
+    const uint64_t* d_turns;    /* [rotary_dim/2], rssm_rope_turns                        */
+    const int32_t* d_positions; /* [tokens]                                               */
+    const void* d_q;            /* NULL, or in_dtype [tokens][q_heads][head_dim] to rotate */
+    void* d_q_out;              /* NULL with d_q; may be d_q, with the same stride        */
+    int64_t q_stride, q_out_stride; /* elements between tokens; 0: dense                  */
+} rssm_attn_rotary;
+
+/* rssm_attn_append of keys that are rotated on the way, in FP32 and before the one
+ * rounding to the cache's type, and beside it d_q to d_q_out (rssm_rotary). d_k is not
+ * changed; a token that has no slot is rotated into d_q_out all the same.
+ * Errors: INVALID_ARG (as rssm_attn_append; null, sizes, strides), UNSUPPORTED
+ * (q_heads*head_dim > 2^24), CUDA. */
+rssm_status rssm_attn_append_rotary(rssm_attn* h, int32_t tokens, const void* d_k, int64_t k_stride, const void* d_v,
+                                    int64_t v_stride, const int32_t* d_slots, const rssm_attn_rotary* rotary, void* stream);
+
+/* The keys and values that the cache holds in the given slots, the reverse of
+ * rssm_attn_append: d_k and d_v get in_dtype [tokens][kv_heads][head_dim], each value
+ * rounded once. The rows of a negative slot are left as they are, and those of one past
+ * the cache too, which is reported.
+ * Errors: INVALID_ARG (null, tokens < 0, a stride below the row), UNSUPPORTED
+ * (kv_heads*head_dim > 2^24), CUDA. */
+rssm_status rssm_attn_read(rssm_attn* h, int32_t tokens, const int32_t* d_slots, void* d_k, int64_t k_stride, void* d_v,
+                           int64_t v_stride, void* stream);
 
 /* The attention of T new tokens a request.
  *   d_q      in_dtype [batch][T][q_heads][head_dim], consecutive tokens q_stride
@@ -677,6 +725,58 @@ rssm_status rssm_attn_get_error(rssm_attn* h, int32_t* err4, void* stream);
 
 /* Free the host handle; caches and workspace stay the caller's. */
 rssm_status rssm_attn_destroy(rssm_attn* h);
+
+/* ---- rotary positions -------------------------------------------------------
+ * Pair i of a head's first rotary_dim channels, (u, v), at position p:
+ *   (u, v) -> gain * (u cos(p w_i) - v sin(p w_i), v cos(p w_i) + u sin(p w_i))
+ * with w_i = base^(-2 i / rotary_dim), or scaled for contexts longer than the `original`
+ * positions that a model was trained on:
+ *   LINEAR      w_i / factor
+ *   NTK         base * factor^(rotary_dim / (rotary_dim - 2)) in the place of base
+ *   YARN        r w_i / factor + (1 - r) w_i with the ramp r = clamp((i - lo)/(hi - lo), 0, 1)
+ *               between the channels that turn `fast` (32) and `slow` (1) times over
+ *               the original positions, c(n) = rotary_dim ln(original/(2 pi n)) / (2 ln base),
+ *               lo = max(floor(c(fast)), 0), hi = min(ceil(c(slow)), rotary_dim - 1);
+ *               gain = 0.1 ln(factor) + 1
+ *   WAVELENGTH  s w_i + (1 - s) w_i / factor with s = clamp((n - slow)/(fast - slow), 0, 1),
+ *               n = original w_i / (2 pi) the channel's turns, fast 4 and slow 1
+ * The angle is exact for every 32-bit position (negative ones turn back): frequencies
+ * enter as 64-bit fractions of a turn. */
+enum { RSSM_ROPE_PLAIN = 0, RSSM_ROPE_LINEAR = 1, RSSM_ROPE_NTK = 2, RSSM_ROPE_YARN = 3, RSSM_ROPE_WAVELENGTH = 4 };
+
+typedef struct {
+    int32_t rotary_dim;   /* even, 2..1024                                      */
+    int32_t scaling;      /* RSSM_ROPE_*                                        */
+    double base;          /* > 1                                                */
+    double factor;        /* > 0, scaled ones only                              */
+    double original;      /* >= 1, YARN and WAVELENGTH only                     */
+    double fast, slow;    /* fast > slow > 0; 0: the values above               */
+    double gain;          /* 0: as above, 1 where nothing is said               */
+} rssm_rope_config;
+
+/* w_i to freq [rotary_dim/2], and the gain. Host only. Errors: INVALID_ARG. */
+rssm_status rssm_rope_frequencies(const rssm_rope_config* cfg, double* freq, float* gain);
+
+/* n frequencies (radians a position, finite) as 2^-64 turns a position, modulo a whole
+ * turn: what d_turns holds on the device. Host only. Errors: INVALID_ARG. */
+rssm_status rssm_rope_turns(int32_t n, const double* freq, uint64_t* turns);
+
+typedef struct {
+    int64_t tokens;
+    int32_t heads, dim;         /* of x; heads*dim <= 2^24                         */
+    int32_t rotary_dim;         /* even, 2..min(dim, 1024)                         */
+    int32_t interleaved;        /* as in rssm_attn_rotary                          */
+    int32_t dtype;              /* RSSM_F32 or RSSM_BF16                           */
+    float gain;
+    int64_t x_stride, out_stride; /* elements between tokens; 0: dense             */
+} rssm_rotary_config;
+
+/* x [tokens][heads][dim] with the first rotary_dim channels of every head rotated, in
+ * FP32 and rounded once, and the others as they are, to out. d_out may be d_x, with the
+ * same stride. d_positions: int32 [tokens]; d_turns: [rotary_dim/2].
+ * Errors: INVALID_ARG, UNSUPPORTED (rotary_dim), CUDA. tokens = 0 is RSSM_OK. */
+rssm_status rssm_rotary(const rssm_rotary_config* cfg, const void* d_x, const int32_t* d_positions, const uint64_t* d_turns,
+                        void* d_out, void* stream);
 
 /* ---- norms around a block --------------------------------------------------
  * All sums in FP32; each output is rounded once. Weights are FP32 and enter as
