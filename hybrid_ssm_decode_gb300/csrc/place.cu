@@ -40,66 +40,182 @@ __device__ __forceinline__ float2 turn_of(int32_t p, uint64_t turn) {
     return (k & 2) ? make_float2(-x, -y) : make_float2(x, y);
 }
 
-// The sines of `n` tokens from `first` on, [n][half].
+enum { kNone = 0, kHalves = 1, kInterleaved = 2 };      // how a head's pairs lie
+
+// The sines of `n` tokens from `first` on. Those of pair i lie at (i % step) * (half / step)
+// + i / step of their token, so that threads that take `step` pairs each read side by side.
 __device__ __forceinline__ void make_turns(float2* cs, const int32_t* positions, const uint64_t* turns, int64_t first, int n,
-                                           int half, float gain) {
+                                           int half, int step, float gain) {
+    const int rows = half / step;
     for (int i = threadIdx.x; i < n * half; i += kThreads) {
-        const int t = i / half;
-        const float2 v = turn_of(positions[first + t], turns[i - t * half]);
-        cs[i] = make_float2(v.x * gain, v.y * gain);
+        const int t = i / half, pair = i - t * half, q = pair / step;
+        const float2 v = turn_of(positions[first + t], turns[pair]);
+        cs[t * half + (pair - q * step) * rows + q] = make_float2(v.x * gain, v.y * gain);
     }
     __syncthreads();
 }
 
-// N consecutive elements, aligned to their size or 16 bytes.
+// N consecutive elements as they are stored (in words, so that BF16 widens by one
+// instruction an element and is rounded two at a time), aligned to their size.
 template <class T, int N>
 struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Pack {
-    T v[N];
+    static constexpr int kWords = N * sizeof(T) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T* p) { *this = *reinterpret_cast<const Pack*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Pack*>(p) = *this; }
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+    }
+    __device__ __forceinline__ void set(const float* x) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[i] = __float_as_uint(x[i]);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    }
+};
+template <>
+struct Pack<__nv_bfloat16, 1> {
+    __nv_bfloat16 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *p; }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *p = v; }
+    __device__ __forceinline__ float at(int) const { return __bfloat162float(v); }
+    __device__ __forceinline__ void set(const float* x) { v = __float2bfloat16_rn(*x); }
 };
 template <class T, int N>
-__device__ __forceinline__ void load_n(float* x, const T* p) {
-    const Pack<T, N> a = *reinterpret_cast<const Pack<T, N>*>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f(a.v[i]);
-}
-template <class T, int N>
 __device__ __forceinline__ void store_n(T* p, const float* x) {
-    Pack<T, N> a;
+    constexpr int kStep = N * sizeof(T) <= 16 ? N : 16 / sizeof(T);
 #pragma unroll
-    for (int i = 0; i < N; ++i) a.v[i] = from_f<T>(x[i]);
-    *reinterpret_cast<Pack<T, N>*>(p) = a;
+    for (int i = 0; i < N; i += kStep) {
+        Pack<T, kStep> a;
+        a.set(x + i);
+        a.store(p + i);
+    }
 }
 
 // u cos - v sin, and with -v in the place of v the other half's v cos + u sin: spelt out,
 // so that every kernel rounds alike.
 __device__ __forceinline__ float turned(float u, float v, float2 t) { return __fmaf_rn(u, t.x, -__fmul_rn(v, t.y)); }
 
-// Pairs of one head, VEC at a time: item e of R/2/VEC, then copies of what is not rotated.
-template <class T, int VEC>
-__device__ __forceinline__ void rotate_item(const T* x, T* out, const float2* cs, int e, int R, bool inter) {
-    const int half = R / 2;
-    const int i = e * VEC;
-    if (i >= half) {
-        const int d = R + (i - half);
-        *reinterpret_cast<Pack<T, VEC>*>(out + d) = *reinterpret_cast<const Pack<T, VEC>*>(x + d);
-        return;
+// The heads of a tile's tokens, rotated. A thread keeps to VEC pairs of one token (or to
+// VEC of the channels beside them, which are copied), so that their sines stay in
+// registers, and goes through the token's heads by twos, the next two's channels under
+// way while it turns these; the first are on their way before the sines are made.
+template <class T, int VEC, int PAIRS>
+struct Rotator {
+    const T* x;                              // the thread's channels of the head under way
+    T* out;                                  // and of the one before
+    const T* x0;
+    T* out0;
+    int64_t x_stride, out_stride;
+    int heads, dim, R, half, per_head;       // per_head: threads of a head
+    int work, groups, per_token, part, parts;   // groups of threads; a token's heads in `parts` parts, per_token of them here
+    static constexpr int kAhead = 2;
+    struct Raw {
+        Pack<T, VEC> a, b;
+    };
+    Raw raw[kAhead];
+    int slot, e, h;
+
+    __device__ __forceinline__ bool pairs() const { return e * VEC < half; }
+    __device__ __forceinline__ int d0() const { return !pairs() ? R - half + e * VEC : PAIRS == kInterleaved ? 2 * e * VEC : e * VEC; }
+    __device__ __forceinline__ int d1() const { return PAIRS == kInterleaved ? VEC : half; }      // from d0
+
+    // x, out: the tile's first token. The block takes part `y` of `ny` of every token's heads.
+    __device__ __forceinline__ void start(const T* x_, T* out_, int64_t xs, int64_t os, int heads_, int dim_, int R_, int tile, int n,
+                                          int y, int ny) {
+        x0 = x_; out0 = out_; x_stride = xs; out_stride = os; heads = heads_; dim = dim_; R = R_; half = R / 2;
+        per_head = (half + (static_cast<const void*>(out_) == x_ ? 0 : dim - R)) / VEC;
+        groups = max(1, kThreads / per_head);                // heads of more threads: one after another
+        per_token = max(1, groups / tile);
+        parts = per_token * ny;
+        part = y * per_token;
+        slot = threadIdx.x / per_head;                       // 0 for heads of more threads than there are
+        e = threadIdx.x - slot * per_head;
+        work = slot < groups ? n * per_token : 0;
+        begin();
     }
-    float a[2 * VEC];
-    const int d0 = inter ? 2 * i : i, d1 = inter ? 2 * i + VEC : half + i;
-    load_n<T, VEC>(a, x + d0);
-    load_n<T, VEC>(a + VEC, x + d1);
+    // The first head of the slot.
+    __device__ __forceinline__ void begin() {
+        h = heads;
+        if (slot >= work) return;
+        const int t = slot / per_token;
+        h = part + slot - t * per_token;
+        x = x0 + t * x_stride + static_cast<int64_t>(h) * dim + d0();
+        out = out0 + t * out_stride + static_cast<int64_t>(h) * dim + d0();
+        fetch();
+    }
+    // The heads from h on, as they are stored.
+    __device__ __forceinline__ void fetch() {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const float2 t = cs[i + j];
-        float& u = inter ? a[2 * j] : a[j];
-        float& v = inter ? a[2 * j + 1] : a[VEC + j];
-        const float y = turned(u, v, t), z = turned(v, -u, t);
-        u = y;
-        v = z;
+        for (int k = 0; k < kAhead; ++k) {
+            if (h + k * parts < heads) {
+                raw[k].a.load(x);
+                if (pairs()) raw[k].b.load(x + d1());
+            }
+            x += parts * static_cast<int64_t>(dim);
+        }
     }
-    store_n<T, VEC>(out + d0, a);
-    store_n<T, VEC>(out + d1, a + VEC);
-}
+    __device__ __forceinline__ void put(const Raw& p, const float2 (&cs)[VEC]) const {
+        if (!pairs()) {
+            p.a.store(out);
+            return;
+        }
+        float r[2 * VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) r[j] = p.a.at(j), r[VEC + j] = p.b.at(j);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            constexpr bool kInter = PAIRS == kInterleaved;
+            const float u = r[kInter ? 2 * j : j], v = r[kInter ? 2 * j + 1 : VEC + j];
+            r[kInter ? 2 * j : j] = turned(u, v, cs[j]);
+            r[kInter ? 2 * j + 1 : VEC + j] = turned(v, -u, cs[j]);
+        }
+        store_n<T, VEC>(out, r);
+        store_n<T, VEC>(out + d1(), r + VEC);
+    }
+    // After the sines are made.
+    __device__ __forceinline__ void run(const float2* cs) {
+        const int rows = half / VEC;
+        for (;;) {
+            if (slot < work) {
+                float2 t[VEC];
+                const int tok = slot / per_token;
+                if (pairs()) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) t[j] = cs[tok * half + j * rows + e];
+                }
+                while (h < heads) {
+                    Raw now[kAhead];
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) now[k] = raw[k];
+                    const int first = h;
+                    h += kAhead * parts;
+                    fetch();
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) {
+                        if (first + k * parts < heads) put(now[k], t);
+                        out += parts * static_cast<int64_t>(dim);
+                    }
+                }
+            }
+            // the next slot; heads of more channels than threads: the next channels first
+            if (per_head > kThreads && (e += kThreads) < per_head) {
+                begin();
+                continue;
+            }
+            e = per_head > kThreads ? static_cast<int>(threadIdx.x) : e;
+            slot += groups;
+            if (slot >= work) return;
+            begin();
+        }
+    }
+};
 
 struct RotaryArgs {
     const void* x;
@@ -111,66 +227,88 @@ struct RotaryArgs {
     float gain;
 };
 
-template <class T, int VEC>
+template <class T, int VEC, int PAIRS>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, int nt) {
     extern __shared__ float2 cs[];
     after_predecessor();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * nt;
-    const int n = static_cast<int>(min(static_cast<int64_t>(nt), a.tokens - first)), half = a.rotary_dim / 2;
-    make_turns(cs, a.positions, a.turns, first, n, half, a.gain);
-    const uint32_t per_head = (half + (a.out == a.x ? 0 : a.dim - a.rotary_dim)) / VEC, per_token = a.heads * per_head;
-    for (uint32_t i = blockIdx.y * kThreads + threadIdx.x; i < n * per_token; i += gridDim.y * kThreads) {
-        const uint32_t t = i / per_token, r = i - t * per_token, h = r / per_head;
-        const T* x = static_cast<const T*>(a.x) + (first + t) * a.x_stride + static_cast<int64_t>(h) * a.dim;
-        T* out = static_cast<T*>(a.out) + (first + t) * a.out_stride + static_cast<int64_t>(h) * a.dim;
-        rotate_item<T, VEC>(x, out, cs + t * half, r - h * per_head, a.rotary_dim, a.interleaved != 0);
-    }
+    const int n = static_cast<int>(min(static_cast<int64_t>(nt), a.tokens - first));
+    Rotator<T, VEC, PAIRS> r;
+    r.start(static_cast<const T*>(a.x) + first * a.x_stride, static_cast<T*>(a.out) + first * a.out_stride, a.x_stride, a.out_stride,
+            a.heads, a.dim, a.rotary_dim, nt, n, blockIdx.y, gridDim.y);
+    make_turns(cs, a.positions, a.turns, first, n, a.rotary_dim / 2, VEC, a.gain);
+    r.run(cs);
 }
 
-// Channels d0..d0 + 15 of a row, rotated.
-template <class T, int VEC, bool ROPE>
-__device__ __forceinline__ void load_block(float (&x)[16], const T* row, int d0, const float2* cs, int R, bool inter) {
+// 16 channels of a key (or, not rotated, of a value): as stored, with the other halves of
+// their pairs, and rotated.
+template <class T, int VEC, int PAIRS>
+struct Key {
+    static constexpr int kSines = PAIRS == kHalves ? 16 : PAIRS == kInterleaved ? 8 : 1;
+    Pack<T, VEC> own[16 / VEC], other[PAIRS == kHalves ? 16 / VEC : 1];
+
+    __device__ __forceinline__ void load(const T* row, int d0, int R) {
 #pragma unroll
-    for (int q = 0; q < 16; q += VEC) load_n<T, VEC>(x + q, row + d0 + q);
-    if (!ROPE) return;
-    const int half = R / 2;
+        for (int q = 0; q < 16 / VEC; ++q) own[q].load(row + d0 + q * VEC);
+        if constexpr (PAIRS == kHalves) {
+            const int half = R / 2;
 #pragma unroll
-    for (int q = 0; q < 16; q += VEC) {
-        const int d = d0 + q;
-        if (d >= R) continue;
-        if (!inter) {
-            // the other halves of the pairs
-            const bool low = d < half;
-            float y[VEC];
-            load_n<T, VEC>(y, row + (low ? d + half : d - half));
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float2 t = cs[(low ? d : d - half) + j];
-                x[q + j] = turned(x[q + j], low ? y[j] : -y[j], t);
+            for (int q = 0; q < 16 / VEC; ++q) {
+                const int d = d0 + q * VEC;
+                if (d < R) other[q].load(row + (d < half ? d + half : d - half));
             }
-        } else if constexpr (VEC > 1) {
-#pragma unroll
-            for (int j = 0; j < VEC; j += 2) {
-                const float2 t = cs[(d + j) / 2];
-                const float u = x[q + j], v = x[q + j + 1];
-                x[q + j] = turned(u, v, t);
-                x[q + j + 1] = turned(v, -u, t);
-            }
-        } else {
-            if (q & 1) continue;                             // d0 is even: q, q + 1 are a pair
-            const float2 t = cs[d / 2];
-            const float u = x[q], v = x[q + 1];
-            x[q] = turned(u, v, t);
-            x[q + 1] = turned(v, -u, t);
         }
     }
-}
-
-__device__ __forceinline__ bool any_nan(const float (&x)[16]) {
-    bool nan = false;
+    // Sines of the 16 channels from their token's, of which a rotator's step is VEC pairs.
+    __device__ __forceinline__ static void sines(float2 (&t)[kSines], const float2* cs, int d0, int R) {
+        const int half = R / 2, rows = half / VEC;
+        if constexpr (PAIRS == kHalves) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) nan = nan || x[i] != x[i];
-    return nan;
+            for (int q = 0; q < 16; q += VEC) {
+                const int d = d0 + q, i = d < half ? d : d - half;       // a multiple of VEC
+                if (d < R) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        t[q + j] = cs[j * rows + i / VEC];
+                        if (d < half) t[q + j].y = -t[q + j].y;          // low halves: u cos - v sin
+                    }
+                }
+            }
+        } else if constexpr (PAIRS == kInterleaved) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = d0 / 2 + j;
+                if (2 * i < R) t[j] = cs[(i % VEC) * rows + i / VEC];
+            }
+        }
+    }
+    __device__ __forceinline__ void rotate(float (&x)[16], const float2 (&t)[kSines], int d0, int R) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = own[i / VEC].at(i % VEC);
+        if constexpr (PAIRS == kHalves) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                // x cos + y sin, the sine's sign turned for low halves: as turned() rounds it
+                const float y = other[i / VEC].at(i % VEC);
+                if (d0 + i / VEC * VEC < R) x[i] = __fmaf_rn(x[i], t[i].x, __fmul_rn(y, t[i].y));
+            }
+        } else if constexpr (PAIRS == kInterleaved) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float u = x[i], v = x[i + 1];
+                if (d0 + i >= R) continue;
+                x[i] = turned(u, v, t[i / 2]);
+                x[i + 1] = turned(v, -u, t[i / 2]);
+            }
+        }
+    }
+};
+
+// The larger one, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // A block of 16 as NVFP4 under the head's scale s: its codes and its scale. The products
@@ -178,18 +316,41 @@ __device__ __forceinline__ bool any_nan(const float (&x)[16]) {
 // a border come out as it says. A NaN makes the block's scale NaN, and with it every
 // value; infinities are held as the largest value.
 __device__ __forceinline__ uint8_t quantise16(const float (&x)[16], float s, uint32_t (&codes)[2]) {
-    float m = 0.f;
+    float m = fabsf(x[0]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
-    const uint32_t b = e4m3x2(__fmul_rn(m, __fdiv_rn(1.f, __fmul_rn(6.f, s))), 0.f) & 0xFF;
-    const float inv = b == 0 ? 0.f : fminf(__fdiv_rn(1.f, __fmul_rn(e4m3_to_f(b), s)), 3.402823466e38f);
+    for (int i = 1; i < 16; ++i) m = max_nan(m, fabsf(x[i]));
+    const uint32_t b = e4m3x2(__fmul_rn(m, __frcp_rn(__fmul_rn(6.f, s))), 0.f) & 0xFF;      // NaN: 0x7F
     codes[0] = codes[1] = 0;
-    if (any_nan(x)) return 0x7F;
-    if (b == 0) return 0;
+    if (b == 0 || b == 0x7F) return static_cast<uint8_t>(b);
+    const float inv = fminf(__frcp_rn(__fmul_rn(e4m3_to_f(b), s)), 3.402823466e38f);
 #pragma unroll
     for (int i = 0; i < 16; i += 2)
         codes[i / 8] |= e2m1x2(__fmul_rn(x[i], inv), __fmul_rn(x[i + 1], inv)) << (4 * (i % 8));
     return static_cast<uint8_t>(b);
+}
+
+// E4M3(x / s) of 16 values, as the rounded quotient gives it. x (1 / s) is within 2.5
+// steps of that (5 below a power of two), so the code is the same unless a border between
+// codes, a number of five significant bits, lies that near: then, of numbers that are
+// not zero or exact one in 30,000, the quotients are taken. Where s is a power of two
+// the product is the quotient.
+__device__ __forceinline__ void divide16(const float (&x)[16], float s, uint32_t (&c)[4]) {
+    const float r = __frcp_rn(s);
+    float y[16];
+    uint32_t near = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        y[i] = __fmul_rn(x[i], r);
+        near = min(near, (__float_as_uint(y[i]) + 8) & 0x7FFFFu);
+    }
+    const bool plain = s > 1e-30f && s < 1e30f;
+    if (!plain || (near <= 16 && (__float_as_uint(s) & 0x7FFFFFu) != 0)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(x[i], s);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = e4m3x2(y[4 * i], y[4 * i + 1]) | (static_cast<uint32_t>(e4m3x2(y[4 * i + 2], y[4 * i + 3])) << 16);
 }
 
 // Where a token's 16 channels from d0 = 16 b on lie in a cache.
@@ -219,12 +380,8 @@ __device__ __forceinline__ void store_block(const PlaceArgs& a, const float (&x)
     } else {
         const int64_t at = (static_cast<int64_t>(head) * a.page_size + in_page) * a.dim + 16 * b;
         if constexpr (KV == RSSM_KV_FP8) {
-            const float s = scales[head];
             uint32_t c[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                c[i] = e4m3x2(__fdiv_rn(x[4 * i], s), __fdiv_rn(x[4 * i + 1], s)) |
-                       (static_cast<uint32_t>(e4m3x2(__fdiv_rn(x[4 * i + 2], s), __fdiv_rn(x[4 * i + 3], s))) << 16);
+            divide16(x, scales[head], c);
             *reinterpret_cast<uint4*>(cache + page * a.page_stride + at) = make_uint4(c[0], c[1], c[2], c[3]);
         } else {
             store_n<T, 16>(reinterpret_cast<T*>(cache + page * a.page_stride) + at, x);
@@ -268,144 +425,160 @@ __device__ __forceinline__ void fetch_block(const PlaceArgs& a, float (&x)[16], 
                 x[2 * i + 1] = __fmul_rn(v.y, s);
             }
         } else {
-            load_n<T, 16>(x, reinterpret_cast<const T*>(cache + page * a.page_stride) + at);
+            constexpr int kStep = 16 / sizeof(T);
+#pragma unroll
+            for (int i = 0; i < 16; i += kStep) {
+                Pack<T, kStep> p;
+                p.load(reinterpret_cast<const T*>(cache + page * a.page_stride) + at + i);
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) x[i + j] = p.at(j);
+            }
         }
     }
 }
 
-// Unit i of a tile's blocks of keys and values. Blocks run fastest, then up to four
-// tokens, whose V codes share a sector, then heads (keys before values), then fours
-// of tokens.
-struct Unit {
-    int t, head, b;
-    bool v;
+// A thread's share of a tile's blocks of 16 channels: one block of one token in every
+// `step`-th head. Blocks run fastest, then tokens (four share a sector of V codes), then heads.
+struct Share {
+    int b, t, head, step;
 };
-__device__ __forceinline__ Unit unit_of(uint32_t i, const PlaceArgs& a, int tq_log2) {
-    const uint32_t nb = a.dim / 16;
-    Unit u;
-    u.b = i & (nb - 1);
-    i /= nb;
-    const uint32_t t = i & ((1u << tq_log2) - 1);
-    i >>= tq_log2;
-    const uint32_t heads = 2 * a.heads, four = i / heads, h = i - four * heads;
-    u.t = static_cast<int>((four << tq_log2) + t);
-    u.v = h >= static_cast<uint32_t>(a.heads);
-    u.head = static_cast<int>(u.v ? h - a.heads : h);
-    return u;
+__device__ __forceinline__ Share share_of(const PlaceArgs& a, int nt_log2) {
+    const int nb = a.dim / 16, nb_log2 = nb == 4 ? 2 : nb == 8 ? 3 : 4;
+    Share s;
+    s.b = threadIdx.x & (nb - 1);
+    s.t = (threadIdx.x >> nb_log2) & ((1 << nt_log2) - 1);
+    const int per = kThreads >> (nb_log2 + nt_log2);
+    s.head = threadIdx.x >> (nb_log2 + nt_log2);
+    s.step = per;
+    return s;
 }
 
-// A slot's page and place, or false where it is to be skipped (and one past the cache is reported).
-__device__ __forceinline__ bool slot_of(const PlaceArgs& a, int64_t tok, const Unit& u, int& page, int& in_page) {
+// A token's page and place, or false where it is to be skipped (and, `tell`, one past the cache is reported).
+__device__ __forceinline__ bool slot_of(const PlaceArgs& a, int64_t tok, bool tell, int& page, int& in_page) {
     const int32_t slot = a.slots[tok];
     if (slot < 0) return false;
     page = slot / a.page_size;
     in_page = slot - page * a.page_size;
     if (page < a.num_pages) return true;
-    if (u.b == 0 && u.head == 0 && !u.v) report_error(a.err, RSSM_DEV_ATTN_SLOT, static_cast<int>(tok), slot);
+    if (tell) report_error(a.err, RSSM_DEV_ATTN_SLOT, static_cast<int>(tok), slot);
     return false;
 }
 
-template <class T, int KV, int VEC, bool ROPE>
-__global__ void __launch_bounds__(kThreads) place_kernel(const PlaceArgs a, int nt, int tq_log2) {
+// grid.y: 1, and a block takes its tile's queries, keys and values; or one block for the
+// keys, one for the values and the others for the queries (none where there are none).
+template <class T, int KV, int VEC, int PAIRS>
+__global__ void __launch_bounds__(kThreads) place_kernel(const PlaceArgs a, int nt_log2) {
     extern __shared__ float2 cs[];
     after_predecessor();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * nt;
-    const int n = static_cast<int>(min(static_cast<int64_t>(nt), a.tokens - first)), half = a.rotary_dim / 2;
-    const bool inter = ROPE && a.interleaved != 0;
-    uint32_t nq = 0, per_head = 1, per_token = 1;
-    if (ROPE) {
-        make_turns(cs, a.positions, a.turns, first, n, half, a.gain);
-        if (a.q != nullptr) {
-            per_head = (half + (a.q_out == a.q ? 0 : a.dim - a.rotary_dim)) / VEC;
-            per_token = a.q_heads * per_head;
-            nq = n * per_token;
-        }
-    }
-    const uint32_t units = static_cast<uint32_t>(nt) * 2 * a.heads * (a.dim / 16);
-    for (uint32_t i = blockIdx.y * kThreads + threadIdx.x; i < nq + units; i += gridDim.y * kThreads) {
-        if (ROPE && i < nq) {
-            const uint32_t t = i / per_token, r = i - t * per_token, h = r / per_head;
-            const T* x = static_cast<const T*>(a.q) + (first + t) * a.q_stride + static_cast<int64_t>(h) * a.dim;
-            T* out = static_cast<T*>(a.q_out) + (first + t) * a.qo_stride + static_cast<int64_t>(h) * a.dim;
-            rotate_item<T, VEC>(x, out, cs + t * half, r - h * per_head, a.rotary_dim, inter);
-            continue;
-        }
-        const Unit u = unit_of(i - nq, a, tq_log2);
-        int page, in_page;
-        if (u.t >= n || !slot_of(a, first + u.t, u, page, in_page)) continue;
-        float x[16];
-        if (u.v) {
-            load_block<T, VEC, false>(x, static_cast<const T*>(a.v) + (first + u.t) * a.v_stride + static_cast<int64_t>(u.head) * a.dim,
-                                      16 * u.b, cs, 0, false);
-            store_block<T, KV, true>(a, x, page, u.head, in_page, u.b);
-        } else {
-            load_block<T, VEC, ROPE>(x, static_cast<const T*>(a.k) + (first + u.t) * a.k_stride + static_cast<int64_t>(u.head) * a.dim,
-                                     16 * u.b, cs + u.t * half, a.rotary_dim, inter);
-            store_block<T, KV, false>(a, x, page, u.head, in_page, u.b);
-        }
-    }
-}
-
-template <class T, int KV, int VEC>
-__global__ void __launch_bounds__(kThreads) read_kernel(const PlaceArgs a, int nt, int tq_log2) {
-    after_predecessor();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * nt;
+    const int nt = 1 << nt_log2, half = a.rotary_dim / 2;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) << nt_log2;
     const int n = static_cast<int>(min(static_cast<int64_t>(nt), a.tokens - first));
-    const uint32_t units = static_cast<uint32_t>(nt) * 2 * a.heads * (a.dim / 16);
-    for (uint32_t i = blockIdx.y * kThreads + threadIdx.x; i < units; i += gridDim.y * kThreads) {
-        const Unit u = unit_of(i, a, tq_log2);
-        int page, in_page;
-        if (u.t >= n || !slot_of(a, first + u.t, u, page, in_page)) continue;
-        float x[16];
-        if (u.v) fetch_block<T, KV, true>(a, x, page, u.head, in_page, u.b);
-        else fetch_block<T, KV, false>(a, x, page, u.head, in_page, u.b);
-        T* out = static_cast<T*>(const_cast<void*>(u.v ? a.v : a.k)) + (first + u.t) * (u.v ? a.v_stride : a.k_stride) +
-                 static_cast<int64_t>(u.head) * a.dim + 16 * u.b;
-#pragma unroll
-        for (int q = 0; q < 16; q += VEC) store_n<T, VEC>(out + q, x + q);
+    const bool all = gridDim.y == 1, keys = all || blockIdx.y == 0, values = all || blockIdx.y == 1;
+    const Share u = share_of(a, nt_log2);
+    int page = 0, in_page = 0;
+    bool live = false;
+    if (keys || values) live = u.t < n && slot_of(a, first + u.t, keys && u.b == 0 && u.head == 0, page, in_page);
+    if constexpr (PAIRS != kNone) {
+        Rotator<T, VEC, PAIRS> r;
+        const bool queries = a.q != nullptr && (all || blockIdx.y > 1);
+        if (queries)
+            r.start(static_cast<const T*>(a.q) + first * a.q_stride, static_cast<T*>(a.q_out) + first * a.qo_stride, a.q_stride, a.qo_stride,
+                    a.q_heads, a.dim, a.rotary_dim, nt, n, all ? 0 : blockIdx.y - 2, all ? 1 : gridDim.y - 2);
+        if (all || !values) make_turns(cs, a.positions, a.turns, first, n, half, VEC, a.gain);
+        if (queries) r.run(cs);
+    }
+    if (!live) return;
+    const int64_t next = u.step * static_cast<int64_t>(a.dim);
+    if (keys) {
+        using K = Key<T, VEC, PAIRS>;
+        float2 t[K::kSines];
+        K::sines(t, cs + u.t * half, 16 * u.b, a.rotary_dim);
+        const T* row = static_cast<const T*>(a.k) + (first + u.t) * a.k_stride + u.head * static_cast<int64_t>(a.dim);
+        K k;
+        if (u.head < a.heads) k.load(row, 16 * u.b, a.rotary_dim);
+        for (int h = u.head; h < a.heads; h += u.step) {
+            const K now = k;
+            row += next;
+            if (h + u.step < a.heads) k.load(row, 16 * u.b, a.rotary_dim);       // the next one's on their way
+            float x[16];
+            now.rotate(x, t, 16 * u.b, a.rotary_dim);
+            store_block<T, KV, false>(a, x, page, h, in_page, u.b);
+        }
+    }
+    if (values) {
+        using K = Key<T, VEC, kNone>;
+        const float2 t[K::kSines] = {};
+        const T* row = static_cast<const T*>(a.v) + (first + u.t) * a.v_stride + u.head * static_cast<int64_t>(a.dim);
+        K v;
+        if (u.head < a.heads) v.load(row, 16 * u.b, 0);
+        for (int h = u.head; h < a.heads; h += u.step) {
+            const K now = v;
+            row += next;
+            if (h + u.step < a.heads) v.load(row, 16 * u.b, 0);
+            float x[16];
+            now.rotate(x, t, 0, 0);
+            store_block<T, KV, true>(a, x, page, h, in_page, u.b);
+        }
     }
 }
 
-// The widest of 8, 4, 2 and 1 elements by which all of `steps` (strides and channel counts,
-// 0 for none) and the pointers, in elements of es bytes, can be taken.
+// grid.y: 0 the keys, 1 the values.
+template <class T, int KV, int VEC>
+__global__ void __launch_bounds__(kThreads) read_kernel(const PlaceArgs a, int nt_log2) {
+    after_predecessor();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) << nt_log2;
+    const Share u = share_of(a, nt_log2);
+    const bool v = blockIdx.y == 1;
+    int page, in_page;
+    if (first + u.t >= a.tokens || !slot_of(a, first + u.t, !v && u.b == 0 && u.head == 0, page, in_page)) return;
+    T* row = static_cast<T*>(const_cast<void*>(v ? a.v : a.k)) + (first + u.t) * (v ? a.v_stride : a.k_stride);
+    for (int h = u.head; h < a.heads; h += u.step) {
+        float x[16];
+        if (v) fetch_block<T, KV, true>(a, x, page, h, in_page, u.b);
+        else fetch_block<T, KV, false>(a, x, page, h, in_page, u.b);
+#pragma unroll
+        for (int q = 0; q < 16; q += VEC) store_n<T, VEC>(row + static_cast<int64_t>(h) * a.dim + 16 * u.b + q, x + q);
+    }
+}
+
+// The widest of 16 bytes, 4, 2 and 1 elements by which all of `steps` (strides and channel
+// counts, 0 for none) and the pointers, in elements of es bytes, can be taken.
 int vec_of(std::initializer_list<int64_t> steps, std::initializer_list<const void*> ptrs, int es) {
-    int vec = 8;
+    int vec = 16 / es;
     const auto fits = [&] {
         for (const int64_t s : steps)
             if (s % vec != 0) return false;
-        const uintptr_t bytes = vec * es < 16 ? vec * es : 16;
         for (const void* p : ptrs)
-            if (reinterpret_cast<uintptr_t>(p) % bytes != 0) return false;
+            if (reinterpret_cast<uintptr_t>(p) % (vec * es) != 0) return false;
         return true;
     };
     while (vec > 1 && !fits()) vec /= 2;
     return vec;
 }
 
-struct Tiling {
-    int nt, tq_log2;
-    dim3 grid;
-};
-
-// Tokens of a block's tile: four, whose sines 256 threads make at once for 128 rotated
-// channels, where that still leaves four blocks an SM; else one, with its units spread
-// over several blocks while those are few.
-cudaError_t tiling(int64_t tokens, int64_t units_per_token, Tiling* t) {
-    int sms = 0, smem = 0;
-    const cudaError_t e = device_limits(&sms, &smem);
-    if (e != cudaSuccess) return e;
-    t->nt = tokens >= 16 * static_cast<int64_t>(sms) ? 4 : 1;
-    t->tq_log2 = t->nt == 4 ? 2 : 0;
-    const int64_t blocks = (tokens + t->nt - 1) / t->nt, per = (units_per_token * t->nt + kThreads - 1) / kThreads;
-    const int64_t room = (4 * static_cast<int64_t>(sms) + blocks - 1) / blocks;
-    t->grid = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(per < room ? per : room));
-    return cudaSuccess;
+// Tokens of a block's tile, as a power of two: up to 16, so that what a thread finds out
+// about its token and channels serves several heads, while eight blocks an SM are left
+// and the sines (half a token) fit 32 KB.
+cudaError_t tile_log2(int64_t tokens, int half, int* sms, int* out) {
+    int smem = 0;
+    const cudaError_t e = device_limits(sms, &smem);
+    *out = 0;
+    while (*out < 4 && tokens >> (*out + 1) >= 8 * static_cast<int64_t>(*sms) && static_cast<size_t>(half) << (*out + 1) <= 32768 / sizeof(float2)) ++*out;
+    return e;
 }
 
-template <class F>
+// Blocks that share the heads of one token's tile: as many as have a row of threads each
+// to work on, while that leaves four blocks an SM at most.
+int split(int64_t blocks, int64_t items, int sms) {
+    const int64_t per = (items + kThreads - 1) / kThreads, room = (4 * static_cast<int64_t>(sms) + blocks - 1) / blocks;
+    return static_cast<int>(per < 1 ? 1 : per < room ? per : room);
+}
+
+template <class T, class F>
 cudaError_t by_vec(int vec, F f) {
+    if constexpr (sizeof(T) == 2)
+        if (vec == 8) return f(std::integral_constant<int, 8>{});
     switch (vec) {
-        case 8: return f(std::integral_constant<int, 8>{});
         case 4: return f(std::integral_constant<int, 4>{});
         case 2: return f(std::integral_constant<int, 2>{});
         default: return f(std::integral_constant<int, 1>{});
@@ -429,30 +602,40 @@ cudaError_t place_launch(const PlaceArgs& a, cudaStream_t s) {
     const int es = a.in_dtype == RSSM_F32 ? 4 : 2, half = a.rotary_dim / 2;
     const bool rope = a.positions != nullptr;
     // a vector lies in one half of the rotated channels, or beside them
-    const int vec = vec_of({a.k_stride, a.v_stride, a.q ? a.q_stride : 0, a.q ? a.qo_stride : 0, a.interleaved ? 0 : half, a.rotary_dim / (a.interleaved ? 2 : 1)},
-                           {a.k, a.v, a.q, a.q_out}, es);
-    Tiling t;
-    const int64_t q_units = rope && a.q ? static_cast<int64_t>(a.q_heads) * ((half + a.dim - a.rotary_dim) / vec) : 0;
-    const cudaError_t e = tiling(a.tokens, q_units + 2 * static_cast<int64_t>(a.heads) * (a.dim / 16), &t);
+    const int vec = vec_of({a.k_stride, a.v_stride, a.q ? a.q_stride : 0, a.q ? a.qo_stride : 0, half}, {a.k, a.v, a.q, a.q_out}, es);
+    int nt = 0, sms = 0;
+    const cudaError_t e = tile_log2(a.tokens, half, &sms, &nt);
     if (e != cudaSuccess) return e;
-    const size_t smem = static_cast<size_t>(t.nt) * half * sizeof(float2);
+    const int64_t blocks = (a.tokens + (1 << nt) - 1) >> nt;
+    dim3 grid(static_cast<unsigned>(blocks));
+    if (nt == 0 && 3 * blocks <= 4 * static_cast<int64_t>(sms)) {
+        // few tokens: keys, values and queries in blocks of their own
+        const int per_head = rope && a.q ? (half + (a.q_out == a.q ? 0 : a.dim - a.rotary_dim)) / vec : 0;
+        grid.y = 2 + (per_head ? split(3 * blocks, static_cast<int64_t>(a.q_heads) * per_head, sms) : 0);
+    }
+    const size_t smem = (static_cast<size_t>(half) << nt) * sizeof(float2);
     return by_cache(a, [&](auto in, auto kv) {
-        return by_vec(vec, [&](auto v) {
-            using T = decltype(in);
-            if (rope) return launch_overlapped(place_kernel<T, decltype(kv)::value, decltype(v)::value, true>, t.grid, kThreads, smem, s, a, t.nt, t.tq_log2);
-            return launch_overlapped(place_kernel<T, decltype(kv)::value, decltype(v)::value, false>, t.grid, kThreads, 0, s, a, t.nt, t.tq_log2);
+        using T = decltype(in);
+        return by_vec<T>(vec, [&](auto v) {
+            constexpr int KV = decltype(kv)::value, VEC = decltype(v)::value;
+            if (rope && a.interleaved) return launch_overlapped(place_kernel<T, KV, VEC, kInterleaved>, grid, kThreads, smem, s, a, nt);
+            if (rope) return launch_overlapped(place_kernel<T, KV, VEC, kHalves>, grid, kThreads, smem, s, a, nt);
+            if constexpr (KV == RSSM_KV_NVFP4) return launch_overlapped(place_kernel<T, KV, VEC, kNone>, grid, kThreads, 0, s, a, nt);
+            return cudaErrorInvalidValue;                    // the others have a writer of their own (attn.cu)
         });
     });
 }
 
 cudaError_t read_launch(const PlaceArgs& a, cudaStream_t s) {
     const int vec = vec_of({a.k_stride, a.v_stride}, {a.k, a.v}, a.in_dtype == RSSM_F32 ? 4 : 2);
-    Tiling t;
-    const cudaError_t e = tiling(a.tokens, 2 * static_cast<int64_t>(a.heads) * (a.dim / 16), &t);
+    int nt = 0, sms = 0;
+    const cudaError_t e = tile_log2(a.tokens, 0, &sms, &nt);
     if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>((a.tokens + (1ll << nt) - 1) >> nt), 2);
     return by_cache(a, [&](auto in, auto kv) {
-        return by_vec(vec, [&](auto v) {
-            return launch_overlapped(read_kernel<decltype(in), decltype(kv)::value, decltype(v)::value>, t.grid, kThreads, 0, s, a, t.nt, t.tq_log2);
+        using T = decltype(in);
+        return by_vec<T>(vec, [&](auto v) {
+            return launch_overlapped(read_kernel<T, decltype(kv)::value, decltype(v)::value>, grid, kThreads, 0, s, a, nt);
         });
     });
 }
@@ -467,16 +650,19 @@ bool is_finite(double x) { return x - x == 0.0; }
 
 template <class T>
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
-    const int half = a.rotary_dim / 2;
-    const int vec = vec_of({a.heads > 1 ? a.dim : 0, a.tokens > 1 ? a.x_stride : 0, a.tokens > 1 ? a.out_stride : 0, half,
-                            a.out == a.x ? 0 : a.dim - a.rotary_dim},
+    const int half = a.rotary_dim / 2, beside = a.out == a.x ? 0 : a.dim - a.rotary_dim;
+    const int vec = vec_of({a.heads > 1 ? a.dim : 0, a.tokens > 1 ? a.x_stride : 0, a.tokens > 1 ? a.out_stride : 0, half, beside},
                            {a.x, a.out}, sizeof(T));
-    Tiling t;
-    const int64_t units = static_cast<int64_t>(a.heads) * ((half + (a.out == a.x ? 0 : a.dim - a.rotary_dim)) / vec);
-    const cudaError_t e = tiling(a.tokens, units, &t);
+    int nt = 0, sms = 0;
+    const cudaError_t e = tile_log2(a.tokens, half, &sms, &nt);
     if (e != cudaSuccess) return e;
-    return by_vec(vec, [&](auto v) {
-        return launch_overlapped(rotary_kernel<T, decltype(v)::value>, t.grid, kThreads, static_cast<size_t>(t.nt) * half * sizeof(float2), s, a, t.nt);
+    const int64_t blocks = (a.tokens + (1 << nt) - 1) >> nt;
+    const dim3 grid(static_cast<unsigned>(blocks), nt == 0 ? split(blocks, static_cast<int64_t>(a.heads) * ((half + beside) / vec), sms) : 1);
+    const size_t smem = (static_cast<size_t>(half) << nt) * sizeof(float2);
+    return by_vec<T>(vec, [&](auto v) {
+        constexpr int VEC = decltype(v)::value;
+        if (a.interleaved) return launch_overlapped(rotary_kernel<T, VEC, kInterleaved>, grid, kThreads, smem, s, a, 1 << nt);
+        return launch_overlapped(rotary_kernel<T, VEC, kHalves>, grid, kThreads, smem, s, a, 1 << nt);
     });
 }
 
