@@ -104,7 +104,10 @@ int attn_chunks(int rows, const rssm_attn_config& c) {
 AttnLayout attn_layout(const rssm_attn_config& c) {
     AttnLayout L{};
     const int rows = c.max_draft * (c.q_heads / c.kv_heads);
-    const size_t parts = 2 * static_cast<size_t>(kAttnMaxGrid) * attn_block_rows(rows, c.kv_dtype, c.head_dim);
+    const int block_rows = attn_block_rows(rows, c.kv_dtype, c.head_dim);
+    const int grid = attn_max_grid(c.kv_dtype == RSSM_KV_NVFP4 ? attn4_blocks(block_rows, c.head_dim) : 2);
+    // a call with fewer drafts may make more blocks, of rows fewer by as much or more
+    const size_t parts = 2 * static_cast<size_t>(grid) * block_rows;
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off += up256(bytes); return o; };
     L.err = take(20);                     // the error word, and whether any wait ran out

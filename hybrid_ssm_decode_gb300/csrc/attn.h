@@ -7,7 +7,7 @@
 
 namespace rssm {
 
-constexpr int kAttnMaxGrid = 304;    // blocks of one launch at most: two per SM
+constexpr int kAttnMaxGrid = 608;    // blocks of one launch at most: four per SM
 constexpr int kAttnGroup = 16;       // tokens that one warp takes at a time
 constexpr int kAttnUnit = 4;         // groups in the unit by which work is shared out
 constexpr int kEvenUnits = 8;        // units a block below which few requests are cut evenly (attn_decode.cuh)
@@ -38,6 +38,11 @@ inline int attn_block_rows(int rows, int kv_dtype, int D) {
     return kv_dtype == RSSM_KV_NVFP4 && rows <= 8 ? 8
          : rows <= 16 ? 16 : rows <= 32 || (kv_dtype == RSSM_F32 && D == 256) ? 32 : 64;
 }
+
+// Blocks an SM for which an NVFP4 launch of that shape is made (attn_nvfp4.cuh), and the
+// blocks of a launch at most; never below two an SM, what the parts' room is made for.
+__host__ __device__ constexpr int attn4_blocks(int rows, int D) { return rows == 8 ? (D == 256 ? 2 : 4) : rows == 16 && D < 256 ? 2 : 1; }
+__host__ __device__ constexpr int attn_max_grid(int blocks_per_sm) { return 152 * (blocks_per_sm < 2 ? 2 : blocks_per_sm); }
 
 // The kernels by cache type (attn_f32.cu, attn_bf16.cu, attn_fp8.cu, attn_nvfp4.cu).
 cudaError_t attn_launch_f32(const AttnArgs& a, int D, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);

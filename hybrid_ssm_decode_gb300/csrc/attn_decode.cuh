@@ -76,7 +76,9 @@ struct Shape {
     static constexpr int CH = RB / CB;
     static constexpr int kHalf = kAttnGroup * RB;        // K (or V) of a slot
     static constexpr int kSlot = 2 * kHalf;
-    static constexpr int kCopied = 2 * kHalf;            // bytes that the copies of a slot bring
+    static constexpr int kSlotGroups = 1;                // groups in a slot
+    static constexpr int kJoin = 16;                     // parts joined at a time
+    static constexpr int kCopied = 2 * kHalf;            // bytes that the copies of a group bring
     static constexpr int QS = D * kQsz + 16;             // bytes from one query row to the next
     static constexpr int OS = D + 8;                     // floats from one merged row to the next
     // Two blocks per SM where the registers allow it: one block's joins then
@@ -375,6 +377,7 @@ struct Part {
     int first;                   // block of the request's first part
     int others;                  // parts of the request and head beside this one
     int at_start;                // the part begins with the request's first unit
+    float ks, vs;                // FP8 and NVFP4: the head's scales
 };
 
 // ---- one warp's products -----------------------------------------------------
@@ -893,16 +896,14 @@ __device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, 
 // Join the parts of a request and head: the consumer warps, once all have
 // arrived. Not inlined: it runs once or twice a block, and its registers are
 // not the stream's.
-constexpr int kJoin = 16;      // parts joined at a time
-
 template <int KV, class S>
 __device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, float* fw, float2* s_row, volatile int* s_last) {
     const int rows = min(S::kRows, a.T * a.group - part.row0);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int D = S::D, kThreads = S::kConsumers * 32;
-    static_assert((kAttnMaxGrid + kJoin - 1) / kJoin <= 32 && 32 <= S::OS, "a round of parts must fit a warp and the buffer");
+    constexpr int D = S::D, kThreads = S::kConsumers * 32, kJoin = S::kJoin;
+    static_assert((attn_max_grid(S::kMinBlocks) + kJoin - 1) / kJoin <= 32 && kJoin <= 32 && 32 <= S::OS, "a round of parts must fit a warp and the buffer");
     const int np = part.others + 1;
-    const float vs = KV == kFP8 || KV == kNVFP4 ? __ldcg(a.v_scale + part.head) : 1.f;
+    const float vs = KV == kFP8 || KV == kNVFP4 ? part.vs : 1.f;
     // this block's kJoin neighbours, and then one part for each such round; or all at once
     int p0 = 0, step = 1, n = np;
     bool final = np <= kJoin;
@@ -976,6 +977,7 @@ __device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, floa
             }
         };
         if (rows * (D / 4) <= kThreads) sums(Int<1>{}, Int<16>{});
+        else if (KV == kNVFP4 && rows * (D / 4) <= 2 * kThreads) sums(Int<2>{}, Int<8>{});
         else sums(Int<4>{}, Int<4>{});
         if (final) return;
         named_sync(1, kThreads);
@@ -993,7 +995,7 @@ __device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, floa
 template <int KV, class S>
 __global__ void __launch_bounds__(S::kThreads, S::kMinBlocks)
 attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    constexpr int D = S::D, NS = S::NS;
+    constexpr int D = S::D, NS = S::NS, kJoin = S::kJoin;
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     char* slots = smem;
@@ -1059,6 +1061,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             nd.b = cur.b;
             nd.len = cur.sp.len;
             nd.head = cur.pair / a.chunks;
+            if (KV == kFP8 || KV == kNVFP4) {                // here, where nobody waits for them
+                nd.ks = __ldcg(a.k_scale + nd.head);
+                nd.vs = __ldcg(a.v_scale + nd.head);
+            }
             nd.row0 = (cur.pair - nd.head * a.chunks) * S::kRows;
             nd.g0 = cur.first_group();
             ng1 = cur.end_group();
@@ -1116,19 +1122,34 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
                 for (int i = 0; i < n; i += S::PB) {
                     const int m = min(S::PB, n - i);
                     const int pg = __shfl_sync(0xffffffffu, page, (i + lane) & 31), rw = __shfl_sync(0xffffffffu, row, (i + lane) & 31);
-                    if (lane < m) {
+                    if constexpr (S::kSlotGroups == 2) {
+                        // a slot's first lane waits for it, and both copy
+                        const int sl = lane / 2;
+                        const bool wrap = pos + sl >= NS;
+                        const int s = pos + sl - (wrap ? NS : 0), tn = turn + (wrap ? 1 : 0);
+                        bool go = false;
+                        if (lane < m && lane % 2 == 0) {
+                            go = (tn == 0 || wait_phase(empty + s, (tn - 1) & 1, dead, a.err)) && !*dead;
+                            if (go) mbar_arrive_expect_tx(full + s, S::kCopied * min(2, m - lane));
+                        }
+                        go = __shfl_sync(0xffffffffu, go, lane & 30);
+                        if (go && lane < m) {
+                            const uint32_t dst = smem_u32(slots + s * S::kSlot + lane % 2 * 2 * S::kHalf);
+                            tma_load_5d(dst, &kmap, 0, rw / kAttnGroup, d.head, pg, full + s);
+                            tma_load_5d(dst + S::kHalf, &vmap, 0, rw / kAttnGroup, d.head, pg, full + s);
+                        }
+                    } else if (lane < m) {
                         const bool wrap = pos + lane >= NS;
                         const int s = pos + lane - (wrap ? NS : 0), tn = turn + (wrap ? 1 : 0);
                         if ((tn == 0 || wait_phase(empty + s, (tn - 1) & 1, dead, a.err)) && !*dead) {
                             const uint32_t dst = smem_u32(slots + s * S::kSlot);
-                            const int tok = KV == kNVFP4 ? 0 : rw, grp = KV == kNVFP4 ? rw / kAttnGroup : 0;
                             mbar_arrive_expect_tx(full + s, S::kCopied);
-                            tma_load_5d(dst, &kmap, tok, grp, d.head, pg, full + s);
-                            tma_load_5d(dst + S::kHalf, &vmap, tok, grp, d.head, pg, full + s);
+                            tma_load_5d(dst, &kmap, rw, 0, d.head, pg, full + s);
+                            tma_load_5d(dst + S::kHalf, &vmap, rw, 0, d.head, pg, full + s);
                         }
                     }
                     __syncwarp();
-                    pos += m;
+                    pos += (m + S::kSlotGroups - 1) / S::kSlotGroups;
                     if (pos >= NS) {
                         pos -= NS;
                         ++turn;
@@ -1186,7 +1207,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         const Part part = s_part[pq];
         if (part.pair < 0) break;
         if (left.pair >= 0 && tid == 0) count_left();
-        const int head = part.head, row0 = part.row0, len = part.len;
+        const int row0 = part.row0, len = part.len;
         const int rows = min(S::kRows, rows_all - row0);
         // what the lane's rows see: [see_lo, see_hi]
         int draft[kLaneRows], see_lo[kLaneRows], see_hi[kLaneRows];
@@ -1202,19 +1223,19 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         const int some_lo = window_start(len - a.T, a.window);
         wp.reset();
         wp.load_q(qbuf + (pq * S::kRows + wm * S::kWarpRows) * S::QS, a.scale_log2,
-                  KV == kFP8 || KV == kNVFP4 ? __ldcg(a.k_scale + head) : 1.f);
+                  KV == kFP8 || KV == kNVFP4 ? part.ks : 1.f);
         if (KV != kF32) {
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty + pq);
         }
         // this warp's groups: those whose slot is wt modulo NT; those that all rows
         // see whole, [f0, f1), two at a time where the registers allow it
-        const int g0 = part.g0, ng = part.ng;
+        const int g0 = part.g0, ng = part.ng, ns = (ng + S::kSlotGroups - 1) / S::kSlotGroups;
         const int f0 = (all_lo + kAttnGroup - 1) / kAttnGroup - g0, f1 = (all_hi + 1) / kAttnGroup - g0;
         constexpr int NG = S::kPair ? 2 : 1;
         int k = (wt + S::NT - pos % S::NT) % S::NT;
         int s = pos + k, tn = turn;
-        const auto forward = [&] {                            // to this warp's next group
+        const auto forward = [&] {                            // to this warp's next slot
             k += S::NT;
             s += S::NT;
             if (s >= NS) {
@@ -1226,11 +1247,28 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             s -= NS;
             ++tn;
         }
-        while (k < ng) {
+        // group i, of which not all tokens may be seen
+        const auto masked = [&](int i, uint32_t kb) {
+            const int tok = (g0 + i) * kAttnGroup;
+            int lo[kLaneRows], hi[kLaneRows];
+#pragma unroll
+            for (int x = 0; x < kLaneRows; ++x) lo[x] = see_lo[x] - tok, hi[x] = see_hi[x] - tok;
+            wp.step_masked(kb, kb + S::kHalf, lo, hi, some_lo - tok, len - 1 - tok, all_lo - tok, all_hi - tok, a.T, tok, len, a.window, draft);
+        };
+        while (k < ns) {
             const uint32_t kb = smem_u32(slots + s * S::kSlot), vb = kb + S::kHalf;
             uint64_t* const done = empty + s;
             bool ok = wait_phase(full + s, tn & 1, dead, a.err);
-            if (k >= f0 && k < f1) {
+            if constexpr (S::kSlotGroups == 2) {
+                const int i = 2 * k;
+                if (ok && i >= f0 && i + 2 <= min(f1, ng)) {
+                    const uint32_t ks[2] = {kb, kb + 2 * S::kHalf}, vs[2] = {vb, vb + 2 * S::kHalf};
+                    wp.step(ks, vs);
+                } else if (ok) {
+#pragma unroll 1
+                    for (int j = 0; j < min(2, ng - i); ++j) masked(i + j, kb + j * 2 * S::kHalf);
+                }
+            } else if (k >= f0 && k < f1) {
                 if (NG == 2 && k + S::NT < min(f1, ng)) {
                     forward();
                     const uint32_t kb2 = smem_u32(slots + s * S::kSlot), vb2 = kb2 + S::kHalf;
@@ -1244,17 +1282,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
                     if (ok) wp.step(ks, vs);
                 }
             } else if (ok) {
-                const int tok = (g0 + k) * kAttnGroup;
-                int lo[kLaneRows], hi[kLaneRows];
-#pragma unroll
-                for (int x = 0; x < kLaneRows; ++x) lo[x] = see_lo[x] - tok, hi[x] = see_hi[x] - tok;
-                wp.step_masked(kb, vb, lo, hi, some_lo - tok, len - 1 - tok, all_lo - tok, all_hi - tok, a.T, tok, len, a.window, draft);
+                masked(k, kb);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(done);
             forward();
         }
-        pos += ng;
+        pos += ns;
         turn += pos / NS;
         pos %= NS;
         if (KV == kF32) {
@@ -1262,7 +1296,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             if (lane == 0) mbar_arrive(qempty + pq);
         }
         ++parts;
-        const float vs = KV == kFP8 || KV == kNVFP4 ? __ldcg(a.v_scale + head) : 1.f;   // there once the warps are joined
+        const float vs = KV == kFP8 || KV == kNVFP4 ? part.vs : 1.f;
 
         // ---- join the warps of each row ----
 #pragma unroll
@@ -1330,7 +1364,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     }
 }
 
-// Launch of one shape: as many blocks as the GPU holds at once, at most kAttnMaxGrid.
+// Launch of one shape: as many blocks as the GPU holds at once, at most attn_max_grid.
 template <int KV, class S>
 cudaError_t launch_shape(const AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
     static LaunchCache lc;
@@ -1340,8 +1374,8 @@ cudaError_t launch_shape(const AttnArgs& a, const CUtensorMap& k, const CUtensor
     auto kernel = attn_decode_kernel<KV, S>;
     e = cached_dyn_smem(lc, kernel, S::kSmem);
     if (e != cudaSuccess) return e;
-    const int want = sms * S::kMinBlocks;
-    return launch_overlapped(kernel, want < kAttnMaxGrid ? want : kAttnMaxGrid, S::kThreads, S::kSmem, s, a, k, v);
+    const int want = sms * S::kMinBlocks, most = attn_max_grid(S::kMinBlocks);
+    return launch_overlapped(kernel, want < most ? want : most, S::kThreads, S::kSmem, s, a, k, v);
 }
 
 template <int KV, int D>

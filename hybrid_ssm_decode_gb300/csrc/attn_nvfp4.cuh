@@ -10,7 +10,8 @@
 //      exchanged); the scale at 8 D + (t%8) D/8 + (b/2%4) D/32 + (t/8) D/64 + (b%2) + 2 (b/8),
 //      heads of 64: 8 D + (t%8) 8 + 2 b + t/8.
 //   V  codes at 4 D (t/8) + 64 b + 8 (t%8), heads of 64: 4 D (t/8) + 64 b + 4 (t%8), the
-//      second half of the block 32 further on; the scale at 8 D + 16 b + 4 (t%8/2) + 2 (t/8) + t%2.
+//      second half of the block 32 further on, a byte's two codes exchanged for odd t; the
+//      scale at 8 D + 16 b + 4 (t%8/2) + 2 (t/8) + t%2.
 //
 // The products. Scores are made as K Q^T and outputs as V^T P^T, 16 tokens or 16
 // channels by 8 query rows: with few rows (8 or less is the common case) the matrix
@@ -20,7 +21,7 @@
 // Two codes cost a conversion and a multiplication, 51 cycles a group of an SM at the
 // rate measured for the pair (10 words of 8 codes a cycle), half of the 98 that the
 // group's bytes take at the bandwidth of a copy. What a widened fragment costs beside
-// that is kept low: the interleaving of two tokens' V codes is four instructions for
+// that is kept low: the interleaving of two tokens' V codes is two instructions for
 // 16 codes, a lane's channels of V all belong to one block, so that a pair of scales
 // serves 16 fragments, and the running maximum is looked at by a vote before the lanes
 // that share a row exchange theirs.
@@ -44,40 +45,47 @@ __host__ __device__ __forceinline__ int nvfp4_scale_at(int D, int t, int b) {
     return 8 * D + (t & 7) * (D / 8) + ((b >> 1) & 3) * (D / 32) + (t >> 3) * (D / 64) + (b & 1) + 2 * (b >> 3);
 }
 
+// A token's V codes as they are stored, and back.
+__device__ __forceinline__ uint32_t nvfp4_exchanged(uint32_t c, int t) {
+    return (t & 1) ? ((c & 0x0F0F0F0Fu) << 4) | ((c >> 4) & 0x0F0F0F0Fu) : c;
+}
+
 namespace attn {
 
 // NR: tiles of 8 query rows that one warp takes.
 template <int D_, int NR_, int WM_>
 struct Shape4 {
     static constexpr int D = D_, NR = NR_, WM = WM_;
-    // Consumer warps per row group, and two blocks an SM where their registers fit. These
+    // Consumer warps per row group, and as many blocks an SM as their registers allow. These
     // are shared out per quarter of an SM: 8 warps leave 255 a thread, 12 leave 168 and 16
     // 128, producers included.
-    static constexpr int kMinBlocks = WM > 1 || (D == 256 && NR == 2) ? 1 : 2;
-    static constexpr int NT = WM == 4 ? (D == 256 ? 1 : 2) : WM == 2 ? 3 : D * NR <= 128 || kMinBlocks == 1 ? 7 : 5;
+    static constexpr int kMinBlocks = attn4_blocks(8 * NR * WM, D);
+    static constexpr int NT = WM == 4 ? (D == 256 ? 1 : 2) : WM == 2 ? 3 : kMinBlocks == 4 ? 2 : kMinBlocks == 1 ? 7 : 5;
+    static constexpr int kJoin = 32;
     static constexpr int kWarpRows = 8 * NR;
     static constexpr int kRows = kWarpRows * WM;
     static constexpr int kConsumers = WM * NT;
     static constexpr int kThreads = (kConsumers + 1) * 32;
     static constexpr int kQsz = 2;
+    // A slot holds two groups, which a warp takes together.
+    static constexpr int kSlotGroups = 2;
     static constexpr int kHalf = (9 * D + 127) / 128 * 128;   // copies begin on 128 bytes
-    static constexpr int kSlot = 2 * kHalf;
+    static constexpr int kSlot = 2 * kSlotGroups * kHalf;
     static constexpr int kCopied = 2 * 9 * D;
     static constexpr int QS = D * kQsz + 16;
     static constexpr int OS = D + 8;
-    static constexpr int kBudget = (kMinBlocks == 2 ? 113 : 226) * 1024 - 1024;
+    static constexpr int kBudget = (kMinBlocks == 4 ? 56 : kMinBlocks == 2 ? 113 : 226) * 1024 - 1024;
     static constexpr int fixed_bytes(int nb) {
         return 2 * kRows * QS + nb * kRows * OS * 4 + NT * kRows * 8 + kRows * 8 + 1024;
     }
-    static constexpr int NB = (kBudget - fixed_bytes(NT)) / kSlot >= 16 ? NT : 1;
+    static constexpr int NB = (kBudget - fixed_bytes(NT)) / kSlot >= 8 ? NT : 1;
     static constexpr int kFixed = fixed_bytes(NB);
     static constexpr int kSlotsFit = (kBudget - kFixed) / kSlot;
-    static constexpr int NS = (kSlotsFit > 48 ? 48 : kSlotsFit) / NT * NT;
-    static constexpr bool kPair = D * NR <= 128;         // two groups at a time
+    static constexpr int NS = (kSlotsFit > 24 ? 24 : kSlotsFit) / NT * NT;
+    static constexpr bool kPair = false;
     static constexpr int PB = 8;
-    static_assert(!kPair || NS - NT >= PB, "a pair of groups must fit the ring");
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
-    static_assert(NS >= NT && NS % NT == 0, "ring too small");
+    static_assert(NS >= NT && NS % NT == 0 && NS >= PB / kSlotGroups, "ring too small");
     static_assert(16 * NS + 32 + 8 + 2 * 48 <= 1024, "barriers and parts");
 };
 
@@ -118,7 +126,7 @@ struct Warp<kNVFP4, S> {
     static constexpr int kTiles = D / 16;        // of 16 channels, in the order in which V's words hold them
     static constexpr int kLaneRows = 2 * NR;     // row x is 8 (x/2) + 2 c + x%2
     static constexpr float kUp = 15.f;           // weights, and l and o with them, are 2^kUp times as large
-    float o[NR][kTiles][4];      // channels of tile i: chan(i) in rows' pair [0..1], the next one in [2..3]
+    float o[NR][kTiles][4];      // of a tile's two channels of this lane: the rows' pair in [0..1] and in [2..3]
     float m[kLaneRows];          // largest score so far, before its multiplier; the same in all lanes of a row
     float base[kLaneRows];       // what weights are relative to: m, or 0 where that is -inf
     float l[kLaneRows];          // this lane's tokens only
@@ -188,18 +196,8 @@ struct Warp<kNVFP4, S> {
         }
     }
 
-    // The lane's K codes of tokens g and g + 8, and their block scales as two FP16 each.
-    __device__ __forceinline__ void keys(uint32_t k, uint32_t (&w)[2][kWords], uint32_t (&s)[2][(kWords + 1) / 2]) const {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint32_t row = k + (g + 8 * t) * (D / 2);
-            if constexpr (D == 64) {
-                lds<2>(w[t], row + 8 * c);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kWords; j += 4) lds<4>(*reinterpret_cast<uint32_t(*)[4]>(&w[t][j]), row + ((16 * c + 16 * j) ^ (D == 256 ? (g & 1) << 6 : 0)));
-            }
-        }
+    // K's block scales of tokens g and g + 8, as two FP16 each.
+    __device__ __forceinline__ void key_scales(uint32_t k, uint32_t (&s)[2][(kWords + 1) / 2]) const {
         const uint32_t at = k + 8 * D + lane * (D / 32);
         if constexpr (D == 64) {
             uint16_t b;
@@ -230,34 +228,44 @@ struct Warp<kNVFP4, S> {
     // group i, rows 8 n + 2 c, +1; before their multiplier.
     template <int NG>
     __device__ __forceinline__ void scores(const uint32_t (&kb)[NG], float (&s)[NG][NR][4]) const {
-        uint32_t w[NG][2][kWords], b[NG][2][(kWords + 1) / 2];
+        constexpr int kStep = D == 64 ? 2 : 4;               // words of a load
+        uint32_t b[NG][2][(kWords + 1) / 2];
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            keys(kb[i], w[i], b[i]);
+            key_scales(kb[i], b[i]);
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][n][j] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < kWords; ++j)
+        for (int j0 = 0; j0 < kWords; j0 += kStep) {
+            uint32_t w[NG][2][kStep];
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                uint32_t x[4], y[4];
-                widen(w[i][0][j], x);
-                widen(w[i][1][j], y);
+            for (int i = 0; i < NG; ++i)
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    x[h] = mul_h2(x[h], b[i][0][j / 2]);
-                    y[h] = mul_h2(y[h], b[i][1][j / 2]);
+                for (int t = 0; t < 2; ++t)
+                    lds<kStep>(w[i][t], kb[i] + (g + 8 * t) * (D / 2) + ((4 * kStep * c + 16 * j0) ^ (D == 256 ? (g & 1) << 6 : 0)));
+#pragma unroll
+            for (int j = 0; j < kStep; ++j)
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    uint32_t x[4], y[4];
+                    widen(w[i][0][j], x);
+                    widen(w[i][1][j], y);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        x[h] = mul_h2(x[h], b[i][0][(j0 + j) / 2]);
+                        y[h] = mul_h2(y[h], b[i][1][(j0 + j) / 2]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t a[4] = {x[2 * h], y[2 * h], x[2 * h + 1], y[2 * h + 1]};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma_f16(s[i][n], a, qf[n][2 * (j0 + j) + h][0], qf[n][2 * (j0 + j) + h][1]);
+                    }
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t a[4] = {x[2 * h], y[2 * h], x[2 * h + 1], y[2 * h + 1]};
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) mma_f16(s[i][n], a, qf[n][2 * j + h][0], qf[n][2 * j + h][1]);
-                }
-            }
+        }
     }
 
     // Running maximum and sum; the scores become weights 2^kUp times as large. A row's
@@ -303,61 +311,74 @@ struct Warp<kNVFP4, S> {
                 }
     }
 
-    // The weights of 16 tokens as the B operand.
+    // The weights of 16 tokens as the B operand; [1]: with neighbouring tokens exchanged.
     struct Weights {
-        uint32_t b[NR][2];
+        uint32_t b[2][NR][2];
     };
     __device__ __forceinline__ Weights weights(const float (&p)[NR][4]) const {
         Weights w;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) w.b[n][t] = transposed(pack_f16(p[n][2 * t], p[n][2 * t + 1]));
+            for (int t = 0; t < 2; ++t) {
+                w.b[0][n][t] = transposed(pack_f16(p[n][2 * t], p[n][2 * t + 1]));
+                w.b[1][n][t] = __byte_perm(w.b[0][n][t], 0, 0x1032);
+            }
         return w;
     }
 
     // V as the A operand, tile after tile, through f(tile, a): registers 0 and 1 hold
-    // tokens 2 c, +1 of a tile's even and odd channel, 2 and 3 tokens 2 c + 8, +9.
+    // tokens 2 c, +1 of the tile's two channels of this lane, 2 and 3 tokens 2 c + 8, +9.
+    // A byte of the interleaved words is one channel of two tokens: even channels of even
+    // tokens and (exchanged as they are stored) of odd ones share a nibble's place with
+    // each other's, so that one selection interleaves eight codes. Odd channels then come
+    // with their tokens exchanged: odd tiles, for the weights' second form.
     template <class F>
     __device__ __forceinline__ void each_value(uint32_t v, F f) const {
         constexpr int kSets = D == 256 ? 2 : 1, kW = D == 64 ? 1 : 2;   // blocks of a lane; words of a token's block
+        constexpr uint32_t kLow = 0x0F0F0F0Fu;
 #pragma unroll
         for (int j = 0; j < kSets; ++j) {
-            uint32_t w[2][2 * kW], s[2];
+            uint32_t w[2][2 * kW], s[2][2];
             const uint32_t b = lds32(v + 8 * D + (D == 64 ? (lane >> 3) * 16 + c * 4 : j * 128 + lane * 4));
-            s[0] = e4m3x2_to_h2(b);
-            s[1] = e4m3x2_to_h2(b >> 16);
+            s[0][0] = e4m3x2_to_h2(b);
+            s[0][1] = e4m3x2_to_h2(b >> 16);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) lds<2 * kW>(w[h], v + 4 * D * h + 512 * j + lane * (8 * kW));
+            for (int h = 0; h < 2; ++h) {
+                s[1][h] = __byte_perm(s[0][h], 0, 0x1032);
+                lds<2 * kW>(w[h], v + 4 * D * h + 512 * j + lane * (8 * kW));
+            }
 #pragma unroll
             for (int k = 0; k < kW; ++k) {
-                uint32_t even[2][4], odd[2][4];
+                uint32_t r[2][2][4];                             // [odd channels][half][channel of four]
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t x = w[h][k], y = w[h][kW + k];     // tokens 2 c and 2 c + 1
-                    widen((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), even[h]);
-                    widen(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), odd[h]);
+                    widen((x & kLow) | (y & ~kLow), r[0][h]);
+                    widen((x & ~kLow) | (y & kLow), r[1][h]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        even[h][i] = mul_h2(even[h][i], s[h]);
-                        odd[h][i] = mul_h2(odd[h][i], s[h]);
+                        r[0][h][i] = mul_h2(r[0][h][i], s[0][h]);
+                        r[1][h][i] = mul_h2(r[1][h][i], s[1][h]);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t a[4] = {even[0][i], odd[0][i], even[1][i], odd[1][i]};
+                    const int odd = i & 1, e = 2 * (i >> 1);
+                    const uint32_t a[4] = {r[odd][0][e], r[odd][0][e + 1], r[odd][1][e], r[odd][1][e + 1]};
                     f(8 * j + 4 * k + i, a);
                 }
             }
         }
     }
-    // The first of a tile's two channels of this lane.
+    // The lane's channels of tiles i (even) and i + 1: from here on, tile i's first, tile
+    // i + 1's first, and their second ones.
     __device__ __forceinline__ int chan(int i) const { return D == 64 ? 8 * g + 2 * i : 16 * (g + 8 * (i >> 3)) + 2 * (i & 7); }
 
     __device__ __forceinline__ void accumulate(uint32_t vb, const Weights& w) {
         each_value(vb, [&](int i, const uint32_t (&a)[4]) {
 #pragma unroll
-            for (int n = 0; n < NR; ++n) mma_f16(o[n][i], a, w.b[n][0], w.b[n][1]);
+            for (int n = 0; n < NR; ++n) mma_f16(o[n][i], a, w.b[i & 1][n][0], w.b[i & 1][n][1]);
         });
     }
 
@@ -372,9 +393,10 @@ struct Warp<kNVFP4, S> {
     }
 
     // A register of two tokens' values with the tokens outside [lo, hi] set to zero bits.
-    __device__ __forceinline__ uint32_t cut(uint32_t v, int half, int lo, int hi) const {
-        const int t = half * 8 + 2 * c;
-        return v & ((t >= lo && t <= hi ? 0x0000FFFFu : 0u) | (t + 1 >= lo && t + 1 <= hi ? 0xFFFF0000u : 0u));
+    __device__ __forceinline__ uint32_t cut(uint32_t v, int tile, int half, int lo, int hi) const {
+        const int t = half * 8 + 2 * c, u = t + (tile & 1);
+        const int w = t + 1 - (tile & 1);
+        return v & ((u >= lo && u <= hi ? 0x0000FFFFu : 0u) | (w >= lo && w <= hi ? 0xFFFF0000u : 0u));
     }
 
     // One group of which row x of the lane sees the tokens lo[x]..hi[x] (0..15) and some
@@ -396,7 +418,7 @@ struct Warp<kNVFP4, S> {
         softmax(s);
         const Weights w = weights(s[0]);
         bool bad = false;
-        if (T > 1) {
+        if (T > 1 && (max(any_lo, 0) < all_lo || min(any_hi, kAttnGroup - 1) > all_hi)) {
             // the tokens that some drafts see and others do not: a value is finite unless
             // its block's scale is NaN
             for (int i = lane; i < kAttnGroup * (D / 16); i += 32) {
@@ -410,10 +432,10 @@ struct Warp<kNVFP4, S> {
         }
         if (!bad) {
             each_value(vb, [&](int i, const uint32_t (&a)[4]) {
-                const uint32_t x[4] = {cut(a[0], 0, any_lo, any_hi), cut(a[1], 0, any_lo, any_hi),
-                                       cut(a[2], 1, any_lo, any_hi), cut(a[3], 1, any_lo, any_hi)};
+                const uint32_t x[4] = {cut(a[0], i, 0, any_lo, any_hi), cut(a[1], i, 0, any_lo, any_hi),
+                                       cut(a[2], i, 1, any_lo, any_hi), cut(a[3], i, 1, any_lo, any_hi)};
 #pragma unroll
-                for (int n = 0; n < NR; ++n) mma_f16(o[n][i], x, w.b[n][0], w.b[n][1]);
+                for (int n = 0; n < NR; ++n) mma_f16(o[n][i], x, w.b[i & 1][n][0], w.b[i & 1][n][1]);
             });
             return;
         }
@@ -423,11 +445,11 @@ struct Warp<kNVFP4, S> {
             const int p = len - T + t;
             const int a0 = window_start(p, window) - tok0, a1 = p - tok0;
             each_value(vb, [&](int i, const uint32_t (&a)[4]) {
-                const uint32_t x[4] = {cut(a[0], 0, a0, a1), cut(a[1], 0, a0, a1), cut(a[2], 1, a0, a1), cut(a[3], 1, a0, a1)};
+                const uint32_t x[4] = {cut(a[0], i, 0, a0, a1), cut(a[1], i, 0, a0, a1), cut(a[2], i, 1, a0, a1), cut(a[3], i, 1, a0, a1)};
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(acc, x, w.b[n][0], w.b[n][1]);
+                    mma_f16(acc, x, w.b[i & 1][n][0], w.b[i & 1][n][1]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (draft[2 * n + (j & 1)] == t) o[n][i][j] += acc[j];
@@ -447,7 +469,7 @@ struct Warp<kNVFP4, S> {
                 for (int i = 0; i < kTiles; i += 2) {
                     float4* p = reinterpret_cast<float4*>(to + (8 * n + 2 * c + e) * S::OS + chan(i));
                     const float fx = f[2 * n + e];
-                    float4 v = make_float4(o[n][i][e] * fx, o[n][i][2 + e] * fx, o[n][i + 1][e] * fx, o[n][i + 1][2 + e] * fx);
+                    float4 v = make_float4(o[n][i][e] * fx, o[n][i + 1][e] * fx, o[n][i][2 + e] * fx, o[n][i + 1][2 + e] * fx);
                     if (kAdd) v.x += p->x, v.y += p->y, v.z += p->z, v.w += p->w;
                     *p = v;
                 }

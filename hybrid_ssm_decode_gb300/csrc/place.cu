@@ -369,6 +369,7 @@ __device__ __forceinline__ void store_block(const PlaceArgs& a, const float (&x)
         const int t = in_page % kAttnGroup;
         uint32_t c[2];
         const uint8_t s = quantise16(x, scales[head], c);
+        if (V) c[0] = nvfp4_exchanged(c[0], t), c[1] = nvfp4_exchanged(c[1], t);
         char* to = at + nvfp4_codes_at<V>(a.dim, t, b);
         if (V && a.dim == 64) {
             *reinterpret_cast<uint32_t*>(to) = c[0];
@@ -405,6 +406,7 @@ __device__ __forceinline__ void fetch_block(const PlaceArgs& a, float (&x)[16], 
         } else {
             c = *reinterpret_cast<const uint2*>(from);
         }
+        if (V) c.x = nvfp4_exchanged(c.x, t), c.y = nvfp4_exchanged(c.y, t);
         const float s = __fmul_rn(e4m3_to_f(*reinterpret_cast<const uint8_t*>(at + nvfp4_scale_at<V>(a.dim, t, b))), scales[head]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
