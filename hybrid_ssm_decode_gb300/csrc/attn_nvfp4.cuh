@@ -83,6 +83,7 @@ struct Shape4 {
     static constexpr int kSlotsFit = (kBudget - kFixed) / kSlot;
     static constexpr int NS = (kSlotsFit > 24 ? 24 : kSlotsFit) / NT * NT;
     static constexpr bool kPair = false;
+    static constexpr bool kTogether = D * NR <= 128;     // the scores of a slot's groups, product by product
     static constexpr int PB = 8;
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
     static_assert(NS >= NT && NS % NT == 0 && NS >= PB / kSlotGroups, "ring too small");
@@ -125,10 +126,15 @@ struct Warp<kNVFP4, S> {
     static constexpr int kWords = D / 32;        // of K codes, per lane and token
     static constexpr int kTiles = D / 16;        // of 16 channels, in the order in which V's words hold them
     static constexpr int kLaneRows = 2 * NR;     // row x is 8 (x/2) + 2 c + x%2
-    static constexpr float kUp = 15.f;           // weights, and l and o with them, are 2^kUp times as large
+    // Weights, and l and o with them, are 2^kUp times as large, and relative to a score
+    // that the row's largest may pass by kSlack before all is rescaled: they stay
+    // below 2^15. Rescaling at every new maximum took a rescale in two of three steps
+    // where 16 rows run over some thousands of tokens. Weights below 2^-26 of that
+    // score lose some of FP16's bits, and those below 2^-37 vanish.
+    static constexpr float kUp = 12.f, kSlack = 3.f;
     float o[NR][kTiles][4];      // of a tile's two channels of this lane: the rows' pair in [0..1] and in [2..3]
-    float m[kLaneRows];          // largest score so far, before its multiplier; the same in all lanes of a row
-    float base[kLaneRows];       // what weights are relative to: m, or 0 where that is -inf
+    float base[kLaneRows];       // the score, before its multiplier, that weights are relative to; the same in all lanes of a row
+    float most[kLaneRows];       // scores up to here need no other; -inf before the first
     float l[kLaneRows];          // this lane's tokens only
     uint32_t qf[NR][2 * kWords][2];
     float mul[kLaneRows];        // score multiplier, > 0
@@ -141,7 +147,7 @@ struct Warp<kNVFP4, S> {
     }
     __device__ __forceinline__ bool speaks() const { return g == 0; }
     // The maximum under which row x's sums stand: rounded, the same wherever it is taken.
-    __device__ __forceinline__ float top(int x) const { return __fmul_rn(m[x], mul[x]); }
+    __device__ __forceinline__ float top(int x) const { return most[x] == -INFINITY ? -INFINITY : __fmul_rn(base[x], mul[x]); }
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -152,7 +158,7 @@ struct Warp<kNVFP4, S> {
                 for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
 #pragma unroll
         for (int x = 0; x < kLaneRows; ++x) {
-            m[x] = -INFINITY;
+            most[x] = -INFINITY;
             base[x] = 0.f;
             l[x] = 0.f;
         }
@@ -196,8 +202,8 @@ struct Warp<kNVFP4, S> {
         }
     }
 
-    // K's block scales of tokens g and g + 8, as two FP16 each.
-    __device__ __forceinline__ void key_scales(uint32_t k, uint32_t (&s)[2][(kWords + 1) / 2]) const {
+    // K's block scales of tokens g and g + 8 for the words from 4 x on, as two FP16 each.
+    __device__ __forceinline__ void key_scales(uint32_t k, int x, uint32_t (&s)[2][2]) const {
         const uint32_t at = k + 8 * D + lane * (D / 32);
         if constexpr (D == 64) {
             uint16_t b;
@@ -208,19 +214,17 @@ struct Warp<kNVFP4, S> {
         } else {
             uint32_t b[2];
             if constexpr (D == 128) {
-                const uint32_t x = lds32(at);
-                b[0] = x & 0xFFFF, b[1] = x >> 16;
+                b[0] = lds32(at);
+                b[1] = b[0] >> 16;
             } else {
                 lds<2>(b, at);
             }
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int j = 0; j < kWords / 4; ++j) {
-                    const uint32_t h = e4m3x2_to_h2(b[t] >> (16 * j));
-                    s[t][2 * j] = __byte_perm(h, h, 0x1010);
-                    s[t][2 * j + 1] = __byte_perm(h, h, 0x3232);
-                }
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t h = e4m3x2_to_h2(b[t] >> (16 * x));
+                s[t][0] = __byte_perm(h, h, 0x1010);
+                s[t][1] = __byte_perm(h, h, 0x3232);
+            }
         }
     }
 
@@ -229,23 +233,22 @@ struct Warp<kNVFP4, S> {
     template <int NG>
     __device__ __forceinline__ void scores(const uint32_t (&kb)[NG], float (&s)[NG][NR][4]) const {
         constexpr int kStep = D == 64 ? 2 : 4;               // words of a load
-        uint32_t b[NG][2][(kWords + 1) / 2];
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            key_scales(kb[i], b[i]);
+        for (int i = 0; i < NG; ++i)
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][n][j] = 0.f;
-        }
 #pragma unroll
         for (int j0 = 0; j0 < kWords; j0 += kStep) {
-            uint32_t w[NG][2][kStep];
+            uint32_t w[NG][2][kStep], b[NG][2][2];
 #pragma unroll
-            for (int i = 0; i < NG; ++i)
+            for (int i = 0; i < NG; ++i) {
+                key_scales(kb[i], j0 / 4, b[i]);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     lds<kStep>(w[i][t], kb[i] + (g + 8 * t) * (D / 2) + ((4 * kStep * c + 16 * j0) ^ (D == 256 ? (g & 1) << 6 : 0)));
+            }
 #pragma unroll
             for (int j = 0; j < kStep; ++j)
 #pragma unroll
@@ -255,8 +258,8 @@ struct Warp<kNVFP4, S> {
                     widen(w[i][1][j], y);
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        x[h] = mul_h2(x[h], b[i][0][(j0 + j) / 2]);
-                        y[h] = mul_h2(y[h], b[i][1][(j0 + j) / 2]);
+                        x[h] = mul_h2(x[h], b[i][0][j / 2]);
+                        y[h] = mul_h2(y[h], b[i][1][j / 2]);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -268,27 +271,28 @@ struct Warp<kNVFP4, S> {
         }
     }
 
-    // Running maximum and sum; the scores become weights 2^kUp times as large. A row's
-    // lanes exchange their maxima only where some lane's passes what is known.
+    // Running sum under a maximum; the scores become weights. A row's lanes exchange their
+    // maxima, and all is rescaled, only where some lane's score passes what is allowed.
     template <int NG>
     __device__ __forceinline__ void softmax(float (&s)[NG][NR][4]) {
         float mx[kLaneRows];
         bool more = false;
 #pragma unroll
         for (int x = 0; x < kLaneRows; ++x) {
-            mx[x] = m[x];
+            mx[x] = fmaxf(s[0][x >> 1][x & 1], s[0][x >> 1][2 + (x & 1)]);
 #pragma unroll
-            for (int i = 0; i < NG; ++i) mx[x] = fmaxf(mx[x], fmaxf(s[i][x >> 1][x & 1], s[i][x >> 1][2 + (x & 1)]));
-            more = more || mx[x] > m[x];
+            for (int i = 1; i < NG; ++i) mx[x] = fmaxf(mx[x], fmaxf(s[i][x >> 1][x & 1], s[i][x >> 1][2 + (x & 1)]));
+            more = more || mx[x] > most[x];
         }
         if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
             for (int x = 0; x < kLaneRows; ++x) {
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], d));
-                const float to = mx[x] == -INFINITY ? 0.f : mx[x];
-                const float f = ex2((m[x] - to) * mul[x]);
-                m[x] = mx[x];
+                const bool up = mx[x] > most[x];
+                const float to = up ? mx[x] : base[x];
+                const float f = most[x] == -INFINITY ? 0.f : ex2((base[x] - to) * mul[x]);
+                if (up) most[x] = to + kSlack / mul[x];
                 base[x] = to;
                 l[x] *= f;
 #pragma unroll
@@ -386,7 +390,13 @@ struct Warp<kNVFP4, S> {
     template <int NG>
     __device__ __forceinline__ void step(const uint32_t (&kb)[NG], const uint32_t (&vb)[NG]) {
         float s[NG][NR][4];
-        scores(kb, s);
+        if constexpr (S::kTogether) {
+            scores(kb, s);
+        } else {
+            // one after the other: their codes and scales side by side do not fit the registers
+#pragma unroll
+            for (int i = 0; i < NG; ++i) scores(*reinterpret_cast<const uint32_t(*)[1]>(&kb[i]), *reinterpret_cast<float(*)[1][NR][4]>(&s[i]));
+        }
         softmax(s);
 #pragma unroll
         for (int i = 0; i < NG; ++i) accumulate(vb[i], weights(s[i]));
