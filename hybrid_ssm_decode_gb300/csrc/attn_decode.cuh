@@ -77,6 +77,8 @@ struct Shape {
     static constexpr int kHalf = kAttnGroup * RB;        // K (or V) of a slot
     static constexpr int kSlot = 2 * kHalf;
     static constexpr int kSlotGroups = 1;                // groups in a slot
+    static constexpr int DS = 1;                         // warps that share a slot's channels (attn_nvfp4.cuh)
+    static constexpr int kShared = 0;                    // bytes in which they exchange scores
     static constexpr int kJoin = 16;                     // parts joined at a time
     static constexpr int kCopied = 2 * kHalf;            // bytes that the copies of a group bring
     static constexpr int QS = D * kQsz + 16;             // bytes from one query row to the next
@@ -1010,12 +1012,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     volatile int* dead = reinterpret_cast<volatile int*>(qempty + 2);
     volatile int* s_last = dead + 1;
     Part* s_part = reinterpret_cast<Part*>(const_cast<int*>(dead + 2));  // [2]
+    [[maybe_unused]] char* shared = smem + S::kSmem - 1024 - S::kShared;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, S::WM);
+            mbar_init(empty + i, S::WM * S::DS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(qfull + i, 1);
@@ -1177,12 +1180,14 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
 
     // ---- consumers ----
     constexpr int kThreads = S::kConsumers * 32;
-    const int wm = warp / S::NT, wt = warp % S::NT;
+    const int wm = warp / (S::NT * S::DS), wt = warp / S::DS % S::NT;
     constexpr int kLaneRows = Warp<KV, S>::kLaneRows;
     Warp<KV, S> wp;
     wp.lane = lane;
     wp.g = lane >> 2;
     wp.c = lane & 3;
+    if constexpr (S::DS > 1) wp.pair_up(warp, shared);
+    const bool speaks = wp.speaks() && warp % S::DS == 0;
     // The part that went to the workspace last: its arrival is counted while the
     // next part runs (one thread waits for the writes and the count, not the
     // block), and if it was the request's last, it is joined after that part.
@@ -1259,6 +1264,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             const uint32_t kb = smem_u32(slots + s * S::kSlot), vb = kb + S::kHalf;
             uint64_t* const done = empty + s;
             bool ok = wait_phase(full + s, tn & 1, dead, a.err);
+            if (S::DS > 1) ok = true;      // the warps of a pair meet at barriers: both go on, whatever one of them saw
             if constexpr (S::kSlotGroups == 2) {
                 const int i = 2 * k;
                 if (ok && i >= f0 && i + 2 <= min(f1, ng)) {
@@ -1302,7 +1308,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
 #pragma unroll
         for (int x = 0; x < kLaneRows; ++x) {
             wp.join_columns(x);
-            if (wp.speaks()) s_ml[wt * S::kRows + wm * S::kWarpRows + wp.row(x)] = make_float2(wp.top(x), wp.l[x]);
+            if (speaks) s_ml[wt * S::kRows + wm * S::kWarpRows + wp.row(x)] = make_float2(wp.top(x), wp.l[x]);
         }
         named_sync(1, kThreads);
         float f[kLaneRows];
@@ -1316,7 +1322,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
 #pragma unroll
             for (int w = 0; w < S::NT; ++w) L += s_ml[w * S::kRows + r].y * ex2(s_ml[w * S::kRows + r].x - ref);
             f[x] = ex2(wp.top(x) - ref);
-            if (wt == 0 && wp.speaks()) s_row[r] = make_float2(M, L);
+            if (wt == 0 && speaks) s_row[r] = make_float2(M, L);
         }
         // warp w into buffer w % NB, those of later rounds adding to it
 #pragma unroll 1

@@ -52,19 +52,26 @@ __device__ __forceinline__ uint32_t nvfp4_exchanged(uint32_t c, int t) {
 
 namespace attn {
 
-// NR: tiles of 8 query rows that one warp takes.
+// NR: tiles of 8 query rows that one warp takes. DS: warps that share the channels of a
+// slot's tokens. Heads of 256 are shared by two: each makes the scores of its half of
+// the channels, they exchange and add them, and each then takes its half of the
+// outputs. One warp alone has 64 registers of outputs and 32 of queries for 8 rows,
+// and twice that for 16, which spilled.
 template <int D_, int NR_, int WM_>
 struct Shape4 {
-    static constexpr int D = D_, NR = NR_, WM = WM_;
+    static constexpr int D = D_, NR = NR_, WM = WM_, DS = D == 256 ? 2 : 1;
     // Consumer warps per row group, and as many blocks an SM as their registers allow. These
     // are shared out per quarter of an SM: 8 warps leave 255 a thread, 12 leave 168 and 16
     // 128, producers included.
     static constexpr int kMinBlocks = attn4_blocks(8 * NR * WM, D);
-    static constexpr int NT = WM == 4 ? (D == 256 ? 1 : 2) : WM == 2 ? 3 : kMinBlocks == 4 ? 2 : kMinBlocks == 1 ? 7 : 5;
+    static constexpr int NT = D == 256 ? (kMinBlocks == 2 ? 2 : WM >= 2 ? 1 : 3)
+                            : WM == 4 ? 2 : WM == 2 ? 3 : kMinBlocks == 4 ? 2 : kMinBlocks == 1 ? 7 : 5;
     static constexpr int kJoin = 32;
     static constexpr int kWarpRows = 8 * NR;
+    static constexpr int kSlotScores = 2 * NR * 4 * 32 * 4;   // bytes of a slot's scores, as one warp holds them
     static constexpr int kRows = kWarpRows * WM;
-    static constexpr int kConsumers = WM * NT;
+    static constexpr int kConsumers = WM * NT * DS;
+    static constexpr int kShared = DS == 1 ? 0 : WM * NT * 2 * 2 * kSlotScores;   // [pair][turn][half]
     static constexpr int kThreads = (kConsumers + 1) * 32;
     static constexpr int kQsz = 2;
     // A slot holds two groups, which a warp takes together.
@@ -76,14 +83,14 @@ struct Shape4 {
     static constexpr int OS = D + 8;
     static constexpr int kBudget = (kMinBlocks == 4 ? 56 : kMinBlocks == 2 ? 113 : 226) * 1024 - 1024;
     static constexpr int fixed_bytes(int nb) {
-        return 2 * kRows * QS + nb * kRows * OS * 4 + NT * kRows * 8 + kRows * 8 + 1024;
+        return 2 * kRows * QS + nb * kRows * OS * 4 + NT * kRows * 8 + kRows * 8 + 1024 + kShared;
     }
     static constexpr int NB = (kBudget - fixed_bytes(NT)) / kSlot >= 8 ? NT : 1;
     static constexpr int kFixed = fixed_bytes(NB);
     static constexpr int kSlotsFit = (kBudget - kFixed) / kSlot;
     static constexpr int NS = (kSlotsFit > 24 ? 24 : kSlotsFit) / NT * NT;
     static constexpr bool kPair = false;
-    static constexpr bool kTogether = D * NR <= 128;     // the scores of a slot's groups, product by product
+    static constexpr bool kTogether = D / DS * NR <= 128;     // the scores of a slot's groups, product by product
     static constexpr int PB = 8;
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
     static_assert(NS >= NT && NS % NT == 0 && NS >= PB / kSlotGroups, "ring too small");
@@ -123,8 +130,8 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
 template <class S>
 struct Warp<kNVFP4, S> {
     static constexpr int D = S::D, NR = S::NR;
-    static constexpr int kWords = D / 32;        // of K codes, per lane and token
-    static constexpr int kTiles = D / 16;        // of 16 channels, in the order in which V's words hold them
+    static constexpr int kWords = D / S::DS / 32;   // of K codes, per lane and token
+    static constexpr int kTiles = D / S::DS / 16;   // of 16 channels, in the order in which V's words hold them
     static constexpr int kLaneRows = 2 * NR;     // row x is 8 (x/2) + 2 c + x%2
     // Weights, and l and o with them, are 2^kUp times as large, and relative to a score
     // that the row's largest may pass by kSlack before all is rescaled: they stay
@@ -139,6 +146,37 @@ struct Warp<kNVFP4, S> {
     uint32_t qf[NR][2 * kWords][2];
     float mul[kLaneRows];        // score multiplier, > 0
     int lane, g, c;
+    int half = 0, pair = 0, turn = 0;   // of a pair's two warps; the pair; of its two exchange buffers
+    char* shared = nullptr;
+
+    // The warp's place in its pair, and where the two exchange their scores.
+    __device__ __forceinline__ void pair_up(int warp, char* buffers) {
+        half = warp & 1;
+        pair = warp >> 1;
+        shared = buffers + pair * 4 * S::kSlotScores;
+    }
+    // The sum of both warps' scores. A buffer is written again two exchanges later, behind
+    // the barrier of the one between them, which the other warp passes after its reads.
+    template <int NG>
+    __device__ __forceinline__ void exchange(float (&s)[NG][NR][4]) {
+        if constexpr (S::DS == 2) {
+            float4* mine = reinterpret_cast<float4*>(shared + (2 * turn + half) * S::kSlotScores) + lane;
+            const float4* other = reinterpret_cast<const float4*>(shared + (2 * turn + 1 - half) * S::kSlotScores) + lane;
+            turn ^= 1;
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mine[(i * NR + n) * 32] = make_float4(s[i][n][0], s[i][n][1], s[i][n][2], s[i][n][3]);
+            named_sync(3 + pair, 64);
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    const float4 v = other[(i * NR + n) * 32];
+                    s[i][n][0] += v.x, s[i][n][1] += v.y, s[i][n][2] += v.z, s[i][n][3] += v.w;
+                }
+        }
+    }
 
     __device__ __forceinline__ int row(int x) const { return 8 * (x >> 1) + 2 * c + (x & 1); }
     __device__ __forceinline__ void join_columns(int x) {
@@ -165,7 +203,7 @@ struct Warp<kNVFP4, S> {
     }
 
     // The lane's channels of a K row: word j holds 8 from here on.
-    __device__ __forceinline__ int channel(int j) const { return D == 64 ? 16 * c + 8 * j : 32 * c + 8 * (j & 3) + 128 * (j >> 2); }
+    __device__ __forceinline__ int channel(int j) const { return D == 64 ? 16 * c + 8 * j : 32 * c + 8 * j + 128 * half; }
 
     // Query rows as the B operand, scaled as for FP8 caches: each by a power of two so
     // that its largest finite value lies in [2^14, 2^15).
@@ -175,10 +213,10 @@ struct Warp<kNVFP4, S> {
             const char* q = rows + (8 * n + g) * S::QS;
             float mx = 0.f;
 #pragma unroll
-            for (int j = 0; j < kWords; ++j)
+            for (int j = 0; j < kWords * S::DS; ++j)          // both halves: the row has one factor
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float4 v = load4(reinterpret_cast<const __nv_bfloat16*>(q) + channel(j) + 4 * h);
+                    const float4 v = load4(reinterpret_cast<const __nv_bfloat16*>(q) + (channel(j % kWords) ^ (j / kWords * 128)) + 4 * h);
                     for (const float x : {v.x, v.y, v.z, v.w}) mx = fabsf(x) < INFINITY ? fmaxf(mx, fabsf(x)) : mx;
                 }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -202,8 +240,8 @@ struct Warp<kNVFP4, S> {
         }
     }
 
-    // K's block scales of tokens g and g + 8 for the words from 4 x on, as two FP16 each.
-    __device__ __forceinline__ void key_scales(uint32_t k, int x, uint32_t (&s)[2][2]) const {
+    // K's block scales of tokens g and g + 8, as two FP16 each.
+    __device__ __forceinline__ void key_scales(uint32_t k, uint32_t (&s)[2][2]) const {
         const uint32_t at = k + 8 * D + lane * (D / 32);
         if constexpr (D == 64) {
             uint16_t b;
@@ -221,7 +259,7 @@ struct Warp<kNVFP4, S> {
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const uint32_t h = e4m3x2_to_h2(b[t] >> (16 * x));
+                const uint32_t h = e4m3x2_to_h2(b[t] >> (16 * half));
                 s[t][0] = __byte_perm(h, h, 0x1010);
                 s[t][1] = __byte_perm(h, h, 0x3232);
             }
@@ -232,43 +270,37 @@ struct Warp<kNVFP4, S> {
     // group i, rows 8 n + 2 c, +1; before their multiplier.
     template <int NG>
     __device__ __forceinline__ void scores(const uint32_t (&kb)[NG], float (&s)[NG][NR][4]) const {
-        constexpr int kStep = D == 64 ? 2 : 4;               // words of a load
+        uint32_t w[NG][2][kWords], b[NG][2][2];
 #pragma unroll
-        for (int i = 0; i < NG; ++i)
+        for (int i = 0; i < NG; ++i) {
+            key_scales(kb[i], b[i]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                lds<kWords>(w[i][t], kb[i] + (g + 8 * t) * (D / 2) + ((4 * kWords * c) ^ (D == 256 ? ((g & 1) ^ half) << 6 : 0)));
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][n][j] = 0.f;
+        }
 #pragma unroll
-        for (int j0 = 0; j0 < kWords; j0 += kStep) {
-            uint32_t w[NG][2][kStep], b[NG][2][2];
+        for (int j = 0; j < kWords; ++j)
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                key_scales(kb[i], j0 / 4, b[i]);
+                uint32_t x[4], y[4];
+                widen(w[i][0][j], x);
+                widen(w[i][1][j], y);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    lds<kStep>(w[i][t], kb[i] + (g + 8 * t) * (D / 2) + ((4 * kStep * c + 16 * j0) ^ (D == 256 ? (g & 1) << 6 : 0)));
-            }
-#pragma unroll
-            for (int j = 0; j < kStep; ++j)
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    uint32_t x[4], y[4];
-                    widen(w[i][0][j], x);
-                    widen(w[i][1][j], y);
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        x[h] = mul_h2(x[h], b[i][0][j / 2]);
-                        y[h] = mul_h2(y[h], b[i][1][j / 2]);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t a[4] = {x[2 * h], y[2 * h], x[2 * h + 1], y[2 * h + 1]};
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) mma_f16(s[i][n], a, qf[n][2 * (j0 + j) + h][0], qf[n][2 * (j0 + j) + h][1]);
-                    }
+                for (int h = 0; h < 4; ++h) {
+                    x[h] = mul_h2(x[h], b[i][0][j / 2]);
+                    y[h] = mul_h2(y[h], b[i][1][j / 2]);
                 }
-        }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a[4] = {x[2 * h], y[2 * h], x[2 * h + 1], y[2 * h + 1]};
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) mma_f16(s[i][n], a, qf[n][2 * j + h][0], qf[n][2 * j + h][1]);
+                }
+            }
     }
 
     // Running sum under a maximum; the scores become weights. A row's lanes exchange their
@@ -339,18 +371,17 @@ struct Warp<kNVFP4, S> {
     // with their tokens exchanged: odd tiles, for the weights' second form.
     template <class F>
     __device__ __forceinline__ void each_value(uint32_t v, F f) const {
-        constexpr int kSets = D == 256 ? 2 : 1, kW = D == 64 ? 1 : 2;   // blocks of a lane; words of a token's block
+        constexpr int kW = D == 64 ? 1 : 2;                  // words of a token's block
         constexpr uint32_t kLow = 0x0F0F0F0Fu;
-#pragma unroll
-        for (int j = 0; j < kSets; ++j) {
+        {
             uint32_t w[2][2 * kW], s[2][2];
-            const uint32_t b = lds32(v + 8 * D + (D == 64 ? (lane >> 3) * 16 + c * 4 : j * 128 + lane * 4));
+            const uint32_t b = lds32(v + 8 * D + (D == 64 ? (lane >> 3) * 16 + c * 4 : half * 128 + lane * 4));
             s[0][0] = e4m3x2_to_h2(b);
             s[0][1] = e4m3x2_to_h2(b >> 16);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 s[1][h] = __byte_perm(s[0][h], 0, 0x1032);
-                lds<2 * kW>(w[h], v + 4 * D * h + 512 * j + lane * (8 * kW));
+                lds<2 * kW>(w[h], v + 4 * D * h + 512 * half + lane * (8 * kW));
             }
 #pragma unroll
             for (int k = 0; k < kW; ++k) {
@@ -370,14 +401,14 @@ struct Warp<kNVFP4, S> {
                 for (int i = 0; i < 4; ++i) {
                     const int odd = i & 1, e = 2 * (i >> 1);
                     const uint32_t a[4] = {r[odd][0][e], r[odd][0][e + 1], r[odd][1][e], r[odd][1][e + 1]};
-                    f(8 * j + 4 * k + i, a);
+                    f(4 * k + i, a);
                 }
             }
         }
     }
     // The lane's channels of tiles i (even) and i + 1: from here on, tile i's first, tile
     // i + 1's first, and their second ones.
-    __device__ __forceinline__ int chan(int i) const { return D == 64 ? 8 * g + 2 * i : 16 * (g + 8 * (i >> 3)) + 2 * (i & 7); }
+    __device__ __forceinline__ int chan(int i) const { return D == 64 ? 8 * g + 2 * i : 16 * (g + 8 * half) + 2 * i; }
 
     __device__ __forceinline__ void accumulate(uint32_t vb, const Weights& w) {
         each_value(vb, [&](int i, const uint32_t (&a)[4]) {
@@ -397,6 +428,7 @@ struct Warp<kNVFP4, S> {
 #pragma unroll
             for (int i = 0; i < NG; ++i) scores(*reinterpret_cast<const uint32_t(*)[1]>(&kb[i]), *reinterpret_cast<float(*)[1][NR][4]>(&s[i]));
         }
+        exchange(s);
         softmax(s);
 #pragma unroll
         for (int i = 0; i < NG; ++i) accumulate(vb[i], weights(s[i]));
@@ -418,6 +450,7 @@ struct Warp<kNVFP4, S> {
         float s[1][NR][4];
         const uint32_t k1[1] = {kb};
         scores(k1, s);
+        exchange(s);
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
