@@ -170,21 +170,24 @@ class HybridStack:
         u, n = add_norm(u, o)                  o: the layer before's output
         "M":  x, z, Bt, Ct, dt as in M2Stack;  y = SSM decode step
               o = gated_norm(y, z) W_out       normalised in G groups of d_inner
-        "A":  q, k, v = n W_qkv;  k, v to the requests' new slots of the cache
+        "A":  q, k, v = n W_qkv;  with rope: q, k rotated to the tokens' positions
+              k, v to the requests' new slots of the cache
               o = attention(q) W_o             over all tokens of the request
 
     All requests share one page table, which every attention layer's cache is
-    laid out by. kv: "bf16" or "fp8" (unit scales). The weights depend on `seed`
-    only. A request begins with no tokens.
+    laid out by. kv: "bf16", "fp8" or "nvfp4" (unit scales). rope: a Rope, or None
+    for no positions. The weights depend on `seed` only. A request begins with no
+    tokens.
     """
 
-    def __init__(self, shape: HybridShape, kv="bf16", seed=0, device="cuda"):
+    def __init__(self, shape: HybridShape, kv="bf16", seed=0, device="cuda", rope=None):
         import torch
         s = self.shape = shape
         if not s.pattern or set(s.pattern) - {"M", "A"}:
             raise ValueError(f"pattern: {s.pattern!r}, must be of M and A")
-        if kv not in ("bf16", "fp8"):
-            raise ValueError(f"kv: {kv!r}, must be bf16 or fp8")
+        if kv not in ("bf16", "fp8", "nvfp4"):
+            raise ValueError(f"kv: {kv!r}, must be bf16, fp8 or nvfp4")
+        self.rope = rope
         gen = torch.Generator(device=device)
         gen.manual_seed(2000 + seed)
 
@@ -215,9 +218,10 @@ class HybridStack:
             else:
                 w.update(qkv=weight(s.d_model, (s.q_heads + 2 * s.kv_heads) * s.attn_dim),
                          out=weight(s.q_heads * s.attn_dim, s.d_model))
-                dtype = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
-                cache = torch.zeros((s.num_pages, 2, s.kv_heads, s.page_size, s.attn_dim), dtype=dtype, device=device)
-                ones = torch.ones((s.kv_heads,), device=device) if kv == "fp8" else None
+                dtype = {"bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "nvfp4": torch.uint8}[kv]
+                row = s.attn_dim if kv != "nvfp4" else s.attn_dim // 2 + s.attn_dim // 16
+                cache = torch.zeros((s.num_pages, 2, s.kv_heads, s.page_size, row), dtype=dtype, device=device)
+                ones = torch.ones((s.kv_heads,), device=device) if kv != "bf16" else None
                 layer = Attention(cache[:, 0], cache[:, 1], batch=s.batch, q_heads=s.q_heads, max_pages=s.max_pages,
                                   max_draft=s.max_draft, window=s.window, k_scale=ones, v_scale=ones, workspace=workspace)
                 workspace = layer.workspace           # the layers run one after another: one workspace
@@ -242,7 +246,7 @@ class HybridStack:
 
             self.buffers[T] = {"u": new(f32, n, s.d_model), "n": new(bf16, n, s.d_model), "y": new(bf16, n, s.d_inner),
                                "g": new(bf16, n, s.d_inner), "o": new(bf16, s.batch, T, s.q_heads, s.attn_dim),
-                               "slots": new(torch.int32, n)}
+                               "slots": new(torch.int32, n), "positions": new(torch.int32, n)}
         return self.buffers[T]
 
     def step(self, u):
@@ -258,7 +262,7 @@ class HybridStack:
         T = 1 if u.dim() == 2 else u.shape[1]
         n_tok = s.batch * T
         b = self._buffers(T, u.device)
-        self.pages.extend(b["slots"], T=T)
+        self.pages.extend(b["slots"], T=T, positions=b["positions"] if self.rope else None)
         b["u"].copy_(u.reshape(n_tok, s.d_model))
         res, n, out = b["u"], b["n"], None
         for w, layer, kind in zip(self.weights, self.layers, s.pattern):
@@ -271,7 +275,10 @@ class HybridStack:
             else:
                 qkv = (n @ w["qkv"]).view(n_tok, s.q_heads + 2 * s.kv_heads, s.attn_dim)
                 q, k, v = qkv.split([s.q_heads, s.kv_heads, s.kv_heads], dim=1)
-                layer.append(k, v, b["slots"])
+                if self.rope:
+                    layer.append(k, v, b["slots"], rope=self.rope, positions=b["positions"], q=q, q_out=q)
+                else:
+                    layer.append(k, v, b["slots"])
                 layer.decode(b["o"], q, self.pages.lens, self.pages.table, T=T)
                 out = b["o"].view(n_tok, -1) @ w["out"]
         final = torch.empty_like(n)
