@@ -95,10 +95,6 @@ def _f64(*names):
     return [(n, ctypes.c_double) for n in names]
 
 
-def _ptr(*names):
-    return [(n, ctypes.c_void_p) for n in names]
-
-
 class PagesConfig(ctypes.Structure):
     _fields_ = _i32("batch", "page_size", "num_pages", "max_pages")
 
@@ -113,8 +109,7 @@ class AttnConfig(ctypes.Structure):
 
 
 class AttnRotary(ctypes.Structure):
-    _fields_ = (_i32("rotary_dim", "interleaved") + _f32("gain") + _ptr("d_turns", "d_positions", "d_q", "d_q_out")
-                + _i64("q_stride", "q_out_stride"))
+    _fields_ = _i32("rotary_dim", "interleaved") + _f32("gain") + _i64("q_stride", "q_out_stride")
 
 
 class RopeConfig(ctypes.Structure):
@@ -231,7 +226,7 @@ def load():
             "rssm_attn_workspace_size": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(sz)], i32),
             "rssm_attn_create": ([ctypes.POINTER(AttnConfig), p, p, p, p, p, sz, p, ctypes.POINTER(p)], i32),
             "rssm_attn_append": ([p, i32, p, i64, p, i64, p, p], i32),
-            "rssm_attn_append_rotary": ([p, i32, p, i64, p, i64, p, ctypes.POINTER(AttnRotary), p], i32),
+            "rssm_attn_append_rotary": ([p, i32, p, i64, p, i64, p, ctypes.POINTER(AttnRotary), p, p, p, p, p], i32),
             "rssm_attn_read": ([p, i32, p, p, i64, p, i64, p], i32),
             "rssm_attn_decode": ([p, i32, p, i64, p, p, p, p, p], i32),
             "rssm_attn_get_error": ([p, ctypes.POINTER(i32), p], i32),
@@ -438,10 +433,11 @@ def rssm_attn_append(handle: int, tokens: int, k, k_stride: int, v, v_stride: in
 
 
 def rssm_attn_append_rotary(handle: int, tokens: int, k, k_stride: int, v, v_stride: int, slots, rotary: AttnRotary,
-                            stream=None) -> None:
+                            positions, turns, q=None, q_out=None, stream=None) -> None:
     _check("rssm_attn_append_rotary",
            load().rssm_attn_append_rotary(handle, tokens, _addr(k), k_stride, _addr(v), v_stride, _addr(slots),
-                                          ctypes.byref(rotary), _stream(stream)))
+                                          ctypes.byref(rotary), _addr(positions), _addr(turns), _addr(q), _addr(q_out),
+                                          _stream(stream)))
 
 
 def rssm_attn_read(handle: int, tokens: int, slots, k, k_stride: int, v, v_stride: int, stream=None) -> None:

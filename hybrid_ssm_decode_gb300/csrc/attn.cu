@@ -310,19 +310,21 @@ rssm_status rssm_attn_append(rssm_attn* h, int32_t tokens, const void* d_k, int6
 }
 
 rssm_status rssm_attn_append_rotary(rssm_attn* h, int32_t tokens, const void* d_k, int64_t k_stride, const void* d_v,
-                                    int64_t v_stride, const int32_t* d_slots, const rssm_attn_rotary* r, void* stream) {
+                                    int64_t v_stride, const int32_t* d_slots, const rssm_attn_rotary* r,
+                                    const int32_t* d_positions, const uint64_t* d_turns, const void* d_q, void* d_q_out,
+                                    void* stream) {
     const rssm_status st = check_tokens(h, tokens, d_k, &k_stride, d_v, &v_stride, d_slots);
     if (st != RSSM_OK) return st;
     if (r == nullptr) return RSSM_ERR_INVALID_ARG;
     const rssm_attn_config& c = h->cfg;
     const int64_t row = static_cast<int64_t>(c.q_heads) * c.head_dim;
     PlaceArgs a = place_args(h, tokens, d_k, k_stride, d_v, v_stride, d_slots);
-    a.q = r->d_q;
-    a.q_out = r->d_q_out;
+    a.q = d_q;
+    a.q_out = d_q_out;
     a.q_stride = r->q_stride ? r->q_stride : row;
     a.qo_stride = r->q_out_stride ? r->q_out_stride : row;
-    a.positions = r->d_positions;
-    a.turns = r->d_turns;
+    a.positions = d_positions;
+    a.turns = d_turns;
     a.gain = r->gain;
     a.rotary_dim = r->rotary_dim;
     a.interleaved = r->interleaved;

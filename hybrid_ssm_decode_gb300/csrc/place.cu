@@ -102,8 +102,14 @@ __device__ __forceinline__ void store_n(T* p, const float* x) {
 // so that every kernel rounds alike.
 __device__ __forceinline__ float turned(float u, float v, float2 t) { return __fmaf_rn(u, t.x, -__fmul_rn(v, t.y)); }
 
+// Threads that a head of `half` pairs and `beside` channels more takes.
+__host__ __device__ __forceinline__ int head_threads(int half, int beside, int vec) {
+    return (half + beside / (beside % (2 * vec) == 0 ? 2 : 1)) / vec;
+}
+
 // The heads of a tile's tokens, rotated. A thread keeps to VEC pairs of one token (or to
-// VEC of the channels beside them, which are copied), so that their sines stay in
+// as many of the channels beside them, which are copied, half as many where they cannot
+// be halved), so that their sines stay in
 // registers, and goes through the token's heads by twos, the next two's channels under
 // way while it turns these; the first are on their way before the sines are made.
 template <class T, int VEC, int PAIRS>
@@ -122,15 +128,18 @@ struct Rotator {
     Raw raw[kAhead];
     int slot, e, h;
 
+    int apart;                               // of a copying thread's two vectors; 0: it has one
     __device__ __forceinline__ bool pairs() const { return e * VEC < half; }
     __device__ __forceinline__ int d0() const { return !pairs() ? R - half + e * VEC : PAIRS == kInterleaved ? 2 * e * VEC : e * VEC; }
-    __device__ __forceinline__ int d1() const { return PAIRS == kInterleaved ? VEC : half; }      // from d0
+    __device__ __forceinline__ int d1() const { return !pairs() ? apart : PAIRS == kInterleaved ? VEC : half; }   // from d0; 0: none
 
     // x, out: the tile's first token. The block takes part `y` of `ny` of every token's heads.
     __device__ __forceinline__ void start(const T* x_, T* out_, int64_t xs, int64_t os, int heads_, int dim_, int R_, int tile, int n,
                                           int y, int ny) {
         x0 = x_; out0 = out_; x_stride = xs; out_stride = os; heads = heads_; dim = dim_; R = R_; half = R / 2;
-        per_head = (half + (static_cast<const void*>(out_) == x_ ? 0 : dim - R)) / VEC;
+        const int beside = static_cast<const void*>(out_) == x_ ? 0 : dim - R;
+        per_head = head_threads(half, beside, VEC);
+        apart = beside % (2 * VEC) == 0 ? beside / 2 : 0;
         groups = max(1, kThreads / per_head);                // heads of more threads: one after another
         per_token = max(1, groups / tile);
         parts = per_token * ny;
@@ -156,7 +165,7 @@ struct Rotator {
         for (int k = 0; k < kAhead; ++k) {
             if (h + k * parts < heads) {
                 raw[k].a.load(x);
-                if (pairs()) raw[k].b.load(x + d1());
+                if (d1()) raw[k].b.load(x + d1());
             }
             x += parts * static_cast<int64_t>(dim);
         }
@@ -164,6 +173,7 @@ struct Rotator {
     __device__ __forceinline__ void put(const Raw& p, const float2 (&cs)[VEC]) const {
         if (!pairs()) {
             p.a.store(out);
+            if (apart) p.b.store(out + apart);
             return;
         }
         float r[2 * VEC];
@@ -359,16 +369,15 @@ __device__ __forceinline__ char* group_of(char* cache, const PlaceArgs& a, int p
     return cache + page * a.page_stride + static_cast<int64_t>(head * (a.page_size / kAttnGroup) + in_page / kAttnGroup) * (9 * a.dim);
 }
 
-// Channels 16 b.. of token `in_page` of a page and head into the cache.
+// Channels 16 b.. of token `in_page` of a page and head, whose scale is s, into the cache.
 template <class T, int KV, bool V>
-__device__ __forceinline__ void store_block(const PlaceArgs& a, const float (&x)[16], int page, int head, int in_page, int b) {
+__device__ __forceinline__ void store_block(const PlaceArgs& a, const float (&x)[16], int page, int head, int in_page, int b, float s) {
     char* cache = V ? a.v_cache : a.k_cache;
-    const float* scales = V ? a.v_scale : a.k_scale;
     if constexpr (KV == RSSM_KV_NVFP4) {
         char* at = group_of<V>(cache, a, page, head, in_page);
         const int t = in_page % kAttnGroup;
         uint32_t c[2];
-        const uint8_t s = quantise16(x, scales[head], c);
+        const uint8_t scale = quantise16(x, s, c);
         if (V) c[0] = nvfp4_exchanged(c[0], t), c[1] = nvfp4_exchanged(c[1], t);
         char* to = at + nvfp4_codes_at<V>(a.dim, t, b);
         if (V && a.dim == 64) {
@@ -377,12 +386,12 @@ __device__ __forceinline__ void store_block(const PlaceArgs& a, const float (&x)
         } else {
             *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
         }
-        *reinterpret_cast<uint8_t*>(at + nvfp4_scale_at<V>(a.dim, t, b)) = s;
+        *reinterpret_cast<uint8_t*>(at + nvfp4_scale_at<V>(a.dim, t, b)) = scale;
     } else {
         const int64_t at = (static_cast<int64_t>(head) * a.page_size + in_page) * a.dim + 16 * b;
         if constexpr (KV == RSSM_KV_FP8) {
             uint32_t c[4];
-            divide16(x, scales[head], c);
+            divide16(x, s, c);
             *reinterpret_cast<uint4*>(cache + page * a.page_stride + at) = make_uint4(c[0], c[1], c[2], c[3]);
         } else {
             store_n<T, 16>(reinterpret_cast<T*>(cache + page * a.page_stride) + at, x);
@@ -390,36 +399,51 @@ __device__ __forceinline__ void store_block(const PlaceArgs& a, const float (&x)
     }
 }
 
-// Channels 16 b.. of a token from the cache.
+// Channels 16 b.. of a token of the cache: as they are stored, and their values.
 template <class T, int KV, bool V>
-__device__ __forceinline__ void fetch_block(const PlaceArgs& a, float (&x)[16], int page, int head, int in_page, int b) {
-    char* cache = V ? a.v_cache : a.k_cache;
-    const float* scales = V ? a.v_scale : a.k_scale;
-    if constexpr (KV == RSSM_KV_NVFP4) {
-        const char* at = group_of<V>(cache, a, page, head, in_page);
-        const int t = in_page % kAttnGroup;
-        const char* from = at + nvfp4_codes_at<V>(a.dim, t, b);
-        uint2 c;
-        if (V && a.dim == 64) {
-            c.x = *reinterpret_cast<const uint32_t*>(from);
-            c.y = *reinterpret_cast<const uint32_t*>(from + 32);
+struct Held {
+    static constexpr int kWords = KV == RSSM_KV_NVFP4 ? 2 : KV == RSSM_KV_FP8 ? 4 : 4 * sizeof(T);
+    uint32_t w[kWords];
+    uint32_t block;              // NVFP4: the block's scale
+    float s;                     // the head's
+
+    __device__ __forceinline__ void load(const PlaceArgs& a, int page, int head, int in_page, int b) {
+        const char* cache = V ? a.v_cache : a.k_cache;
+        if constexpr (KV == RSSM_KV_NVFP4 || KV == RSSM_KV_FP8) s = (V ? a.v_scale : a.k_scale)[head];
+        if constexpr (KV == RSSM_KV_NVFP4) {
+            const char* at = group_of<V>(const_cast<char*>(cache), a, page, head, in_page);
+            const int t = in_page % kAttnGroup;
+            const char* from = at + nvfp4_codes_at<V>(a.dim, t, b);
+            block = *reinterpret_cast<const uint8_t*>(at + nvfp4_scale_at<V>(a.dim, t, b));
+            if (V && a.dim == 64) {
+                w[0] = *reinterpret_cast<const uint32_t*>(from);
+                w[1] = *reinterpret_cast<const uint32_t*>(from + 32);
+            } else {
+                const uint2 c = *reinterpret_cast<const uint2*>(from);
+                w[0] = c.x, w[1] = c.y;
+            }
         } else {
-            c = *reinterpret_cast<const uint2*>(from);
-        }
-        if (V) c.x = nvfp4_exchanged(c.x, t), c.y = nvfp4_exchanged(c.y, t);
-        const float s = __fmul_rn(e4m3_to_f(*reinterpret_cast<const uint8_t*>(at + nvfp4_scale_at<V>(a.dim, t, b))), scales[head]);
+            constexpr int kSize = KV == RSSM_KV_FP8 ? 1 : sizeof(T);
+            const uint4* from = reinterpret_cast<const uint4*>(
+                cache + page * a.page_stride + ((static_cast<int64_t>(head) * a.page_size + in_page) * a.dim + 16 * b) * kSize);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 v = e2m1x2_to_f2(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFF);
-            x[2 * i] = __fmul_rn(v.x, s);
-            x[2 * i + 1] = __fmul_rn(v.y, s);
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 c = from[i];
+                w[4 * i] = c.x, w[4 * i + 1] = c.y, w[4 * i + 2] = c.z, w[4 * i + 3] = c.w;
+            }
         }
-    } else {
-        const int64_t at = (static_cast<int64_t>(head) * a.page_size + in_page) * a.dim + 16 * b;
-        if constexpr (KV == RSSM_KV_FP8) {
-            const float s = scales[head];
-            const uint4 c = *reinterpret_cast<const uint4*>(cache + page * a.page_stride + at);
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    }
+    __device__ __forceinline__ void get(float (&x)[16], int in_page) const {
+        if constexpr (KV == RSSM_KV_NVFP4) {
+            const float f = __fmul_rn(e4m3_to_f(block), s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t c = V ? nvfp4_exchanged(w[i / 4], in_page) : w[i / 4];
+                const float2 v = e2m1x2_to_f2((c >> (8 * (i & 3))) & 0xFF);
+                x[2 * i] = __fmul_rn(v.x, f);
+                x[2 * i + 1] = __fmul_rn(v.y, f);
+            }
+        } else if constexpr (KV == RSSM_KV_FP8) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float2 v = e4m3x2_to_f2(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1))));
@@ -427,17 +451,12 @@ __device__ __forceinline__ void fetch_block(const PlaceArgs& a, float (&x)[16], 
                 x[2 * i + 1] = __fmul_rn(v.y, s);
             }
         } else {
-            constexpr int kStep = 16 / sizeof(T);
 #pragma unroll
-            for (int i = 0; i < 16; i += kStep) {
-                Pack<T, kStep> p;
-                p.load(reinterpret_cast<const T*>(cache + page * a.page_stride) + at + i);
-#pragma unroll
-                for (int j = 0; j < kStep; ++j) x[i + j] = p.at(j);
-            }
+            for (int i = 0; i < 16; ++i)
+                x[i] = __uint_as_float(sizeof(T) == 4 ? w[i * sizeof(T) / 4] : (i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
         }
     }
-}
+};
 
 // A thread's share of a tile's blocks of 16 channels: one block of one token in every
 // `step`-th head. Blocks run fastest, then tokens (four share a sector of V codes), then heads.
@@ -466,10 +485,40 @@ __device__ __forceinline__ bool slot_of(const PlaceArgs& a, int64_t tok, bool te
     return false;
 }
 
+// A thread's blocks of one token's keys or values, the next head's on its way while this
+// one's is written. (Two heads ahead cost occupancy: 32,750 tokens to a 4-bit cache 36
+// -> 43 us.)
+template <class T, int KV, int VEC, int PAIRS, bool V>
+__device__ __forceinline__ void write_heads(const PlaceArgs& a, const T* row, const Share& u, int page, int in_page,
+                                            const float2 (&t)[Key<T, VEC, PAIRS>::kSines]) {
+    constexpr bool kScaled = KV == RSSM_KV_FP8 || KV == RSSM_KV_NVFP4;
+    const float* scales = V ? a.v_scale : a.k_scale;
+    const int64_t next = u.step * static_cast<int64_t>(a.dim);
+    Key<T, VEC, PAIRS> raw;
+    float s = 0.f;
+    row += u.head * static_cast<int64_t>(a.dim);
+    if (u.head < a.heads) {
+        raw.load(row, 16 * u.b, a.rotary_dim);
+        if (kScaled) s = scales[u.head];
+    }
+    for (int h = u.head; h < a.heads; h += u.step) {
+        const Key<T, VEC, PAIRS> now = raw;
+        const float scale = s;
+        row += next;
+        if (h + u.step < a.heads) {
+            raw.load(row, 16 * u.b, a.rotary_dim);
+            if (kScaled) s = scales[h + u.step];
+        }
+        float x[16];
+        now.rotate(x, t, 16 * u.b, a.rotary_dim);
+        store_block<T, KV, V>(a, x, page, h, in_page, u.b, scale);
+    }
+}
+
 // grid.y: 1, and a block takes its tile's queries, keys and values; or one block for the
 // keys, one for the values and the others for the queries (none where there are none).
 template <class T, int KV, int VEC, int PAIRS>
-__global__ void __launch_bounds__(kThreads) place_kernel(const PlaceArgs a, int nt_log2) {
+__global__ void __launch_bounds__(kThreads, PAIRS == kNone ? 5 : 1) place_kernel(const PlaceArgs a, int nt_log2) {
     extern __shared__ float2 cs[];
     after_predecessor();
     const int nt = 1 << nt_log2, half = a.rotary_dim / 2;
@@ -490,37 +539,30 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const PlaceArgs a, int 
         if (queries) r.run(cs);
     }
     if (!live) return;
-    const int64_t next = u.step * static_cast<int64_t>(a.dim);
     if (keys) {
-        using K = Key<T, VEC, PAIRS>;
-        float2 t[K::kSines];
-        K::sines(t, cs + u.t * half, 16 * u.b, a.rotary_dim);
-        const T* row = static_cast<const T*>(a.k) + (first + u.t) * a.k_stride + u.head * static_cast<int64_t>(a.dim);
-        K k;
-        if (u.head < a.heads) k.load(row, 16 * u.b, a.rotary_dim);
-        for (int h = u.head; h < a.heads; h += u.step) {
-            const K now = k;
-            row += next;
-            if (h + u.step < a.heads) k.load(row, 16 * u.b, a.rotary_dim);       // the next one's on their way
-            float x[16];
-            now.rotate(x, t, 16 * u.b, a.rotary_dim);
-            store_block<T, KV, false>(a, x, page, h, in_page, u.b);
-        }
+        float2 t[Key<T, VEC, PAIRS>::kSines];
+        Key<T, VEC, PAIRS>::sines(t, cs + u.t * half, 16 * u.b, a.rotary_dim);
+        write_heads<T, KV, VEC, PAIRS, false>(a, static_cast<const T*>(a.k) + (first + u.t) * a.k_stride, u, page, in_page, t);
     }
     if (values) {
-        using K = Key<T, VEC, kNone>;
-        const float2 t[K::kSines] = {};
-        const T* row = static_cast<const T*>(a.v) + (first + u.t) * a.v_stride + u.head * static_cast<int64_t>(a.dim);
-        K v;
-        if (u.head < a.heads) v.load(row, 16 * u.b, 0);
-        for (int h = u.head; h < a.heads; h += u.step) {
-            const K now = v;
-            row += next;
-            if (h + u.step < a.heads) v.load(row, 16 * u.b, 0);
-            float x[16];
-            now.rotate(x, t, 0, 0);
-            store_block<T, KV, true>(a, x, page, h, in_page, u.b);
-        }
+        const float2 t[1] = {};
+        write_heads<T, KV, VEC, kNone, true>(a, static_cast<const T*>(a.v) + (first + u.t) * a.v_stride, u, page, in_page, t);
+    }
+}
+
+// A thread's blocks of one token, the next head's on its way.
+template <class T, int KV, int VEC, bool V>
+__device__ __forceinline__ void read_heads(const PlaceArgs& a, int64_t tok, const Share& u, int page, int in_page) {
+    T* row = static_cast<T*>(const_cast<void*>(V ? a.v : a.k)) + tok * (V ? a.v_stride : a.k_stride) + 16 * u.b;
+    Held<T, KV, V> raw;
+    if (u.head < a.heads) raw.load(a, page, u.head, in_page, u.b);
+    for (int h = u.head; h < a.heads; h += u.step) {
+        const Held<T, KV, V> now = raw;
+        if (h + u.step < a.heads) raw.load(a, page, h + u.step, in_page, u.b);
+        float x[16];
+        now.get(x, in_page);
+#pragma unroll
+        for (int q = 0; q < 16; q += VEC) store_n<T, VEC>(row + static_cast<int64_t>(h) * a.dim + q, x + q);
     }
 }
 
@@ -530,17 +572,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const PlaceArgs a, int n
     after_predecessor();
     const int64_t first = static_cast<int64_t>(blockIdx.x) << nt_log2;
     const Share u = share_of(a, nt_log2);
-    const bool v = blockIdx.y == 1;
     int page, in_page;
-    if (first + u.t >= a.tokens || !slot_of(a, first + u.t, !v && u.b == 0 && u.head == 0, page, in_page)) return;
-    T* row = static_cast<T*>(const_cast<void*>(v ? a.v : a.k)) + (first + u.t) * (v ? a.v_stride : a.k_stride);
-    for (int h = u.head; h < a.heads; h += u.step) {
-        float x[16];
-        if (v) fetch_block<T, KV, true>(a, x, page, h, in_page, u.b);
-        else fetch_block<T, KV, false>(a, x, page, h, in_page, u.b);
-#pragma unroll
-        for (int q = 0; q < 16; q += VEC) store_n<T, VEC>(row + static_cast<int64_t>(h) * a.dim + 16 * u.b + q, x + q);
-    }
+    if (first + u.t >= a.tokens || !slot_of(a, first + u.t, blockIdx.y == 0 && u.b == 0 && u.head == 0, page, in_page)) return;
+    if (blockIdx.y == 0) read_heads<T, KV, VEC, false>(a, first + u.t, u, page, in_page);
+    else read_heads<T, KV, VEC, true>(a, first + u.t, u, page, in_page);
 }
 
 // The widest of 16 bytes, 4, 2 and 1 elements by which all of `steps` (strides and channel
@@ -612,7 +647,7 @@ cudaError_t place_launch(const PlaceArgs& a, cudaStream_t s) {
     dim3 grid(static_cast<unsigned>(blocks));
     if (nt == 0 && 3 * blocks <= 4 * static_cast<int64_t>(sms)) {
         // few tokens: keys, values and queries in blocks of their own
-        const int per_head = rope && a.q ? (half + (a.q_out == a.q ? 0 : a.dim - a.rotary_dim)) / vec : 0;
+        const int per_head = rope && a.q ? head_threads(half, a.q_out == a.q ? 0 : a.dim - a.rotary_dim, vec) : 0;
         grid.y = 2 + (per_head ? split(3 * blocks, static_cast<int64_t>(a.q_heads) * per_head, sms) : 0);
     }
     const size_t smem = (static_cast<size_t>(half) << nt) * sizeof(float2);
@@ -659,7 +694,7 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
     const cudaError_t e = tile_log2(a.tokens, half, &sms, &nt);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (a.tokens + (1 << nt) - 1) >> nt;
-    const dim3 grid(static_cast<unsigned>(blocks), nt == 0 ? split(blocks, static_cast<int64_t>(a.heads) * ((half + beside) / vec), sms) : 1);
+    const dim3 grid(static_cast<unsigned>(blocks), nt == 0 ? split(blocks, static_cast<int64_t>(a.heads) * head_threads(half, beside, vec), sms) : 1);
     const size_t smem = (static_cast<size_t>(half) << nt) * sizeof(float2);
     return by_vec<T>(vec, [&](auto v) {
         constexpr int VEC = decltype(v)::value;

@@ -258,6 +258,8 @@ class Rope:
         turns = [t - (1 << 64) if t >> 63 else t for t in _r.rssm_rope_turns(inv_freq)]
         self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
         _cuda(self.turns.device, "device")
+        # what a call's checks look at of it
+        self.signature = (self.rotary_dim, self.interleaved, self.gain, self.turns.get_device())
 
 
 _rotary_seen: dict = {}
@@ -268,7 +270,7 @@ def rotary(out, x, positions, rope, stream=None):
     rope.rotary_dim channels of every head turned by their token's position (int32
     [tokens]), to out, alike in shape and type. float32 or bfloat16; x and out may
     be slices of a wider projection, and out may be x."""
-    key = (_sig(out), _sig(x), _sig(positions), rope.rotary_dim, rope.interleaved, rope.gain, rope.turns.get_device())
+    key = (_sig(out), _sig(x), _sig(positions), rope.signature)
     cfg = _rotary_seen.get(key)
     if cfg is None:
         cfg = _keep(_rotary_seen, key, _check_rotary(out, x, positions, rope))
@@ -399,8 +401,7 @@ class Attention:
                 _tokens(v, n, c.kv_heads, c.head_dim, self.dtype, self.device, "v"))
 
     def _append_rotary(self, k, v, slots, rope, positions, q, q_out, stream):
-        key = (_sig(k), _sig(v), _sig(slots), _sig(positions), _sig(q), _sig(q_out), rope.rotary_dim, rope.interleaved, rope.gain,
-               rope.turns.get_device())
+        key = (_sig(k), _sig(v), _sig(slots), _sig(positions), _sig(q), _sig(q_out), rope.signature)
         seen = self._seen.get(key)
         if seen is None:
             c = self.cfg
@@ -414,11 +415,10 @@ class Attention:
             if q is not None:
                 qs = _tokens(q, n, c.q_heads, c.head_dim, self.dtype, self.device, "q")
                 qo = _tokens(q_out, n, c.q_heads, c.head_dim, self.dtype, self.device, "q_out")
-            seen = _keep(self._seen, key, (n, ks, vs, qs, qo))
-        n, ks, vs, qs, qo = seen
-        r = _r.AttnRotary(rope.rotary_dim, rope.interleaved, rope.gain, rope.turns.data_ptr(), positions.data_ptr(),
-                          None if q is None else q.data_ptr(), None if q is None else q_out.data_ptr(), qs, qo)
-        st = self._fn.rssm_attn_append_rotary(self.handle, n, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), _by_ref(r),
+            seen = _keep(self._seen, key, (n, ks, vs, _by_ref(_r.AttnRotary(rope.rotary_dim, rope.interleaved, rope.gain, qs, qo))))
+        st = self._fn.rssm_attn_append_rotary(self.handle, seen[0], k.data_ptr(), seen[1], v.data_ptr(), seen[2], slots.data_ptr(),
+                                              seen[3], positions.data_ptr(), rope.turns.data_ptr(),
+                                              None if q is None else q.data_ptr(), None if q is None else q_out.data_ptr(),
                                               _stream_of(stream, self.device.index))
         if st:
             _r._check("rssm_attn_append_rotary", st)

@@ -679,20 +679,21 @@ typedef struct {
     int32_t rotary_dim;         /* the first channels of a head, even, 2..head_dim        */
     int32_t interleaved;        /* pairs: 0 channels i and i + rotary_dim/2, 1 2i and 2i + 1 */
     float gain;                 /* on the rotated channels, finite                        */
-    const uint64_t* d_turns;    /* [rotary_dim/2], rssm_rope_turns                        */
-    const int32_t* d_positions; /* [tokens]                                               */
-    const void* d_q;            /* NULL, or in_dtype [tokens][q_heads][head_dim] to rotate */
-    void* d_q_out;              /* NULL with d_q; may be d_q, with the same stride        */
     int64_t q_stride, q_out_stride; /* elements between tokens; 0: dense                  */
 } rssm_attn_rotary;
 
 /* rssm_attn_append of keys that are rotated on the way, in FP32 and before the one
- * rounding to the cache's type, and beside it d_q to d_q_out (rssm_rotary). d_k is not
- * changed; a token that has no slot is rotated into d_q_out all the same.
+ * rounding to the cache's type, and of the queries beside them (rssm_rotary).
+ *   d_positions  int32 [tokens].    d_turns  [rotary_dim/2], from rssm_rope_turns.
+ *   d_q          NULL, or in_dtype [tokens][q_heads][head_dim], rotated into d_q_out
+ *                (NULL with it), which may be d_q, with the same stride.
+ * d_k is not changed; a token that has no slot is rotated into d_q_out all the same.
  * Errors: INVALID_ARG (as rssm_attn_append; null, sizes, strides), UNSUPPORTED
  * (q_heads*head_dim > 2^24), CUDA. */
 rssm_status rssm_attn_append_rotary(rssm_attn* h, int32_t tokens, const void* d_k, int64_t k_stride, const void* d_v,
-                                    int64_t v_stride, const int32_t* d_slots, const rssm_attn_rotary* rotary, void* stream);
+                                    int64_t v_stride, const int32_t* d_slots, const rssm_attn_rotary* rotary,
+                                    const int32_t* d_positions, const uint64_t* d_turns, const void* d_q, void* d_q_out,
+                                    void* stream);
 
 /* The keys and values that the cache holds in the given slots, the reverse of
  * rssm_attn_append: d_k and d_v get in_dtype [tokens][kv_heads][head_dim], each value

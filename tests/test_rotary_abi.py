@@ -176,7 +176,7 @@ def test_python_refusals(lib):
             rssm.Rope(64, **kw)
     x = torch.zeros((2, 3, 64))
     with pytest.raises(ValueError, match="x: on cpu"):
-        rssm.rotary(x, x, torch.zeros(2, dtype=torch.int32), type("R", (), dict(rotary_dim=64, interleaved=False, gain=1.0, turns=x))())
+        rssm.rotary(x, x, torch.zeros(2, dtype=torch.int32), type("R", (), dict(rotary_dim=64, interleaved=False, gain=1.0, turns=x, signature=()))())
     cache = torch.zeros((2, 1, 16, 72), dtype=torch.uint8)
     with pytest.raises(ValueError, match="k_cache: on cpu"):
         rssm.Attention(cache, cache, batch=1, q_heads=1, max_pages=1)
