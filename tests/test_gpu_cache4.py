@@ -493,3 +493,77 @@ def test_refusals(cuda_lib):
     none = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
     a.read(none, none, slots[:0])
     a.append(none, none, slots[:0], rope=rope, positions=pos[:0])
+
+
+@pytest.mark.parametrize("kv", ["nvfp4", "fp8", "bf16"])
+@pytest.mark.parametrize("off,step", [(4, 772), (2, 770), (1, 769)])
+def test_rotated_from_rows_wherever_they_begin(cuda_lib, kv, off, step):
+    n, heads, q_heads, dim, ps = 21, 2, 4, 64, 16
+    ks, vs = scales(heads)
+    rope = rssm.Rope(64)
+    a = layer(*caches(3, heads, ps, dim, kv), kv, ks, vs, q_heads)
+    flat = torch.randn(off + n * step).bfloat16().cuda()
+    q, k, v = (flat.as_strided((n, h, dim), (step, dim, 1), off + at * dim) for h, at in ((q_heads, 0), (heads, q_heads), (heads, q_heads + heads)))
+    slots, pos = torch.randperm(3 * ps)[:n].to(torch.int32).cuda(), torch.arange(n, dtype=torch.int32, device="cuda") * 1000
+    out, want, turned = torch.empty((n, q_heads, dim), dtype=torch.bfloat16, device="cuda"), torch.empty((n, q_heads, dim), dtype=torch.bfloat16, device="cuda"), torch.empty((n, heads, dim), device="cuda")
+    a.append(k, v, slots, rope=rope, positions=pos, q=q, q_out=out)
+    rssm.rotary(want, q.contiguous(), pos, rope)
+    rssm.rotary(turned, k.float().contiguous(), pos, rope)
+    ko, vo = torch.empty((2, n, heads, dim), dtype=torch.bfloat16, device="cuda")
+    a.read(ko, vo, slots)
+    assert torch.equal(out, want)
+    assert same(ko.cpu(), stored(turned.cpu(), ks, kv)) and same(vo.cpu(), stored(v.cpu(), vs, kv))
+
+
+def test_a_cache_beyond_4_gb(cuda_lib):
+    """Pages whose bytes lie past 2^32, in the writer, the reader and the attention."""
+    heads, dim, ps, num = 8, 128, 16, 520_000                  # 9216 bytes a page: 4.8 GB each
+    ks, vs = scales(heads)
+    k_cache, v_cache = (torch.empty((num, heads, ps, dim // 16 * 9), dtype=torch.uint8, device="cuda") for _ in "kv")
+    lens, table = [50, 33], torch.tensor([[num - 1, 5, num - 7, num - 300], [num - 2, 470_000, num - 3, 0]], dtype=torch.int32)
+    a = layer(k_cache, v_cache, "nvfp4", ks, vs, 16, batch=2, max_pages=4)
+    q = torch.randn((2, 1, 16, dim)).bfloat16()
+    out, lse = torch.empty_like(q, device="cuda"), torch.empty((2, 1, 16), device="cuda")
+    held = []
+    for b, n in enumerate(lens):
+        k, v = (torch.randn((n, heads, dim)).bfloat16() for _ in "kv")
+        i = torch.arange(n)
+        slots = (table[b, i // ps].long() * ps + i % ps).int().cuda()
+        a.append(k.cuda(), v.cuda(), slots)
+        ko, vo = torch.empty((2, n, heads, dim), dtype=torch.bfloat16, device="cuda")
+        a.read(ko, vo, slots)
+        held.append((quantised(k, ks), quantised(v, vs)))
+        assert same(ko.cpu(), held[b][0].bfloat16()) and same(vo.cpu(), held[b][1].bfloat16())
+    a.decode(out, q.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), table.cuda(), lse=lse)
+    assert a.get_error() == (0, 0, 0, 0)
+    for b in range(2):
+        k, v = (x.double() for x in held[b])
+        s = torch.einsum("hgd,nhd->hgn", q[b, 0].double().view(heads, 2, dim), k) / math.sqrt(dim)
+        l = torch.logsumexp(s, -1)
+        w = torch.einsum("hgn,nhd->hgd", torch.exp(s - l[..., None]), v).reshape(16, dim)
+        lim = float(v.abs().max()) * (2.0 ** -13 + 2.0 ** -12) + BF16 * w.abs()
+        assert bool(((out[b, 0].cpu().double() - w).abs() <= lim).all())
+        assert float((lse[b, 0].cpu().double() - l.reshape(16)).abs().max()) <= 2.0 ** -14
+
+
+def test_a_long_tail_under_one_large_score(cuda_lib):
+    """Weights of 2^-22 of the largest, 20,000 of them, add up as they should, although each is far below the output's rounding."""
+    n, dim = 20001, 64
+
+    def spoil(b, k, v):
+        k[:] = 0.0
+        k[:, :, :16] = 1.0                                     # every tail token's score: q.k of the first block
+        k[0, :, :16] = 0.0
+        k[0, :, 16:32] = 1.0
+        v[:] = 1.0
+        v[0] = 0.0
+    c = Case([n], q_heads=1, kv_heads=1, dim=dim, scale=1.0, spoil=spoil)
+    held = float(c.tokens[0][0][1, 0, 0])
+    gap = 22 * math.log(2.0)                                   # the first token's score over the others'
+    c.q[:] = 0.0
+    c.q[0, 0, 0, 16] = gap / held
+    c.check(c.run())
+    w_out, _ = c.want()
+    assert float(w_out[0, 0, 0, 0]) > 0.003                     # the tail is what the output is made of
+    out, _ = c.run()
+    assert abs(float(out[0, 0, 0, 0]) / float(w_out[0, 0, 0, 0]) - 1) < 2.0 ** -7
