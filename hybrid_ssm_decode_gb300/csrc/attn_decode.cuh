@@ -78,7 +78,7 @@ struct Shape {
     static constexpr int kSlot = 2 * kHalf;
     static constexpr int kSlotGroups = 1;                // groups in a slot
     static constexpr int DS = 1;                         // warps that share a slot's channels (attn_nvfp4.cuh)
-    static constexpr int kShared = 0;                    // bytes in which they exchange scores
+    static constexpr int kShared = 0;                    // bytes that its warps keep for themselves
     static constexpr int kJoin = 16;                     // parts joined at a time
     static constexpr int kCopied = 2 * kHalf;            // bytes that the copies of a group bring
     static constexpr int QS = D * kQsz + 16;             // bytes from one query row to the next
@@ -1186,7 +1186,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     wp.lane = lane;
     wp.g = lane >> 2;
     wp.c = lane & 3;
-    if constexpr (S::DS > 1) wp.pair_up(warp, shared);
+    if constexpr (S::kShared > 0) wp.settle(warp, shared);
     const bool speaks = wp.speaks() && warp % S::DS == 0;
     // The part that went to the workspace last: its arrival is counted while the
     // next part runs (one thread waits for the writes and the count, not the

@@ -64,14 +64,20 @@ struct Shape4 {
     // are shared out per quarter of an SM: 8 warps leave 255 a thread, 12 leave 168 and 16
     // 128, producers included.
     static constexpr int kMinBlocks = attn4_blocks(8 * NR * WM, D);
-    static constexpr int NT = D == 256 ? (kMinBlocks == 2 ? 2 : WM >= 2 ? 1 : 3)
-                            : WM == 4 ? 2 : WM == 2 ? 3 : kMinBlocks == 4 ? 2 : kMinBlocks == 1 ? 7 : 5;
+    static constexpr int NT = D == 256 ? (NR == 1 ? 2 : WM == 1 ? 3 : 2)
+                            : D == 128 ? (NR == 1 ? 2 : WM == 4 ? 2 : 5)
+                                       : (NR == 1 ? 2 : WM == 4 ? 2 : WM == 2 ? 3 : 5);
     static constexpr int kJoin = 32;
     static constexpr int kWarpRows = 8 * NR;
+    // 32 and 64 rows: queries are read from shared memory at each product. In registers, beside
+    // the outputs, they leave an SM five to seven warps, and those a third of its issue slots.
+    static constexpr bool kQShared = WM > 1 && D >= 128;
+    static constexpr int kQueries = NR * (D / DS / 16) * 2 * 32 * 4;           // bytes of a warp's queries
     static constexpr int kSlotScores = 2 * NR * 4 * 32 * 4;   // bytes of a slot's scores, as one warp holds them
     static constexpr int kRows = kWarpRows * WM;
     static constexpr int kConsumers = WM * NT * DS;
-    static constexpr int kShared = DS == 1 ? 0 : WM * NT * 2 * 2 * kSlotScores;   // [pair][turn][half]
+    static constexpr int kExchange = DS == 1 ? 0 : WM * NT * 2 * 2 * kSlotScores;   // [pair][turn][half]
+    static constexpr int kShared = kExchange + (kQShared ? kConsumers * kQueries : 0);
     static constexpr int kThreads = (kConsumers + 1) * 32;
     static constexpr int kQsz = 2;
     // A slot holds two groups, which a warp takes together.
@@ -90,7 +96,7 @@ struct Shape4 {
     static constexpr int kSlotsFit = (kBudget - kFixed) / kSlot;
     static constexpr int NS = (kSlotsFit > 24 ? 24 : kSlotsFit) / NT * NT;
     static constexpr bool kPair = false;
-    static constexpr bool kTogether = D / DS * NR <= 128;     // the scores of a slot's groups, product by product
+    static constexpr bool kTogether = D / DS * NR <= 128 || kQShared;     // the scores of a slot's groups, product by product
     static constexpr int PB = 8;
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
     static_assert(NS >= NT && NS % NT == 0 && NS >= PB / kSlotGroups, "ring too small");
@@ -143,17 +149,22 @@ struct Warp<kNVFP4, S> {
     float base[kLaneRows];       // the score, before its multiplier, that weights are relative to; the same in all lanes of a row
     float most[kLaneRows];       // scores up to here need no other; -inf before the first
     float l[kLaneRows];          // this lane's tokens only
-    uint32_t qf[NR][2 * kWords][2];
+    uint32_t qf[S::kQShared ? 1 : NR][2 * kWords][2];
+    uint32_t qs = 0;             // or in shared memory, [NR][2 kWords][lane] pairs of words
     float mul[kLaneRows];        // score multiplier, > 0
     int lane, g, c;
     int half = 0, pair = 0, turn = 0;   // of a pair's two warps; the pair; of its two exchange buffers
     char* shared = nullptr;
 
-    // The warp's place in its pair, and where the two exchange their scores.
-    __device__ __forceinline__ void pair_up(int warp, char* buffers) {
-        half = warp & 1;
-        pair = warp >> 1;
-        shared = buffers + pair * 4 * S::kSlotScores;
+    // The warp's place in its pair, where the two exchange their scores, and where its
+    // queries are.
+    __device__ __forceinline__ void settle(int warp, char* buffers) {
+        if constexpr (S::DS == 2) {
+            half = warp & 1;
+            pair = warp >> 1;
+            shared = buffers + pair * 4 * S::kSlotScores;
+        }
+        if constexpr (S::kQShared) qs = smem_u32(buffers + S::kExchange + warp * S::kQueries) + lane * 8;
     }
     // The sum of both warps' scores. A buffer is written again two exchanges later, behind
     // the barrier of the one between them, which the other warp passes after its reads.
@@ -234,8 +245,13 @@ struct Warp<kNVFP4, S> {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float4 v = load4(reinterpret_cast<const __nv_bfloat16*>(q) + channel(j) + 4 * h);
-                    qf[n][2 * j + h][0] = pack_f16(v.x * f1 * f2, v.y * f1 * f2);
-                    qf[n][2 * j + h][1] = pack_f16(v.z * f1 * f2, v.w * f1 * f2);
+                    const uint32_t q0 = pack_f16(v.x * f1 * f2, v.y * f1 * f2), q1 = pack_f16(v.z * f1 * f2, v.w * f1 * f2);
+                    if constexpr (S::kQShared) {
+                        asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(qs + ((n * 2 * kWords) + 2 * j + h) * 256), "r"(q0), "r"(q1) : "memory");
+                    } else {
+                        qf[n][2 * j + h][0] = q0;
+                        qf[n][2 * j + h][1] = q1;
+                    }
                 }
         }
     }
@@ -283,7 +299,15 @@ struct Warp<kNVFP4, S> {
                 for (int j = 0; j < 4; ++j) s[i][n][j] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < kWords; ++j)
+        for (int j = 0; j < kWords; ++j) {
+            uint32_t q[2][NR][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    if constexpr (S::kQShared) lds<2>(q[h][n], qs + (n * 2 * kWords + 2 * j + h) * 256);
+                    else q[h][n][0] = qf[n][2 * j + h][0], q[h][n][1] = qf[n][2 * j + h][1];
+                }
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 uint32_t x[4], y[4];
@@ -298,9 +322,10 @@ struct Warp<kNVFP4, S> {
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t a[4] = {x[2 * h], y[2 * h], x[2 * h + 1], y[2 * h + 1]};
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) mma_f16(s[i][n], a, qf[n][2 * j + h][0], qf[n][2 * j + h][1]);
+                    for (int n = 0; n < NR; ++n) mma_f16(s[i][n], a, q[h][n][0], q[h][n][1]);
                 }
             }
+        }
     }
 
     // Running sum under a maximum; the scores become weights. A row's lanes exchange their
