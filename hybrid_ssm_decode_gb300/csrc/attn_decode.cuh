@@ -45,7 +45,7 @@
 // widen exactly to FP16 (Q scaled per row by a power of two into FP16's range;
 // 2^(s-m+15) rounded to FP16's 11 bits, so that only weights below 2^-29 of the largest
 // lose some of them and only those below 2^-40 vanish: a long tail under one large
-// score counts), and on FP32 caches m16n8k8 on TF32 with both
+// score counts; NVFP4 caches: attn_nvfp4.cuh), and on FP32 caches m16n8k8 on TF32 with both
 // operands split in two (three products; what is left out is below 2^-21).
 #pragma once
 
