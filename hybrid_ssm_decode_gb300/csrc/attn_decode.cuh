@@ -110,6 +110,7 @@ struct Shape {
     static_assert(!kPair || NS - NT >= PB, "a pair of groups must fit the ring");
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
     static_assert(NS >= NT && NS % NT == 0, "ring too small");
+    static_assert(16 * NS + 32 + 8 + 2 * 40 <= 512, "barriers and parts");
 };
 
 template <int N> struct Int { static constexpr int value = N; };
@@ -379,8 +380,9 @@ struct Part {
     int first;                   // block of the request's first part
     int others;                  // parts of the request and head beside this one
     int at_start;                // the part begins with the request's first unit
-    float ks, vs;                // FP8 and NVFP4: the head's scales
 };
+
+static_assert(sizeof(Part) == 40, "two of them, beside the barriers");
 
 // ---- one warp's products -----------------------------------------------------
 // The byte of a slot's K or V at (token r, 16-byte chunk c) under the TMA swizzle.
@@ -905,7 +907,7 @@ __device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, floa
     constexpr int D = S::D, kThreads = S::kConsumers * 32, kJoin = S::kJoin;
     static_assert((attn_max_grid(S::kMinBlocks) + kJoin - 1) / kJoin <= 32 && kJoin <= 32 && 32 <= S::OS, "a round of parts must fit a warp and the buffer");
     const int np = part.others + 1;
-    const float vs = KV == kFP8 || KV == kNVFP4 ? part.vs : 1.f;
+    const float vs = KV == kFP8 || KV == kNVFP4 ? __ldcg(a.v_scale + part.head) : 1.f;
     // this block's kJoin neighbours, and then one part for each such round; or all at once
     int p0 = 0, step = 1, n = np;
     bool final = np <= kJoin;
@@ -1012,6 +1014,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     volatile int* dead = reinterpret_cast<volatile int*>(qempty + 2);
     volatile int* s_last = dead + 1;
     Part* s_part = reinterpret_cast<Part*>(const_cast<int*>(dead + 2));  // [2]
+    [[maybe_unused]] float2* s_scales = reinterpret_cast<float2*>(s_part + 2);   // [2], NVFP4
     [[maybe_unused]] char* shared = smem + S::kSmem - 1024 - S::kShared;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1050,6 +1053,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         // current one's copies go out: a part's start then costs no round trip.
         Part d, nd;
         int g1 = 0, ng1 = 0, next_page = 0, next_row = 0;
+        float2 scales, next_scales = make_float2(0.f, 0.f);
         const auto look_up = [&](int b, int base, int end, int& page, int& row) {
             page = a.num_pages;                          // outside the map: read as zeros
             row = 0;
@@ -1064,10 +1068,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             nd.b = cur.b;
             nd.len = cur.sp.len;
             nd.head = cur.pair / a.chunks;
-            if (KV == kFP8 || KV == kNVFP4) {                // here, where nobody waits for them
-                nd.ks = __ldcg(a.k_scale + nd.head);
-                nd.vs = __ldcg(a.v_scale + nd.head);
-            }
+            // the head's scales: asked for here, where nobody waits for them
+            if (KV == kNVFP4) next_scales = make_float2(__ldcg(a.k_scale + nd.head), __ldcg(a.v_scale + nd.head));
             nd.row0 = (cur.pair - nd.head * a.chunks) * S::kRows;
             nd.g0 = cur.first_group();
             ng1 = cur.end_group();
@@ -1091,11 +1093,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             d = nd;
             g1 = ng1;
             int page = next_page, row = next_row;
+            scales = next_scales;
             const int rows = min(S::kRows, rows_all - d.row0);
             const int pq = parts & 1;
             if ((parts < 2 || wait_phase(qempty + pq, ((parts >> 1) - 1) & 1, dead, a.err)) && !*dead) {
                 if (lane == 0) {
                     s_part[pq] = d;
+                    if (KV == kNVFP4) s_scales[pq] = scales;
                     if (d.at_start && d.pair == 0) {
                         const int given = __ldcg(a.lens + d.b);
                         if (given != d.len) report_error(a.err, RSSM_DEV_ATTN_LEN, d.b, given);
@@ -1212,7 +1216,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         const Part part = s_part[pq];
         if (part.pair < 0) break;
         if (left.pair >= 0 && tid == 0) count_left();
-        const int row0 = part.row0, len = part.len;
+        const int head = part.head, row0 = part.row0, len = part.len;
+        const float2 scales = KV == kNVFP4 ? s_scales[pq] : make_float2(1.f, 1.f);
         const int rows = min(S::kRows, rows_all - row0);
         // what the lane's rows see: [see_lo, see_hi]
         int draft[kLaneRows], see_lo[kLaneRows], see_hi[kLaneRows];
@@ -1228,7 +1233,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         const int some_lo = window_start(len - a.T, a.window);
         wp.reset();
         wp.load_q(qbuf + (pq * S::kRows + wm * S::kWarpRows) * S::QS, a.scale_log2,
-                  KV == kFP8 || KV == kNVFP4 ? part.ks : 1.f);
+                  KV == kFP8 ? __ldcg(a.k_scale + head) : scales.x);
         if (KV != kF32) {
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty + pq);
@@ -1302,7 +1307,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             if (lane == 0) mbar_arrive(qempty + pq);
         }
         ++parts;
-        const float vs = KV == kFP8 || KV == kNVFP4 ? part.vs : 1.f;
+        const float vs = KV == kFP8 ? __ldcg(a.v_scale + head) : scales.y;   // there once the warps are joined
 
         // ---- join the warps of each row ----
 #pragma unroll

@@ -667,8 +667,7 @@ rssm_status rssm_attn_create(const rssm_attn_config* cfg, void* d_k_cache, void*
  * scale b = E4M3(m * (1 / (6 scale))), at most 448, and the codes E2M1(x * (1 / (b scale))),
  * at most +-6, to nearest even, in FP32 (b = 0: zeros). A NaN makes b NaN, and so the 16
  * values; an infinity is held as the largest value.
- * A slot twice in one call: one of its tokens stays, which is not said (NVFP4: each
- * block of 16 channels may be another's).
+ * A slot may be given once in a call: what one given twice holds is not said.
  * Errors: INVALID_ARG (null, tokens < 0, a stride below the row), UNSUPPORTED (NVFP4
  * rows of more than 2^24 elements), CUDA. */
 rssm_status rssm_attn_append(rssm_attn* h, int32_t tokens, const void* d_k, int64_t k_stride, const void* d_v,

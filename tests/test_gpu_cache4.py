@@ -567,3 +567,22 @@ def test_a_long_tail_under_one_large_score(cuda_lib):
     assert float(w_out[0, 0, 0, 0]) > 0.003                     # the tail is what the output is made of
     out, _ = c.run()
     assert abs(float(out[0, 0, 0, 0]) / float(w_out[0, 0, 0, 0]) - 1) < 2.0 ** -7
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.0123, 0.3333333, 2.0 ** -7, 7.77, 3e-39, 1e-31, 1e31])
+def test_fp8_codes_of_every_bf16_number(cuda_lib, scale):
+    """The writer with rotary positions, at position 0, stores what the writer without them does: the rounded quotient's code."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = bits.view(1024, 1, 64)
+    k = torch.where(x.isfinite(), x, torch.zeros_like(x))      # a pair's infinity would reach its other half
+    s = torch.tensor([scale])
+    slots, pos = torch.randperm(1024).to(torch.int32).cuda(), torch.zeros(1024, dtype=torch.int32, device="cuda")
+    made = []
+    for kw in ({}, dict(rope=rssm.Rope(64), positions=pos)):
+        c = caches(64, 1, 16, 64, "fp8", fill=0)
+        layer(*c, "fp8", s, s, 1).append(k.cuda(), x.cuda(), slots, **kw)
+        made.append([t.view(torch.uint8).cpu() for t in c])
+    assert torch.equal(made[0][1], made[1][1])
+    # a key's zero may change its sign: -0 cos 0 - u sin 0
+    differ = made[0][0] != made[1][0]
+    assert bool(((made[0][0][differ] | made[1][0][differ]) == 0x80).all())
