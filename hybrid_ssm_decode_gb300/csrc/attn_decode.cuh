@@ -373,7 +373,7 @@ struct Cursor {
 };
 
 // A part as the producer describes it to the consumers.
-struct Part {
+struct PartBase {
     int b, len, head, row0;      // request, its length, cache head, first query row
     int g0, ng;                  // groups of 16 tokens
     int pair;                    // -1: no more parts
@@ -382,7 +382,13 @@ struct Part {
     int at_start;                // the part begins with the request's first unit
 };
 
-static_assert(sizeof(Part) == 40, "two of them, beside the barriers");
+template <int KV>
+struct Part : PartBase {};
+template <>
+struct Part<kNVFP4> : PartBase {
+    float ks, vs;                // the head's scales
+};
+static_assert(sizeof(Part<kFP8>) == 40 && sizeof(Part<kNVFP4>) == 48, "two of them, beside the barriers");
 
 // ---- one warp's products -----------------------------------------------------
 // The byte of a slot's K or V at (token r, 16-byte chunk c) under the TMA swizzle.
@@ -880,7 +886,7 @@ struct Warp {
 // Outputs of row r of a part, columns col..col + 3, from the sums v under maximum
 // M and total L; vs: FP8 and NVFP4, the scale of the head's values.
 template <int KV, class S>
-__device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, int col, float4 v, float M, float L, float vs) {
+__device__ __forceinline__ void put(const AttnArgs& a, const Part<KV>& part, int r, int col, float4 v, float M, float L, float vs) {
     const int t = (part.row0 + r) / a.group, j = (part.row0 + r) % a.group;
     const int64_t at = (static_cast<int64_t>(part.b) * a.T + t) * a.q_heads + part.head * a.group + j;
     const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -901,13 +907,15 @@ __device__ __forceinline__ void put(const AttnArgs& a, const Part& part, int r, 
 // arrived. Not inlined: it runs once or twice a block, and its registers are
 // not the stream's.
 template <int KV, class S>
-__device__ __noinline__ void join_parts(const AttnArgs& a, const Part part, float* fw, float2* s_row, volatile int* s_last) {
+__device__ __noinline__ void join_parts(const AttnArgs& a, const Part<KV> part, float* fw, float2* s_row, volatile int* s_last) {
     const int rows = min(S::kRows, a.T * a.group - part.row0);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int D = S::D, kThreads = S::kConsumers * 32, kJoin = S::kJoin;
     static_assert((attn_max_grid(S::kMinBlocks) + kJoin - 1) / kJoin <= 32 && kJoin <= 32 && 32 <= S::OS, "a round of parts must fit a warp and the buffer");
     const int np = part.others + 1;
-    const float vs = KV == kFP8 || KV == kNVFP4 ? __ldcg(a.v_scale + part.head) : 1.f;
+    float vs = 1.f;
+    if constexpr (KV == kFP8) vs = __ldcg(a.v_scale + part.head);
+    if constexpr (KV == kNVFP4) vs = part.vs;
     // this block's kJoin neighbours, and then one part for each such round; or all at once
     int p0 = 0, step = 1, n = np;
     bool final = np <= kJoin;
@@ -1013,8 +1021,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     uint64_t* qempty = qfull + 2;
     volatile int* dead = reinterpret_cast<volatile int*>(qempty + 2);
     volatile int* s_last = dead + 1;
-    Part* s_part = reinterpret_cast<Part*>(const_cast<int*>(dead + 2));  // [2]
-    [[maybe_unused]] float2* s_scales = reinterpret_cast<float2*>(s_part + 2);   // [2], NVFP4
+    Part<KV>* s_part = reinterpret_cast<Part<KV>*>(const_cast<int*>(dead + 2));  // [2]
     [[maybe_unused]] char* shared = smem + S::kSmem - 1024 - S::kShared;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1051,9 +1058,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         Cursor cur;
         // The next part is found, and its first pages are looked up, before the
         // current one's copies go out: a part's start then costs no round trip.
-        Part d, nd;
+        Part<KV> d, nd;
         int g1 = 0, ng1 = 0, next_page = 0, next_row = 0;
-        float2 scales, next_scales = make_float2(0.f, 0.f);
         const auto look_up = [&](int b, int base, int end, int& page, int& row) {
             page = a.num_pages;                          // outside the map: read as zeros
             row = 0;
@@ -1068,8 +1074,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             nd.b = cur.b;
             nd.len = cur.sp.len;
             nd.head = cur.pair / a.chunks;
-            // the head's scales: asked for here, where nobody waits for them
-            if (KV == kNVFP4) next_scales = make_float2(__ldcg(a.k_scale + nd.head), __ldcg(a.v_scale + nd.head));
+            if constexpr (KV == kNVFP4) {                    // here, where nobody waits for them
+                nd.ks = __ldcg(a.k_scale + nd.head);
+                nd.vs = __ldcg(a.v_scale + nd.head);
+            }
             nd.row0 = (cur.pair - nd.head * a.chunks) * S::kRows;
             nd.g0 = cur.first_group();
             ng1 = cur.end_group();
@@ -1093,13 +1101,11 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             d = nd;
             g1 = ng1;
             int page = next_page, row = next_row;
-            scales = next_scales;
             const int rows = min(S::kRows, rows_all - d.row0);
             const int pq = parts & 1;
             if ((parts < 2 || wait_phase(qempty + pq, ((parts >> 1) - 1) & 1, dead, a.err)) && !*dead) {
                 if (lane == 0) {
                     s_part[pq] = d;
-                    if (KV == kNVFP4) s_scales[pq] = scales;
                     if (d.at_start && d.pair == 0) {
                         const int given = __ldcg(a.lens + d.b);
                         if (given != d.len) report_error(a.err, RSSM_DEV_ATTN_LEN, d.b, given);
@@ -1195,7 +1201,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
     // The part that went to the workspace last: its arrival is counted while the
     // next part runs (one thread waits for the writes and the count, not the
     // block), and if it was the request's last, it is joined after that part.
-    Part left;
+    Part<KV> left;
     left.pair = -1;
     // A split request and head is known by the block of its first part: that part ends
     // its block's share, so no block has two such.
@@ -1213,11 +1219,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         // all consumer warps go on, or none: one that gave up must not leave the
         // others at a barrier
         if (!all_of(wait_phase(qfull + pq, (parts >> 1) & 1, dead, a.err), 2, kThreads)) break;
-        const Part part = s_part[pq];
+        const Part<KV> part = s_part[pq];
         if (part.pair < 0) break;
         if (left.pair >= 0 && tid == 0) count_left();
         const int head = part.head, row0 = part.row0, len = part.len;
-        const float2 scales = KV == kNVFP4 ? s_scales[pq] : make_float2(1.f, 1.f);
         const int rows = min(S::kRows, rows_all - row0);
         // what the lane's rows see: [see_lo, see_hi]
         int draft[kLaneRows], see_lo[kLaneRows], see_hi[kLaneRows];
@@ -1232,8 +1237,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
         const int all_lo = window_start(len - 1, a.window);         // and the first
         const int some_lo = window_start(len - a.T, a.window);
         wp.reset();
-        wp.load_q(qbuf + (pq * S::kRows + wm * S::kWarpRows) * S::QS, a.scale_log2,
-                  KV == kFP8 ? __ldcg(a.k_scale + head) : scales.x);
+        float ks = 1.f, vs = 1.f;
+        if constexpr (KV == kFP8) ks = __ldcg(a.k_scale + head);
+        if constexpr (KV == kNVFP4) ks = part.ks, vs = part.vs;
+        wp.load_q(qbuf + (pq * S::kRows + wm * S::kWarpRows) * S::QS, a.scale_log2, ks);
         if (KV != kF32) {
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty + pq);
@@ -1307,7 +1314,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             if (lane == 0) mbar_arrive(qempty + pq);
         }
         ++parts;
-        const float vs = KV == kFP8 ? __ldcg(a.v_scale + head) : scales.y;   // there once the warps are joined
+        if constexpr (KV == kFP8) vs = __ldcg(a.v_scale + head);               // there once the warps are joined
 
         // ---- join the warps of each row ----
 #pragma unroll

@@ -108,7 +108,7 @@ struct Shape4 {
     static constexpr int PB = 8;
     static constexpr int kSmem = 1024 + NS * kSlot + kFixed;
     static_assert(NS >= NT && NS % NT == 0 && NS >= PB / kSlotGroups, "ring too small");
-    static_assert(16 * NS + 32 + 8 + 2 * 40 + 16 <= 1024, "barriers, parts and scales");
+    static_assert(16 * NS + 32 + 8 + 2 * 48 <= 1024, "barriers and parts");
 };
 
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
