@@ -373,7 +373,7 @@ class Attention:
         except Exception:
             pass
 
-    def append(self, k, v, slots, rope=None, positions=None, q=None, q_out=None, stream=None):
+    def append(self, k, v, slots, stream=None, *, rope=None, positions=None, q=None, q_out=None):
         """Write the new tokens' keys and values ([tokens][kv_heads][head_dim],
         slices of a wider projection too) to their slots.
 

@@ -1,0 +1,38 @@
+"""The attention binding's calls on the host: what they pass on, and what they refuse."""
+import pytest
+import torch
+
+import hybrid_ssm_decode_gb300 as rssm
+
+BF16 = torch.bfloat16
+
+
+class Calls:
+    """In the place of the library: keeps the arguments of the last call."""
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.last = (name, args)
+            return 0
+        return call
+
+
+def attention(monkeypatch):
+    """A layer of 2 cache heads of 64 and 4 query heads, on CPU tensors and without a handle."""
+    monkeypatch.setattr(rssm.hybrid, "_stream_of", lambda stream, device: stream)
+    a = object.__new__(rssm.Attention)
+    a.handle, a.device, a.dtype, a._seen, a._fn = 0, torch.device("cpu"), BF16, {}, Calls()
+    a.cfg = rssm.AttnConfig(batch=1, q_heads=4, kv_heads=2, head_dim=64)
+    return a
+
+
+def test_append_takes_the_stream_behind_the_slots(monkeypatch):
+    """Its fourth argument is the stream, with or without a name; what goes with rope has to be named."""
+    a = attention(monkeypatch)
+    x, slots = torch.zeros((3, 2, 64), dtype=BF16), torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: a.append(x, x, slots, 64), lambda: a.append(x, x, slots, stream=64)):
+        call()
+        name, args = a._fn.last
+        assert name == "rssm_attn_append" and args[-1] == 64
+    with pytest.raises(TypeError):
+        a.append(x, x, slots, None, slots)
