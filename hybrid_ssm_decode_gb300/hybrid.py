@@ -236,7 +236,8 @@ class Rope:
     formulas), with `factor`, and for the last two `original`, the positions that the
     model was trained on, and optionally fast and slow. gain: the factor on the
     rotated channels; None: the scaling's own. inv_freq: the frequencies
-    themselves, radians a position, in the place of base and scaling.
+    themselves, radians a position, in the place of base and scaling. A Rope stays as
+    it is made: calls know what they concluded about one by its `signature`.
     """
 
     def __init__(self, rotary_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=0, fast=0.0, slow=0.0,
@@ -253,13 +254,18 @@ class Rope:
             _need(scaling == "none", "inv_freq: given, so scaling must be none")
             inv_freq = [float(w) for w in inv_freq]
             _need(len(inv_freq) == rotary_dim // 2, f"inv_freq: {len(inv_freq)} frequencies, must be {rotary_dim // 2}")
-        self.rotary_dim, self.interleaved, self.frequencies = rotary_dim, bool(interleaved), inv_freq
-        self.gain = own if gain is None else float(gain)
+        interleaved, gain = bool(interleaved), own if gain is None else float(gain)
         turns = [t - (1 << 64) if t >> 63 else t for t in _r.rssm_rope_turns(inv_freq)]
-        self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
-        _cuda(self.turns.device, "device")
-        # what a call's checks look at of it
-        self.signature = (self.rotary_dim, self.interleaved, self.gain, self.turns.get_device())
+        turns = torch.tensor(turns, dtype=torch.int64, device=device)
+        _cuda(turns.device, "device")
+        self.__dict__.update(rotary_dim=rotary_dim, interleaved=interleaved, frequencies=tuple(inv_freq), gain=gain, turns=turns,
+                             # what a call's checks look at of it
+                             signature=(rotary_dim, interleaved, gain, turns.get_device()))
+
+    def __setattr__(self, name, value=None):
+        raise AttributeError(f"{name}: a Rope stays as it is made")
+
+    __delattr__ = __setattr__
 
 
 _rotary_seen: dict = {}

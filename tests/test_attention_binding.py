@@ -36,3 +36,20 @@ def test_append_takes_the_stream_behind_the_slots(monkeypatch):
         assert name == "rssm_attn_append" and args[-1] == 64
     with pytest.raises(TypeError):
         a.append(x, x, slots, None, slots)
+
+
+def test_a_rope_stays_as_it_is_made(monkeypatch):
+    """Calls keep what they concluded about a Rope by its signature: a later gain would reach new shapes alone."""
+    monkeypatch.setattr(rssm.hybrid, "_cuda", lambda device, name: None)
+    rope = rssm.Rope(64, base=500.0, gain=1.5, device="cpu")
+    freq = list(rope.frequencies)
+    for name, value in (("gain", 0.5), ("interleaved", True), ("rotary_dim", 32), ("frequencies", freq[:1]),
+                        ("turns", rope.turns.clone()), ("signature", ())):
+        with pytest.raises(AttributeError, match="stays as it is made"):
+            setattr(rope, name, value)
+        with pytest.raises(AttributeError, match="stays as it is made"):
+            delattr(rope, name)
+    with pytest.raises(TypeError):
+        rope.frequencies[0] = 0.0
+    assert (rope.gain, rope.interleaved, rope.rotary_dim, list(rope.frequencies)) == (1.5, False, 64, freq)
+    assert rope.signature[:3] == (64, False, 1.5)
