@@ -38,7 +38,13 @@ def test_append_takes_the_stream_behind_the_slots(monkeypatch):
         a.append(x, x, slots, None, slots)
 
 
-def test_a_rope_stays_as_it_is_made(monkeypatch):
+@pytest.fixture(scope="module")
+def lib():
+    rssm.build()
+    return rssm.load()
+
+
+def test_a_rope_stays_as_it_is_made(lib, monkeypatch):
     """Calls keep what they concluded about a Rope by its signature: a later gain would reach new shapes alone."""
     monkeypatch.setattr(rssm.hybrid, "_cuda", lambda device, name: None)
     rope = rssm.Rope(64, base=500.0, gain=1.5, device="cpu")
