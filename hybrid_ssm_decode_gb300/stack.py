@@ -187,6 +187,13 @@ class HybridStack:
             raise ValueError(f"pattern: {s.pattern!r}, must be of M and A")
         if kv not in ("bf16", "fp8", "nvfp4"):
             raise ValueError(f"kv: {kv!r}, must be bf16, fp8 or nvfp4")
+        if rope is not None and "A" in s.pattern:
+            # here, and not in a step's append, when the page table has grown already
+            if rope.rotary_dim > s.attn_dim:
+                raise ValueError(f"rope: {rope.rotary_dim} rotated channels, heads have {s.attn_dim}")
+            on = torch.empty(0, device=device).device
+            if rope.turns.device != on:
+                raise ValueError(f"rope: on {rope.turns.device}, must be on {on}")
         self.rope = rope
         gen = torch.Generator(device=device)
         gen.manual_seed(2000 + seed)

@@ -59,3 +59,13 @@ def test_a_rope_stays_as_it_is_made(lib, monkeypatch):
         rope.frequencies[0] = 0.0
     assert (rope.gain, rope.interleaved, rope.rotary_dim, list(rope.frequencies)) == (1.5, False, 64, freq)
     assert rope.signature[:3] == (64, False, 1.5)
+
+
+@pytest.mark.parametrize("rot,device,what", [(128, "cpu", "rope: 128 rotated channels"), (64, "meta", "rope: on cpu")])
+def test_a_stack_refuses_a_rope_that_its_layers_would(lib, monkeypatch, rot, device, what):
+    """Before its first step: there the page table and the layers in front have already moved on."""
+    from hybrid_ssm_decode_gb300.stack import HybridShape, HybridStack
+    monkeypatch.setattr(rssm.hybrid, "_cuda", lambda device, name: None)
+    rope = rssm.Rope(rot, device="cpu")
+    with pytest.raises(ValueError, match=what):
+        HybridStack(HybridShape("MA", 1, q_heads=2, kv_heads=1, attn_dim=64), device=device, rope=rope)
