@@ -855,11 +855,12 @@ struct Warp {
         }
     }
 
-    // The outputs times f[row] to rows g and g + 8 of a buffer (`to`: row 0), or
-    // added to what is there.
+    // The outputs times f[row] to rows g and g + 8 of a buffer (`to`: row first_row()), or
+    // added to what is there. (From row 0 on, with g added here, FP8 heads of 256 got other
+    // registers: 64 rows of 64 requests of 2048 to 4096 tokens 330 -> 364 us.)
+    __device__ __forceinline__ int first_row() const { return g; }
     template <bool kAdd>
     __device__ __forceinline__ void leave(float* to, const float (&f)[2]) const {
-        to += g * S::OS;
 #pragma unroll
         for (int i = 0; i < kTiles; i += 2)
 #pragma unroll
@@ -1264,14 +1265,6 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
             s -= NS;
             ++tn;
         }
-        // group i, of which not all tokens may be seen
-        const auto masked = [&](int i, uint32_t kb) {
-            const int tok = (g0 + i) * kAttnGroup;
-            int lo[kLaneRows], hi[kLaneRows];
-#pragma unroll
-            for (int x = 0; x < kLaneRows; ++x) lo[x] = see_lo[x] - tok, hi[x] = see_hi[x] - tok;
-            wp.step_masked(kb, kb + S::kHalf, lo, hi, some_lo - tok, len - 1 - tok, all_lo - tok, all_hi - tok, a.T, tok, len, a.window, draft);
-        };
         while (k < ns) {
             const uint32_t kb = smem_u32(slots + s * S::kSlot), vb = kb + S::kHalf;
             uint64_t* const done = empty + s;
@@ -1284,7 +1277,14 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
                     wp.step(ks, vs);
                 } else if (ok) {
 #pragma unroll 1
-                    for (int j = 0; j < min(2, ng - i); ++j) masked(i + j, kb + j * 2 * S::kHalf);
+                    for (int j = 0; j < min(2, ng - i); ++j) {       // groups of which not all tokens may be seen
+                        const int tok = (g0 + i + j) * kAttnGroup;
+                        const uint32_t kj = kb + j * 2 * S::kHalf;
+                        int lo[kLaneRows], hi[kLaneRows];
+#pragma unroll
+                        for (int x = 0; x < kLaneRows; ++x) lo[x] = see_lo[x] - tok, hi[x] = see_hi[x] - tok;
+                        wp.step_masked(kj, kj + S::kHalf, lo, hi, some_lo - tok, len - 1 - tok, all_lo - tok, all_hi - tok, a.T, tok, len, a.window, draft);
+                    }
                 }
             } else if (k >= f0 && k < f1) {
                 if (NG == 2 && k + S::NT < min(f1, ng)) {
@@ -1300,7 +1300,12 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
                     if (ok) wp.step(ks, vs);
                 }
             } else if (ok) {
-                masked(k, kb);
+                // written out, not shared with the branch above: through a function of both, FP32
+                // heads of 128 spilled (32 rows of 16 requests of 1000 to 2000 tokens 96.5 -> 99.9
+                // us), and 64 rows of BF16 heads of 64 took 336 for 320 us
+                const int tok = (g0 + k) * kAttnGroup;
+                const int lo[2] = {see_lo[0] - tok, see_lo[1] - tok}, hi[2] = {see_hi[0] - tok, see_hi[1] - tok};
+                wp.step_masked(kb, vb, lo, hi, some_lo - tok, len - 1 - tok, all_lo - tok, all_hi - tok, a.T, tok, len, a.window, draft);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(done);
@@ -1340,7 +1345,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ C
 #pragma unroll 1
         for (int w = 0; w < S::NT; w += S::NB) {
             if (wt >= w && wt < w + S::NB) {
-                float* to = merged + ((wt - w) * S::kRows + wm * S::kWarpRows) * S::OS;
+                float* to = merged + ((wt - w) * S::kRows + wm * S::kWarpRows + wp.first_row()) * S::OS;
                 if (w == 0) wp.template leave<false>(to, f);
                 else wp.template leave<true>(to, f);
             }

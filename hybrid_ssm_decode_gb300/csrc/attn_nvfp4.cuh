@@ -539,6 +539,7 @@ struct Warp<kNVFP4, S> {
     }
 
     // The outputs times f[row] to the warp's rows of a buffer, or added to what is there.
+    __device__ __forceinline__ int first_row() const { return 0; }
     template <bool kAdd>
     __device__ __forceinline__ void leave(float* to, const float (&f)[kLaneRows]) const {
 #pragma unroll
