@@ -338,7 +338,8 @@ __device__ __forceinline__ uint8_t quantise16(const float (&x)[16], float s, uin
     for (int i = 1; i < 16; ++i) m = max_nan(m, fabsf(x[i]));
     const uint32_t b = e4m3x2(__fmul_rn(m, __frcp_rn(__fmul_rn(6.f, s))), 0.f) & 0xFF;      // NaN: 0x7F
     codes[0] = codes[1] = 0;
-    if (b == 0 || b == 0x7F) return static_cast<uint8_t>(b);
+    // (1 / (6 s) is infinite for the smallest s, and 0 times it NaN: zeros stay zeros)
+    if (b == 0 || b == 0x7F) return static_cast<uint8_t>(m == 0.f ? 0 : b);
     const float inv = fminf(__frcp_rn(__fmul_rn(e4m3_to_f(b), s)), 3.402823466e38f);
 #pragma unroll
     for (int i = 0; i < 16; i += 2)

@@ -665,8 +665,9 @@ rssm_status rssm_attn_create(const rssm_attn_config* cfg, void* d_k_cache, void*
  * RSSM_KV_FP8 stores E4M3(x / scale), to nearest even, at most +-448. RSSM_KV_NVFP4
  * stores, with m the largest magnitude of a token's 16 channels of a block, the block
  * scale b = E4M3(m * (1 / (6 scale))), at most 448, and the codes E2M1(x * (1 / (b scale))),
- * at most +-6, to nearest even, in FP32 (b = 0: zeros). A NaN makes b NaN, and so the 16
- * values; an infinity is held as the largest value.
+ * at most +-6, to nearest even, in FP32 (m = 0 or b = 0: zeros). A NaN makes b NaN, and so
+ * the 16 values; an infinity is held as the largest value. (Both reciprocals are FP32 numbers for
+ * scales from 2^-120 to 2^100; beyond, what is not zero may be held far from its value.)
  * A slot may be given once in a call: what one given twice holds is not said.
  * Errors: INVALID_ARG (null, tokens < 0, a stride below the row), UNSUPPORTED (NVFP4
  * rows of more than 2^24 elements), CUDA. */
