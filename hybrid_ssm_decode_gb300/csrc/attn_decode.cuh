@@ -403,10 +403,14 @@ struct Warp {
     static constexpr int D = S::D;
     static constexpr int kQRegs = KV == kF32 ? 1 : D / 16;
     static constexpr int kTiles = D / 8;
-    static constexpr float kUp = KV == kFP8 ? 15.f : 0.f;   // weights, and l and o with them, are 2^kUp times as large
+    static constexpr float kUp = KV == kFP8 ? 15.f : 0.f;   // the largest score's weight is 2^kUp
+    static constexpr float kOver = 0.f;                     // l and o are 2^kOver times what top() says
     static constexpr int kLaneRows = 2;
     float o[kTiles][4];
-    float m[2], l[2];            // rows lane/4 and lane/4 + 8; l is this lane's columns only
+    // Rows lane/4 and lane/4 + 8; l is this lane's columns only. m: the largest score less kUp,
+    // rounded up, so that where scores are so large that kUp is not whole steps of theirs, no
+    // weight passes 2^kUp and all that are made, rescaled and joined are relative to one number.
+    float m[2], l[2];
     uint32_t qf[kQRegs][4];
     const float* qs;             // FP32: the query rows in shared memory
     float mul[2];                // score multiplier of the two rows
@@ -420,7 +424,7 @@ struct Warp {
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
     }
     __device__ __forceinline__ bool speaks() const { return c == 0; }
-    // The maximum under which row x's sums stand.
+    // The exponent under which row x's sums stand.
     __device__ __forceinline__ float top(int x) const { return m[x]; }
 
     __device__ __forceinline__ void reset() {
@@ -705,7 +709,7 @@ struct Warp {
     // weights; the outputs so far are rescaled where the maximum grew.
     template <int N>
     __device__ __forceinline__ void softmax(float (&s)[N][4]) {
-        float mx[2] = {m[0], m[1]};
+        float mx[2] = {kUp == 0.f ? m[0] : -INFINITY, kUp == 0.f ? m[1] : -INFINITY};
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -714,6 +718,7 @@ struct Warp {
         for (int x = 0; x < 2; ++x) {
             mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
             mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+            if constexpr (kUp != 0.f) mx[x] = fmaxf(m[x], __fsub_ru(mx[x], kUp));
         }
         if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
             float f[2];
@@ -731,7 +736,7 @@ struct Warp {
                 o[i][3] *= f[1];
             }
         }
-        const float ref[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - kUp, (m[1] == -INFINITY ? 0.f : m[1]) - kUp};
+        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -901,7 +906,7 @@ __device__ __forceinline__ void put(const AttnArgs& a, const Part<KV>& part, int
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * S::D + col) =
             make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     }
-    if (a.lse != nullptr && col == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + (log2f(L) - Warp<KV, S>::kUp)) * 0.69314718055994531f;
+    if (a.lse != nullptr && col == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + (log2f(L) - Warp<KV, S>::kOver)) * 0.69314718055994531f;
 }
 
 // Join the parts of a request and head: the consumer warps, once all have

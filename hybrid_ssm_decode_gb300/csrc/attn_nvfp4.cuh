@@ -152,7 +152,7 @@ struct Warp<kNVFP4, S> {
     // below 2^16. Rescaling at every new maximum took a rescale in two of three steps
     // where 16 rows run over some thousands of tokens. Weights below 2^-26 of that
     // score lose some of FP16's bits, and those below 2^-37 vanish.
-    static constexpr float kUp = 12.f, kSlack = 3.f;
+    static constexpr float kUp = 12.f, kSlack = 3.f, kOver = kUp;
     float o[NR][kTiles][4];      // of a tile's two channels of this lane: the rows' pair in [0..1] and in [2..3]
     float base[kLaneRows];       // the score, before its multiplier, that weights are relative to; the same in all lanes of a row
     float most[kLaneRows];       // scores up to here need no other; -inf before the first
