@@ -34,7 +34,7 @@ struct AttnArgs {
 // Query rows (drafts x heads of a cache head) that one block takes, for `rows` in
 // all: 16, 32 or 64, and 8 over NVFP4 caches, whose kernel takes rows by eights. Heads of
 // 256 stop at 32 over FP32 caches (the ring's slots are 32 KB there) and over NVFP4 ones
-// (64 requests of 4096 tokens, 64 rows: 230 us in one block, 202 in two of 32).
+// (64 requests of 4096 tokens, 64 rows: 231 us in one block, 183 in two of 32).
 inline int attn_block_rows(int rows, int kv_dtype, int D) {
     if (kv_dtype == RSSM_KV_NVFP4 && rows <= 8) return 8;
     const bool most32 = D == 256 && (kv_dtype == RSSM_F32 || kv_dtype == RSSM_KV_NVFP4);

@@ -43,7 +43,7 @@
 // Matrix instructions. m16n8k16 on BF16 caches, with 2^(s-m) split into two
 // BF16 terms, so that the outputs carry only their own rounding; on FP8 caches the codes
 // widen exactly to FP16 (Q scaled per row by a power of two into FP16's range;
-// 2^(s-m+15) rounded to FP16's 11 bits, so that only weights below 2^-29 of the largest
+// 2^(s-(m-15)), m-15 rounded up, in FP16's 11 bits, so that only weights below 2^-29 of the largest
 // lose some of them and only those below 2^-40 vanish: a long tail under one large
 // score counts; NVFP4 caches: attn_nvfp4.cuh), and on FP32 caches m16n8k8 on TF32 with both
 // operands split in two (three products; what is left out is below 2^-21).

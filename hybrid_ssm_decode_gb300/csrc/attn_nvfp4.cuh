@@ -22,8 +22,9 @@
 // What bounds it. A group of 16 tokens of 128 channels takes 98 cycles of an SM at the
 // bandwidth of a copy; its 512 words of codes take 51 at the rate measured for a conversion
 // and a multiplication a pair (10 words of 8 codes a cycle), and in all a warp issues 260
-// instructions for it, 65 cycles if the SM never waited. So the issue slots bind (55 %
-// used) before the memory does (80 %), and what a widened fragment costs beside its
+// instructions for it, 65 cycles if the SM never waited. Neither bound is reached (80 % of
+// the bandwidth, 55 % of the issue slots): three warps a scheduler do not cover each
+// other's waits for fixed latencies and for shared memory. So what a widened fragment costs beside its
 // conversion is kept low: the interleaving of two tokens' V codes is two instructions for
 // 16 codes, a lane's channels of V all belong to one block, so that a pair of scales
 // serves 16 fragments, and the running maximum is looked at by a vote. Small blocks of two
@@ -31,8 +32,11 @@
 // registers lose their interleaving, and fewer producers refill too late.
 //
 // Measured: 8 requests of 128k, 1.07 GB: 199 us, 5.4 TB/s; 256 ragged requests, 1.33 GB:
-// 265 us, 5.0 TB/s; 4 drafts of 8 heads of 256, 64 requests: 139 us; windows of 1000 over
-// 16 heads of 64, 128 requests: 66 us; one request of 777 tokens: 11 us.
+// 265 us, 5.0 TB/s; 4 drafts of 8 heads of 256, 64 requests: 141 us; windows of 1000 over
+// 16 heads of 64, 128 requests: 67 us; one request of 777 tokens: 11 us. 64 requests of 4096
+// tokens over 4 heads of 128: 42 us for 8 rows, 68 for 16, whose 64 outputs and 32 queries
+// a thread do not fit 168 registers (340 bytes of spills; 32 and 64 rows, and heads of
+// 256 at 32: 92 to 116), 97 for 32.
 #pragma once
 
 #include "attn_decode.cuh"
@@ -378,7 +382,7 @@ struct Warp<kNVFP4, S> {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int x = 2 * n + (j & 1);
-                    // the difference first: it is exact near the largest score, however large that is
+                    // the difference first: it is exact near the reference, however large that is
                     s[i][n][j] = ex2(fmaf(s[i][n][j] - base[x], mul[x], kUp));
                     l[x] += s[i][n][j];
                 }

@@ -18,8 +18,9 @@
 // Bound by HBM for many tokens: 16384 tokens of 40 heads of 128 rotated in 53 us
 // (6.4 TB/s), FP32 with a quarter of 256 channels 30 us (6.1 TB/s), 32,750 tokens of 8
 // heads to a 4-bit cache in 33 us and back in 33 (5.2 TB/s; instructions, 65 % of the
-// issue slots), 12,003 tokens with 32 query heads to an FP8 cache 58 us (4.7 TB/s: 121
-// registers leave two blocks an SM). By latency for few: one token's rotation 2.1 us
+// issue slots), 12,003 tokens with 32 query heads to an FP8 cache 58 us (4.7 TB/s: as it
+// is arranged, 121 registers leave two blocks an SM; BF16 and 4-bit caches, 114 and 112,
+// take as long, and FP32 ones, twice the bytes, 100). By latency for few: one token's rotation 2.1 us
 // and a step of 256 tokens into the cache 4.1 us from a CUDA graph.
 #include <cmath>
 #include <initializer_list>
@@ -525,6 +526,8 @@ __device__ __forceinline__ void write_heads(const PlaceArgs& a, const T* row, co
 
 // grid.y: 1, and a block takes its tile's queries, keys and values; or one block for the
 // keys, one for the values and the others for the queries (none where there are none).
+// Without rotation five blocks an SM leave 48 registers: 24 bytes of spills a thread, up to
+// 118 where rows do not begin on 16 bytes.
 template <class T, int KV, int VEC, int PAIRS>
 __global__ void __launch_bounds__(kThreads, PAIRS == kNone ? 5 : 1) place_kernel(const PlaceArgs a, int nt_log2) {
     extern __shared__ float2 cs[];

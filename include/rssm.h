@@ -737,8 +737,8 @@ rssm_status rssm_attn_destroy(rssm_attn* h);
  *   YARN        r w_i / factor + (1 - r) w_i with the ramp r = clamp((i - lo)/(hi - lo), 0, 1)
  *               between the channels that turn `fast` (32) and `slow` (1) times over
  *               the original positions, c(n) = rotary_dim ln(original/(2 pi n)) / (2 ln base),
- *               lo = max(floor(c(fast)), 0), hi = min(ceil(c(slow)), rotary_dim - 1);
- *               gain = 0.1 ln(factor) + 1
+ *               lo = max(floor(c(fast)), 0), hi = min(ceil(c(slow)), rotary_dim - 1)
+ *               (hi - lo at least 0.001); gain = 0.1 ln(factor) + 1
  *   WAVELENGTH  s w_i + (1 - s) w_i / factor with s = clamp((n - slow)/(fast - slow), 0, 1),
  *               n = original w_i / (2 pi) the channel's turns, fast 4 and slow 1
  * The angle is exact for every 32-bit position (negative ones turn back): frequencies
